@@ -178,7 +178,7 @@ def prepare(case, seed):
     s["idx"] = torch.rand((T, E), device=DEV, generator=gen).argsort(1)[:, :k].to(torch.int32).contiguous()
     s["weights"] = torch.randn((T, k), device=DEV, generator=gen).softmax(1)
     s["out"] = torch.empty((T, H), dtype=torch.bfloat16, device=DEV)
-    s["workspace"] = torch.empty((T * k, inter), dtype=torch.bfloat16, device=DEV)
+    s["workspace"] = torch.empty((T * k, inter), device=DEV)
     return s
 
 
