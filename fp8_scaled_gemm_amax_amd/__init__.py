@@ -24,7 +24,9 @@ __all__ = [
     "grouped_layout_width", "GROUP_K_ALIGN", "MX_BLOCK", "fp8_mx_quantize_row", "fp8_gemm_mx",
     "fp8_grouped_gemm_mx", "mx_scale_records", "fp8_moe_route", "fp8_moe_permute_quantize_row",
     "fp8_swiglu_quantize_row", "fp8_moe_unpermute_combine", "fp8_blockwise_quantize_act",
-    "fp8_blockwise_quantize_weight", "EXPORTED_SYMBOLS",
+    "fp8_blockwise_quantize_weight", "NORM_LAYER", "NORM_RMS", "MOE_FEW_TOKENS", "fp8_norm_quantize_row",
+    "norm_workspace", "fp8_norm_backward", "fp8_mx_norm_backward", "fp8_swiglu_quantize_row_mx",
+    "fp8_swiglu_backward", "fp8_mx_swiglu_backward", "moe_few_workspace", "fp8_moe_few_tokens", "EXPORTED_SYMBOLS",
 ]
 
 E4M3, E5M2, E4M3_FNUZ, E5M2_FNUZ = 0, 1, 2, 3
@@ -32,6 +34,7 @@ AXIS_TENSOR, AXIS_ROW, AXIS_COL = 0, 1, 2
 AMAX_MOST_RECENT, AMAX_MAX = 0, 1
 SCALE_TENSOR, SCALE_VECTOR = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
+NORM_LAYER, NORM_RMS = 0, 1
 
 EXPORTED_SYMBOLS = (
     "fp8_query_device", "fp8_status_string", "fp8_last_error", "fp8_amax", "fp8_quantize_tensor",
@@ -40,12 +43,15 @@ EXPORTED_SYMBOLS = (
     "fp8_grouped_gemm_scaled", "fp8_grouped_quantize_col", "fp8_grouped_gemm_ragged_k",
     "fp8_mx_quantize_row", "fp8_gemm_mx", "fp8_grouped_gemm_mx", "fp8_moe_route", "fp8_moe_permute_quantize_row",
     "fp8_swiglu_quantize_row", "fp8_moe_unpermute_combine", "fp8_blockwise_quantize_act",
-    "fp8_blockwise_quantize_weight",
+    "fp8_blockwise_quantize_weight", "fp8_norm_quantize_row", "fp8_norm_backward_workspace", "fp8_norm_backward",
+    "fp8_mx_norm_backward", "fp8_swiglu_quantize_row_mx", "fp8_swiglu_backward", "fp8_mx_swiglu_backward",
+    "fp8_moe_few_tokens",
 )
 
 GROUP_K_ALIGN = 256     # FP8_GROUP_K_ALIGN of the C header
 MAX_ROW_BATCH = 8       # FP8_MAX_ROW_BATCH of the C header
 MX_BLOCK = 32           # FP8_MX_BLOCK of the C header
+MOE_FEW_TOKENS = 64     # FP8_MOE_FEW_TOKENS of the C header
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8amax.so")
 
@@ -67,7 +73,7 @@ def _load():
         raise ImportError(f"{LIB_PATH} is not built: run __graft_entry__.build() (or make -C "
                           f"{os.path.dirname(LIB_PATH)}) first")
     L = ctypes.CDLL(LIB_PATH)
-    P, I64, I32, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
+    P, I64, I32, I, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_float
     sigs = {
         "fp8_query_device": [I, ctypes.POINTER(_DeviceInfo)],
         "fp8_amax": [P, I64, I64, I64, I, P, P],
@@ -91,11 +97,22 @@ def _load():
         "fp8_moe_permute_quantize_row": [P, I64, I64, I64, P, I32, I64, I, I32, P, I64, P, P],
         "fp8_swiglu_quantize_row": [P, I64, I64, I64, I, I32, P, I64, P, P],
         "fp8_moe_unpermute_combine": [P, I64, I64, I64, P, P, I64, I32, P, I64, P],
+        "fp8_norm_quantize_row": [P, I64, I64, I64, P, P, I, F, I, I, I32, P, I64, P, P, I64, P, P, P, I, I64, P, I64,
+                                  P],
+        "fp8_norm_backward": [P, I64, I64, I64, P, I64, P, I, P, P, I, P, I64, P, P, P, I64, P],
+        "fp8_mx_norm_backward": [P, I64, I64, I64, P, I, I64, P, I64, P, P, I, P, I, P, I64, P, P, P, I64, P, I64, P],
+        "fp8_swiglu_quantize_row_mx": [P, I64, I64, I64, I, I32, P, I64, P, P, I, I64, P, I64, P],
+        "fp8_swiglu_backward": [P, I64, I64, I64, P, I64, P, I64, P, I64, P],
+        "fp8_mx_swiglu_backward": [P, I64, I64, I64, P, I, I64, P, I64, P, I64, P, I64, P],
+        "fp8_moe_few_tokens": [P, I64, I64, I64, P, P, I32, I32, P, I, I64, I64, P, P, I, I64, I64, P, I64, P, I64, P,
+                               I64, P],
     }
     for name, args in sigs.items():
         fn = getattr(L, name)
         fn.argtypes = args
         fn.restype = I
+    L.fp8_norm_backward_workspace.argtypes = [I64, I64]
+    L.fp8_norm_backward_workspace.restype = I64
     L.fp8_status_string.argtypes = [I]
     L.fp8_status_string.restype = ctypes.c_char_p
     L.fp8_last_error.argtypes = []
@@ -465,3 +482,247 @@ def fp8_blockwise_quantize_act(x, fmt, q, scale_records):
 def fp8_blockwise_quantize_weight(w, fmt, q, scale_records):
     """128 x 128 tiles: as fp8_blockwise_quantize_act, one scale per tile."""
     _blockwise(lib.fp8_blockwise_quantize_weight, w, fmt, q, scale_records)
+
+
+def _on(dev, **tensors):
+    """Every tensor that is not None is on the device dev, a GPU (a kernel given
+    another device's or the host's address would fault)."""
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be on a GPU, got {dev}")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+class _device:
+    """Makes dev the current device for a call (a launch goes to the current
+    device); free where it is the current one already."""
+
+    def __init__(self, dev):
+        self.dev, self.prev = dev, None
+
+    def __enter__(self):
+        current = torch.cuda.current_device()
+        if self.dev.index is not None and self.dev.index != current:
+            self.prev = current
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+
+
+def _vec(t, name, n, dtype=torch.float32):
+    if t is not None and (t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor [{n}], got {tuple(t.shape)} {t.dtype}")
+
+
+def _rows(t, name, elem_size=None):
+    """(rows, cols, ld) of a bf16 tensor (or one of codes, elem_size bytes each)
+    whose rows do not overlap: a row stride below cols, such as an expanded
+    tensor's 0, has no leading dimension."""
+    rows, cols, ld = _mat(t, name, elem_size) if elem_size is not None else _bf16(t, name)
+    if rows <= 1:
+        return rows, cols, max(cols, 1)
+    if cols > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name}'s rows overlap (row stride {t.stride(0)}, {cols} columns): make it contiguous")
+    return rows, cols, ld
+
+
+def _like(t, name, rows, cols, elem_size=None):
+    """Leading dimension of the [rows x cols] tensor t (bf16, or codes of elem_size bytes)."""
+    r, c, ld = _rows(t, name, elem_size)
+    if (r, c) != (rows, cols):
+        raise ValueError(f"{name} must be [{rows} x {cols}], got {tuple(t.shape)}")
+    return ld
+
+
+def _norm_weights(gamma, beta, cols):
+    """The weight type of gamma and beta (either may be None)."""
+    w = gamma if gamma is not None else beta
+    if w is None:
+        return OUT_BF16
+    if w.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"gamma and beta are bfloat16 or float32, got {w.dtype}")
+    _vec(gamma, "gamma", cols, w.dtype)
+    _vec(beta, "beta", cols, w.dtype)
+    return OUT_F32 if w.dtype == torch.float32 else OUT_BF16
+
+
+def _checkpoint(q, name, scale, rows, cols):
+    """(ld of the codes, ld of the records) of an MX checkpoint of a [rows x cols] matrix."""
+    if scale is None:
+        raise ValueError(f"{name} needs its scale records")
+    ldq = _like(q, name, rows, cols, 1)
+    J, r, lds = _records(scale, f"{name}'s scale records")
+    if r != rows or J != (cols + 127) // 128:
+        raise ValueError(f"{name}'s scale records must be [{(cols + 127) // 128} x {rows} x 4], "
+                         f"got {tuple(scale.shape)}")
+    return ldq, lds
+
+
+def fp8_norm_quantize_row(x, gamma, beta, eps, kind, fmt, margin, q, scale_inv_out, y=None, mean_out=None,
+                          rstd_out=None, xhat_q=None, xhat_fmt=E4M3, xhat_scale=None):
+    """Layer norm (NORM_LAYER) or its RMS form (NORM_RMS) of x bf16 [rows x cols],
+    fused with the rowwise cast: q codes [rows x cols] and scale_inv_out fp32
+    [rows] (both None to skip), y bf16 (or None). gamma, beta [cols]: bf16 or
+    fp32, None for 1 and 0. mean_out, rstd_out fp32 [rows] (or None); xhat_q
+    codes and xhat_scale records (mx_scale_records) save the normalised rows in
+    8 bits for fp8_mx_norm_backward (cols % 32 == 0)."""
+    rows, cols, ldx = _rows(x, "x")
+    w_type = _norm_weights(gamma, beta, cols)
+    ldq = _like(q, "q", rows, cols, 1) if q is not None else cols
+    ldy = _like(y, "y", rows, cols) if y is not None else cols
+    for name, t in (("scale_inv_out", scale_inv_out), ("mean_out", mean_out), ("rstd_out", rstd_out)):
+        _vec(t, name, rows)
+    ldxq = lds = 0
+    if xhat_q is not None or xhat_scale is not None:
+        if xhat_q is None:
+            raise ValueError("xhat_scale needs xhat_q")
+        ldxq, lds = _checkpoint(xhat_q, "xhat_q", xhat_scale, rows, cols)
+    dev = x.device
+    _on(dev, gamma=gamma, beta=beta, q=q, scale_inv_out=scale_inv_out, y=y, mean_out=mean_out, rstd_out=rstd_out,
+        xhat_q=xhat_q, xhat_scale=xhat_scale)
+    with _device(dev):
+        _check(lib.fp8_norm_quantize_row(_ptr(x), rows, cols, ldx, _ptr(gamma), _ptr(beta), w_type, eps, kind, fmt,
+                                         margin, _ptr(q), ldq, _ptr(scale_inv_out), _ptr(y), ldy, _ptr(mean_out),
+                                         _ptr(rstd_out), _ptr(xhat_q), xhat_fmt, ldxq, _ptr(xhat_scale), lds,
+                                         _stream(x)))
+
+
+def norm_workspace(rows, cols, device="cuda:0"):
+    """A workspace that fp8_norm_backward and fp8_mx_norm_backward of a [rows x cols] tensor accept."""
+    return torch.empty(lib.fp8_norm_backward_workspace(rows, cols) // 4, dtype=torch.float32, device=device)
+
+
+def _workspace(t):
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return _ptr(t), t.numel() * t.element_size()
+
+
+def fp8_norm_backward(dy, x, gamma, mean, rstd, kind, dx, dgamma=None, dbeta=None, workspace=None):
+    """Gradients of fp8_norm_quantize_row's y: dx bf16 [rows x cols] and, if given,
+    dgamma, dbeta fp32 [cols] (overwritten), from dy and x bf16 [rows x cols] and
+    the forward pass's mean and rstd (mean None for NORM_RMS). workspace
+    (norm_workspace) is needed with dgamma or dbeta."""
+    rows, cols, lddy = _rows(dy, "dy")
+    ldx, lddx = _like(x, "x", rows, cols), _like(dx, "dx", rows, cols)
+    w_type = _norm_weights(gamma, None, cols)
+    _vec(mean, "mean", rows)
+    _vec(rstd, "rstd", rows)
+    _vec(dgamma, "dgamma", cols)
+    _vec(dbeta, "dbeta", cols)
+    ws, ws_bytes = _workspace(workspace)
+    dev = dy.device
+    _on(dev, x=x, gamma=gamma, mean=mean, rstd=rstd, dx=dx, dgamma=dgamma, dbeta=dbeta, workspace=workspace)
+    with _device(dev):
+        _check(lib.fp8_norm_backward(_ptr(dy), rows, cols, lddy, _ptr(x), ldx, _ptr(gamma), w_type, _ptr(mean),
+                                     _ptr(rstd), kind, _ptr(dx), lddx, _ptr(dgamma), _ptr(dbeta), ws, ws_bytes,
+                                     _stream(dy)))
+
+
+def fp8_mx_norm_backward(dy, xhat_q, xhat_fmt, xhat_scale, gamma, beta, rstd, kind, dx, dgamma=None, dbeta=None,
+                         y=None, workspace=None):
+    """fp8_norm_backward from the 8-bit checkpoint of the normalised rows. y (bf16,
+    or None) receives xhat * gamma + beta; beta is used for y alone."""
+    rows, cols, lddy = _rows(dy, "dy")
+    lddx = _like(dx, "dx", rows, cols)
+    ldy = _like(y, "y", rows, cols) if y is not None else cols
+    ldxq, lds = _checkpoint(xhat_q, "xhat_q", xhat_scale, rows, cols)
+    w_type = _norm_weights(gamma, beta, cols)
+    _vec(rstd, "rstd", rows)
+    _vec(dgamma, "dgamma", cols)
+    _vec(dbeta, "dbeta", cols)
+    ws, ws_bytes = _workspace(workspace)
+    dev = dy.device
+    _on(dev, xhat_q=xhat_q, xhat_scale=xhat_scale, gamma=gamma, beta=beta, rstd=rstd, dx=dx, dgamma=dgamma,
+        dbeta=dbeta, y=y, workspace=workspace)
+    with _device(dev):
+        _check(lib.fp8_mx_norm_backward(_ptr(dy), rows, cols, lddy, _ptr(xhat_q), xhat_fmt, ldxq, _ptr(xhat_scale),
+                                        lds, _ptr(gamma), _ptr(beta), w_type, _ptr(rstd), kind, _ptr(dx), lddx,
+                                        _ptr(dgamma), _ptr(dbeta), _ptr(y), ldy, ws, ws_bytes, _stream(dy)))
+
+
+def fp8_swiglu_quantize_row_mx(h, fmt, margin, q, scale_inv_out, hq, h_fmt, h_scale):
+    """fp8_swiglu_quantize_row that also saves h bf16 [rows x 2I] in 8 bits: hq codes
+    [rows x 2I] and h_scale records (mx_scale_records); I % 32 == 0."""
+    rows, two_i, ldh = _rows(h, "h")
+    if two_i % 2:
+        raise ValueError("h must have an even number of columns (gate | up)")
+    ldq = _like(q, "q", rows, two_i // 2, 1)
+    _vec(scale_inv_out, "scale_inv_out", rows)
+    ldhq, lds = _checkpoint(hq, "hq", h_scale, rows, two_i)
+    dev = h.device
+    _on(dev, q=q, scale_inv_out=scale_inv_out, hq=hq, h_scale=h_scale)
+    with _device(dev):
+        _check(lib.fp8_swiglu_quantize_row_mx(_ptr(h), rows, two_i // 2, ldh, fmt, margin, _ptr(q), ldq,
+                                              _ptr(scale_inv_out), _ptr(hq), h_fmt, ldhq, _ptr(h_scale), lds,
+                                              _stream(h)))
+
+
+def fp8_swiglu_backward(da, h, dh, a=None):
+    """SwiGLU's backward pass: da bf16 [rows x I], h and dh bf16 [rows x 2I] (gate |
+    up); a (bf16 [rows x I], or None) receives silu(gate) * up."""
+    rows, inter, ldda = _rows(da, "da")
+    ldh, lddh = _like(h, "h", rows, 2 * inter), _like(dh, "dh", rows, 2 * inter)
+    lda = _like(a, "a", rows, inter) if a is not None else inter
+    dev = da.device
+    _on(dev, h=h, dh=dh, a=a)
+    with _device(dev):
+        _check(lib.fp8_swiglu_backward(_ptr(da), rows, inter, ldda, _ptr(h), ldh, _ptr(dh), lddh, _ptr(a), lda,
+                                       _stream(da)))
+
+
+def fp8_mx_swiglu_backward(da, hq, h_fmt, h_scale, dh, a=None):
+    """fp8_swiglu_backward from the 8-bit checkpoint of h (codes hq [rows x 2I] and
+    scale records, as fp8_swiglu_quantize_row_mx or fp8_mx_quantize_row gives them)."""
+    rows, inter, ldda = _rows(da, "da")
+    lddh = _like(dh, "dh", rows, 2 * inter)
+    lda = _like(a, "a", rows, inter) if a is not None else inter
+    ldhq, lds = _checkpoint(hq, "hq", h_scale, rows, 2 * inter)
+    dev = da.device
+    _on(dev, hq=hq, h_scale=h_scale, dh=dh, a=a)
+    with _device(dev):
+        _check(lib.fp8_mx_swiglu_backward(_ptr(da), rows, inter, ldda, _ptr(hq), h_fmt, ldhq, _ptr(h_scale), lds,
+                                          _ptr(dh), lddh, _ptr(a), lda, _stream(da)))
+
+
+def moe_few_workspace(tokens, topk, inter, device="cuda:0"):
+    """A workspace that fp8_moe_few_tokens accepts for these sizes or smaller ones."""
+    return torch.empty((tokens * topk, inter), dtype=torch.float32, device=device)
+
+
+def fp8_moe_few_tokens(x, expert_idx, weights, w1, f1, w1_scale_inv, w2, f2, w2_scale_inv, out, workspace):
+    """The MoE layer for at most MOE_FEW_TOKENS tokens: x, out bf16 [T x H];
+    expert_idx int32, weights fp32 [T x k]; w1 codes [E x 2I x H] (gate rows, then
+    up rows) with w1_scale_inv fp32 [E x 2I]; w2 codes [E x H x I] with
+    w2_scale_inv fp32 [E x H]; workspace: moe_few_workspace(T, k, I)."""
+    T, H, ldx = _rows(x, "x")
+    k = _i32_2d(expert_idx, "expert_idx")[1]
+    if expert_idx.shape[0] != T:
+        raise ValueError(f"expert_idx has {expert_idx.shape[0]} rows, x has {T}")
+    if tuple(weights.shape) != (T, k) or weights.dtype != torch.float32 or not weights.is_contiguous():
+        raise ValueError(f"weights must be a contiguous float32 [{T} x {k}] tensor")
+    for name, t in (("w1", w1), ("w2", w2)):
+        if t.dim() != 3 or t.element_size() != 1 or t.stride(2) != 1 or t.stride(1) < t.shape[2]:
+            raise ValueError(f"{name} must be a 3-D 1-byte tensor with unit last stride and rows that do not overlap")
+    E, two_i, h1 = w1.shape
+    inter = two_i // 2
+    if h1 != H or two_i % 2 or tuple(w2.shape) != (E, H, inter):
+        raise ValueError(f"w1 {tuple(w1.shape)} and w2 {tuple(w2.shape)} do not match x's {H} columns")
+    for name, t, n in (("w1_scale_inv", w1_scale_inv, two_i), ("w2_scale_inv", w2_scale_inv, H)):
+        if tuple(t.shape) != (E, n) or t.dtype != torch.float32 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 [{E} x {n}] tensor")
+    ldo = _like(out, "out", T, H)
+    ws, ws_bytes = _workspace(workspace)
+    dev = x.device
+    _on(dev, expert_idx=expert_idx, weights=weights, w1=w1, w1_scale_inv=w1_scale_inv, w2=w2,
+        w2_scale_inv=w2_scale_inv, out=out, workspace=workspace)
+    with _device(dev):
+        _check(lib.fp8_moe_few_tokens(_ptr(x), T, H, ldx, _ptr(expert_idx), _ptr(weights), k, E, _ptr(w1), f1,
+                                      w1.stride(1), w1.stride(0) if E > 1 else 0, _ptr(w1_scale_inv), _ptr(w2), f2,
+                                      w2.stride(1), w2.stride(0) if E > 1 else 0, _ptr(w2_scale_inv), inter, _ptr(out),
+                                      ldo, ws, ws_bytes, _stream(x)))

@@ -1,0 +1,613 @@
+// norm.hip - layer norm and its RMS form before an FP8 product: the forward
+// pass fused with the rowwise cast (and with an 8-bit checkpoint of the
+// normalised rows), the backward pass with the reduction of the weights'
+// gradients, from x or from the checkpoint.
+//
+//   forward, row r of N columns: mu = sum x / N (RMS: 0), v = sum (x - mu)^2 / N,
+//     rstd = 1 / sqrt(v + eps), xh = (x - mu) rstd, y = xh gamma + beta
+//   backward: w = dy gamma, dx = rstd (w - mean(w) - xh mean(w xh))
+//     (RMS: without mean(w)), dgamma = sum_r dy xh, dbeta = sum_r dy
+//
+// Everything here is bound by HBM: the rows are held in registers from their
+// one read to their last use, and all statistics and sums are fp32.
+#include "kernels.hpp"
+#include "layer_device.hpp"
+
+namespace fp8amax {
+namespace {
+
+constexpr int kBlock = 256;   // 4 wavefronts
+constexpr int kWaves = kBlock / 64;
+
+// Eight of gamma's or beta's values (bf16 or fp32), chunk ch.
+__device__ __forceinline__ void load_weights8(const void* w, int w_f32, uint32_t ch, float* o) {
+    if (w_f32) {
+        const float4 a = *at<float4>(w, ch * 32), b = *at<float4>(w, ch * 32 + 16);
+        o[0] = a.x;
+        o[1] = a.y;
+        o[2] = a.z;
+        o[3] = a.w;
+        o[4] = b.x;
+        o[5] = b.y;
+        o[6] = b.z;
+        o[7] = b.w;
+    } else {
+        unpack8(*at<uint4>(w, ch * 16), o);
+    }
+}
+__device__ __forceinline__ float load_weight(const void* w, int w_f32, int64_t c) {
+    return w_f32 ? static_cast<const float*>(w)[c] : __uint_as_float((uint32_t) static_cast<const uint16_t*>(w)[c] << 16);
+}
+
+// ---------------------------------------------------------------- forward --
+// WPR wavefronts per row. The variance is the second pass over the registers
+// (sum of (x - mu)^2), so a row whose mean is large against its deviation
+// loses nothing. y is formed in fp32 and cast from there.
+template <int F, int MAXC, int WPR>
+__global__ __launch_bounds__(kBlock) void k_norm_quant_row(NormFwd p) {
+    __shared__ float red[2][kWaves];
+    __shared__ uint32_t redu[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int t = WPR == 1 ? lane : (int)threadIdx.x;
+    constexpr int TPR = WPR * 64;
+    const int64_t row = WPR == 1 ? xcd_block(blockIdx.x, gridDim.x) * kWaves + wave : xcd_block(blockIdx.x, gridDim.x);
+    if (row >= p.rows) return;                              // (uniform over the wavefronts of a row)
+    const int nch = (int)(p.cols >> 3);
+    const float inv_n = 1.0f / (float)p.cols;
+    const uint4* xr = reinterpret_cast<const uint4*>(p.x + row * p.ldx);
+    uint4 raw[MAXC];
+#pragma unroll
+    for (int c = 0; c < MAXC; ++c) {
+        const int ch = t + c * TPR;
+        raw[c] = load_stream(xr + (ch < nch ? ch : nch - 1));
+    }
+    float v[MAXC][8];
+    float s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < MAXC; ++c) {
+        unpack8(raw[c], v[c]);
+        const bool live = t + c * TPR < nch;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[c][i] = live ? v[c][i] : 0.0f;
+            s += v[c][i];
+        }
+    }
+    float mean = 0.0f;
+    if (!p.rms) {
+        s = wave_sum(s);
+        if (WPR > 1) {
+            if (lane == 0) red[0][wave] = s;
+            __syncthreads();
+            s = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
+        }
+        mean = s * inv_n;
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int c = 0; c < MAXC; ++c) {
+        const bool live = t + c * TPR < nch;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[c][i] = live ? v[c][i] - mean : 0.0f;
+            ss = fmaf(v[c][i], v[c][i], ss);
+        }
+    }
+    ss = wave_sum(ss);
+    if (WPR > 1) {
+        if (lane == 0) red[1][wave] = ss;
+        __syncthreads();
+        ss = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    }
+    const float rstd = 1.0f / __builtin_sqrtf(ss * inv_n + p.eps);
+    if (t == 0) {
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+    uint32_t mx = 0;
+#pragma unroll
+    for (int c = 0; c < MAXC; ++c) {
+        const int ch = t + c * TPR;
+        const bool live = ch < nch;
+        const uint32_t cc = (uint32_t)(live ? ch : nch - 1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] *= rstd;
+        if (p.xq) {
+            uint32_t record;
+            const uint2 code = p.ckpt_e5m2 ? mx_chunk<kE5M2>(v[c], live, &record) : mx_chunk<kE4M3>(v[c], live, &record);
+            if (live) {
+                reinterpret_cast<uint2*>(p.xq + row * p.ldxq)[ch] = code;
+                if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.xs + 4 * ((int64_t)(ch >> 4) * p.ldxs + row)) = record;
+            }
+        }
+        if (p.gamma) {
+            float g[8];
+            load_weights8(p.gamma, p.w_f32, cc, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] *= g[i];
+        }
+        if (p.beta) {
+            float b[8];
+            load_weights8(p.beta, p.w_f32, cc, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] += b[i];
+        }
+        if (live) {
+            if (p.y) reinterpret_cast<uint4*>(p.y + row * p.ldy)[ch] = pack8(v[c]);
+            const uint32_t m = absmax8(v[c]);
+            mx = m > mx ? m : mx;
+        }
+    }
+    if (!p.q) return;
+    mx = wave_max_u32(mx);
+    if (WPR > 1) {
+        if (lane == 0) redu[wave] = mx;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) mx = redu[w] > mx ? redu[w] : mx;
+    }
+    const float amax = __uint_as_float(mx);
+    const float sc = scale_from_amax<F>(amax, p.margin);
+    if (t == 0) p.scale_inv[row] = 1.0f / sc;
+    uint2* qr = reinterpret_cast<uint2*>(p.q + row * p.ldq);
+    const bool nan_free = !__builtin_isnan(amax);
+#pragma unroll
+    for (int c = 0; c < MAXC; ++c) {
+        const int ch = t + c * TPR;
+        const uint2 o = nan_free ? encode8f<F, true>(v[c], sc) : encode8f<F, false>(v[c], sc);
+        if (ch < nch) qr[ch] = o;
+    }
+}
+
+// Any layout (columns, strides and pointers of any alignment, rows of any
+// length): one workgroup per row, element loads, the row read again from the
+// caches for each pass.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+    v = wave_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (red[0] + red[1]) + (red[2] + red[3]);
+}
+__device__ __forceinline__ float load_bf16(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+
+template <int F>
+__global__ __launch_bounds__(kBlock) void k_norm_quant_row_any(NormFwd p) {
+    __shared__ float red[kWaves];
+    __shared__ uint32_t redu[kWaves];
+    const int tid = threadIdx.x;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const uint16_t* xr = p.x + row * p.ldx;
+        const float inv_n = 1.0f / (float)p.cols;
+        float mean = 0.0f, s = 0.0f;
+        if (!p.rms) {
+            for (int64_t c = tid; c < p.cols; c += kBlock) s += load_bf16(xr + c);
+            mean = block_sum(s, red) * inv_n;
+        }
+        float ss = 0.0f;
+        for (int64_t c = tid; c < p.cols; c += kBlock) {
+            const float d = load_bf16(xr + c) - mean;
+            ss = fmaf(d, d, ss);
+        }
+        const float rstd = 1.0f / __builtin_sqrtf(block_sum(ss, red) * inv_n + p.eps);
+        if (tid == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+        auto value = [&](int64_t c) {
+            float y = (load_bf16(xr + c) - mean) * rstd;
+            if (p.gamma) y *= load_weight(p.gamma, p.w_f32, c);
+            if (p.beta) y += load_weight(p.beta, p.w_f32, c);
+            return y;
+        };
+        uint32_t mx = 0;
+        for (int64_t c = tid; c < p.cols; c += kBlock) {
+            const float y = value(c);
+            if (p.y) p.y[row * p.ldy + c] = (uint16_t)f32_to_bf16(y);
+            const uint32_t b = __float_as_uint(y) & 0x7fffffffu;
+            mx = b > mx ? b : mx;
+        }
+        if (!p.q) continue;
+        mx = wave_max_u32(mx);
+        __syncthreads();
+        if ((tid & 63) == 0) redu[tid >> 6] = mx;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) mx = redu[w] > mx ? redu[w] : mx;
+        const float sc = scale_from_amax<F>(__uint_as_float(mx), p.margin);
+        if (tid == 0) p.scale_inv[row] = 1.0f / sc;
+        for (int64_t c = tid; c < p.cols; c += kBlock) p.q[row * p.ldq + c] = (uint8_t)encode_sw<F>(value(c) * sc);
+    }
+}
+
+// --------------------------------------------------------------- backward --
+// A workgroup owns a band of neighbouring rows; TPR threads work on one row (a
+// team), each on the same MAXC chunks of 8 columns for every row, so that the
+// sums over rows of the weights' gradients stay in registers. A row costs one
+// barrier (its two sums meet in LDS, in one of two buffers); the next row's
+// loads are issued before the current row is worked on. At the end the teams'
+// sums are added in LDS in team order and the band's sums are written to the
+// workspace; k_norm_weight_grad adds the bands in order. No atomics: results
+// do not depend on timing.
+// SRC: 0 = x in bf16 with mean and rstd, 1 / 2 = the checkpoint in e4m3 / e5m2.
+template <int SRC, int MAXC>
+struct RowData {
+    uint4 dy[MAXC];
+    uint32_t x[MAXC][SRC == 0 ? 4 : 2];
+    uint32_t byte[MAXC];                // (SRC > 0: the block's scale)
+    float mean, rstd;
+};
+
+template <int SRC, int TPR, int MAXC>
+__device__ __forceinline__ void load_row(const NormBwd& p, int row, uint32_t tt, uint32_t nch, RowData<SRC, MAXC>* d) {
+    d->rstd = p.rstd[row];
+    d->mean = SRC == 0 && p.mean ? p.mean[row] : 0.0f;
+    const uint16_t* dr = p.dy + row * p.lddy;
+#pragma unroll
+    for (int c = 0; c < MAXC; ++c) {
+        const uint32_t ch = tt + c * TPR;
+        const uint32_t cc = ch < nch ? ch : nch - 1;
+        d->dy[c] = load_stream(at<uint4>(dr, cc * 16));
+        if constexpr (SRC == 0) {
+            const uint4 x = load_stream(at<uint4>(p.x + row * p.ldx, cc * 16));
+            d->x[c][0] = x.x;
+            d->x[c][1] = x.y;
+            d->x[c][2] = x.z;
+            d->x[c][3] = x.w;
+        } else {
+            const uint2 q = *at<uint2>(p.xq + row * p.ldxq, cc * 8);
+            d->x[c][0] = q.x;
+            d->x[c][1] = q.y;
+            d->byte[c] = (p.xs + 4 * (int64_t)row)[4 * (int64_t)(cc >> 4) * p.ldxs + ((cc >> 2) & 3u)];
+        }
+    }
+}
+
+// (4-byte stores: dgamma and dbeta have no alignment of their own)
+__device__ __forceinline__ void store8(float* p, const float* v) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = v[i];
+}
+
+// Chunk c of the row as fp32: xh and dy, zeros where it is not live.
+template <int SRC, int MAXC>
+__device__ __forceinline__ void row_values(const RowData<SRC, MAXC>& d, int c, bool live, float* xh, float* dy) {
+    unpack8(d.dy[c], dy);
+    if constexpr (SRC == 0) {
+        unpack8(make_uint4(d.x[c][0], d.x[c][1], d.x[c][2], d.x[c][3]), xh);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xh[i] = (xh[i] - d.mean) * d.rstd;
+    } else {
+        decode4<SRC == 1 ? kE4M3 : kE5M2>(d.x[c][0], xh);
+        decode4<SRC == 1 ? kE4M3 : kE5M2>(d.x[c][1], xh + 4);
+        const float bs = e8m0_value(d.byte[c]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xh[i] *= bs;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        xh[i] = live ? xh[i] : 0.0f;
+        dy[i] = live ? dy[i] : 0.0f;
+    }
+}
+
+template <int SRC, int TPR, int MAXC>
+__global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_norm_grad(NormBwd p) {
+    constexpr int WG = TPR < 512 ? 512 : TPR, TEAMS = WG / TPR, NW = TPR / 64;
+    __shared__ float2 red[2][WG / 64];
+    __shared__ float fold[TEAMS > 1 ? 2 * MAXC * 8 * TPR : 1];
+    __shared__ float beta[SRC > 0 ? MAXC * 8 * TPR : 1];
+    // (the team is uniform over a wavefront: row addresses stay in scalar registers)
+    const int tid = threadIdx.x, team = __builtin_amdgcn_readfirstlane(tid / TPR);
+    const int wave = tid >> 6, lane = tid & 63;
+    uint32_t tt = (uint32_t)tid % TPR;
+    const uint32_t nch = (uint32_t)(p.cols >> 3);
+    const float inv_n = 1.0f / (float)p.cols;
+    const int r0 = (int)(blockIdx.x * p.band);
+    const int r1 = r0 + p.band < p.rows ? (int)(r0 + p.band) : (int)p.rows;
+    const bool want = p.dgamma || p.dbeta;
+    float g[MAXC][8], dg[MAXC][8], db[MAXC][8];
+#pragma unroll
+    for (int c = 0; c < MAXC; ++c) {
+        const uint32_t ch = tt + c * TPR, cc = ch < nch ? ch : nch - 1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            g[c][i] = 1.0f;
+            dg[c][i] = db[c][i] = 0.0f;
+        }
+        if (p.gamma) load_weights8(p.gamma, p.w_f32, cc, g[c]);
+        // beta in LDS: the addresses of its two forms, kept over the loop, spilled
+        if (SRC > 0 && p.y && p.beta && team == 0) {
+            float b[8];
+            load_weights8(p.beta, p.w_f32, cc, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) beta[(c * TPR + tt) * 8 + i] = b[i];
+        }
+    }
+    if (SRC > 0) __syncthreads();
+    RowData<SRC, MAXC> cur, nxt;
+    load_row<SRC, TPR, MAXC>(p, r0 + team < r1 ? r0 + team : r1 - 1, tt, nch, &cur);
+    int buf = 0;
+    for (int r = r0; r < r1; r += TEAMS, buf ^= 1) {
+        const int row = r + team;
+        const bool live_row = row < r1;
+        const int next = row + TEAMS;
+        // tt opaque in every step: offsets are then formed where they are used,
+        // next to scalar bases, and not kept as 64-bit pairs over the loop
+        asm volatile("" : "+v"(tt));
+        load_row<SRC, TPR, MAXC>(p, next < r1 ? next : r1 - 1, tt, nch, &nxt);
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int c = 0; c < MAXC; ++c) {
+            const uint32_t ch = tt + c * TPR;
+            const bool live = live_row && ch < nch;
+            float xh[8], dy[8];
+            row_values<SRC>(cur, c, live, xh, dy);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float w = dy[i] * g[c][i];
+                s1 = fmaf(w, xh[i], s1);
+                s2 += w;
+            }
+            if (SRC > 0 && p.y && live) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    xh[i] *= g[c][i];
+                    if (p.beta) xh[i] += beta[(c * TPR + tt) * 8 + i];
+                }
+                *at<uint4>(p.y + row * p.ldy, ch * 16) = pack8(xh);
+            }
+        }
+        s1 = wave_sum(s1);
+        s2 = wave_sum(s2);
+        if (NW > 1) {
+            if (lane == 0) red[buf][wave] = make_float2(s1, s2);
+            __syncthreads();
+            s1 = s2 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float2 f = red[buf][team * NW + w];
+                s1 += f.x;
+                s2 += f.y;
+            }
+        }
+        const float c1 = s1 * inv_n, c2 = p.rms ? 0.0f : s2 * inv_n;
+#pragma unroll
+        for (int c = 0; c < MAXC; ++c) {
+            const uint32_t ch = tt + c * TPR;
+            const bool live = live_row && ch < nch;
+            // the row's values again from its raw words (made opaque here, so
+            // that they are not kept): holding them across the reduction took
+            // 178 VGPRs, one workgroup of 512 threads per CU instead of two
+            asm volatile("" : "+v"(cur.dy[c].x), "+v"(cur.dy[c].y), "+v"(cur.dy[c].z), "+v"(cur.dy[c].w));
+            asm volatile("" : "+v"(cur.x[c][0]), "+v"(cur.x[c][1]));
+            if constexpr (SRC == 0) asm volatile("" : "+v"(cur.x[c][2]), "+v"(cur.x[c][3]));
+            float xh[8], dy[8], o[8];
+            row_values<SRC>(cur, c, live, xh, dy);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = cur.rstd * (fmaf(-c1, xh[i], dy[i] * g[c][i]) - c2);
+            if (live) *at<uint4>(p.dx + row * p.lddx, ch * 16) = pack8(o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dg[c][i] = fmaf(dy[i], xh[i], dg[c][i]);
+                db[c][i] += dy[i];
+            }
+        }
+        cur = nxt;
+    }
+    if (!want) return;
+    if constexpr (TEAMS > 1) {                              // word (2 c' + which) * TPR + tt: no bank conflicts
+        for (int t = 1; t < TEAMS; ++t) {
+            __syncthreads();
+            if (team == t) {
+#pragma unroll
+                for (int c = 0; c < MAXC; ++c)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        fold[(2 * (c * 8 + i)) * TPR + tt] = dg[c][i];
+                        fold[(2 * (c * 8 + i) + 1) * TPR + tt] = db[c][i];
+                    }
+            }
+            __syncthreads();
+            if (team == 0) {
+#pragma unroll
+                for (int c = 0; c < MAXC; ++c)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        dg[c][i] += fold[(2 * (c * 8 + i)) * TPR + tt];
+                        db[c][i] += fold[(2 * (c * 8 + i) + 1) * TPR + tt];
+                    }
+            }
+        }
+        if (team != 0) return;
+    }
+    // one band: its sums are the result
+    float* og = p.bands == 1 ? p.dgamma : p.partial + (int64_t)blockIdx.x * 2 * p.cols;
+    float* ob = p.bands == 1 ? p.dbeta : p.partial + (int64_t)blockIdx.x * 2 * p.cols + p.cols;
+#pragma unroll
+    for (int c = 0; c < MAXC; ++c) {
+        const uint32_t ch = tt + c * TPR;
+        if (ch >= nch) continue;
+        if (p.dgamma) store8(og + (int64_t)ch * 8, dg[c]);
+        if (p.dbeta) store8(ob + (int64_t)ch * 8, db[c]);
+    }
+}
+
+// Sums of the bands, in order: 32 columns x 8 slices of the bands per
+// workgroup, the slices added in order. blockIdx.y: 0 = dgamma, 1 = dbeta.
+constexpr int kSliceCols = 32, kSlices = 8;
+__global__ __launch_bounds__(kBlock) void k_norm_weight_grad(const float* __restrict__ partial, int64_t bands,
+                                                             int64_t cols, float* dgamma, float* dbeta) {
+    __shared__ float red[kSlices][kSliceCols];
+    float* out = blockIdx.y == 0 ? dgamma : dbeta;
+    if (!out) return;
+    const int cl = threadIdx.x % kSliceCols, sl = threadIdx.x / kSliceCols;
+    const int64_t col = (int64_t)blockIdx.x * kSliceCols + cl;
+    const int64_t per = (bands + kSlices - 1) / kSlices;
+    const int64_t b0 = sl * per, b1 = b0 + per < bands ? b0 + per : bands;
+    const float* src = partial + (int64_t)blockIdx.y * cols + (col < cols ? col : cols - 1);
+    float s = 0.0f;
+#pragma unroll 8
+    for (int64_t b = b0; b < b1; ++b) s += src[b * 2 * cols];
+    red[sl][cl] = s;
+    __syncthreads();
+    if (sl == 0 && col < cols) {
+#pragma unroll
+        for (int i = 1; i < kSlices; ++i) s += red[i][cl];
+        out[col] = s;
+    }
+}
+
+// Any layout, from x: one workgroup per row for dx; for the weights' gradients
+// one thread per column over a band of rows.
+__global__ __launch_bounds__(kBlock) void k_norm_grad_row_any(NormBwd p) {
+    __shared__ float red[kWaves];
+    const int tid = threadIdx.x;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const uint16_t *xr = p.x + row * p.ldx, *dr = p.dy + row * p.lddy;
+        const float rstd = p.rstd[row], mean = p.mean ? p.mean[row] : 0.0f, inv_n = 1.0f / (float)p.cols;
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int64_t c = tid; c < p.cols; c += kBlock) {
+            const float w = load_bf16(dr + c) * (p.gamma ? load_weight(p.gamma, p.w_f32, c) : 1.0f);
+            s1 = fmaf(w, (load_bf16(xr + c) - mean) * rstd, s1);
+            s2 += w;
+        }
+        const float c1 = block_sum(s1, red) * inv_n, c2 = p.rms ? 0.0f : block_sum(s2, red) * inv_n;
+        for (int64_t c = tid; c < p.cols; c += kBlock) {
+            const float w = load_bf16(dr + c) * (p.gamma ? load_weight(p.gamma, p.w_f32, c) : 1.0f);
+            const float xh = (load_bf16(xr + c) - mean) * rstd;
+            p.dx[row * p.lddx + c] = (uint16_t)f32_to_bf16(rstd * (fmaf(-c1, xh, w) - c2));
+        }
+    }
+}
+
+__global__ __launch_bounds__(kBlock) void k_norm_grad_cols_any(NormBwd p) {
+    const int64_t c = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+    if (c >= p.cols) return;
+    const int64_t r0 = (int64_t)blockIdx.y * p.band;
+    const int64_t r1 = r0 + p.band < p.rows ? r0 + p.band : p.rows;
+    float dg = 0.0f, db = 0.0f;
+#pragma unroll 4
+    for (int64_t r = r0; r < r1; ++r) {
+        const float xh = (load_bf16(p.x + r * p.ldx + c) - (p.mean ? p.mean[r] : 0.0f)) * p.rstd[r];
+        const float dy = load_bf16(p.dy + r * p.lddy + c);
+        dg = fmaf(dy, xh, dg);
+        db += dy;
+    }
+    float* og = p.bands == 1 ? p.dgamma : p.partial + (int64_t)blockIdx.y * 2 * p.cols;
+    float* ob = p.bands == 1 ? p.dbeta : p.partial + (int64_t)blockIdx.y * 2 * p.cols + p.cols;
+    if (p.dgamma) og[c] = dg;
+    if (p.dbeta) ob[c] = db;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+unsigned row_grid(int64_t rows) { return (unsigned)(rows < (1 << 20) ? rows : (1 << 20)); }
+
+}  // namespace
+
+template <int F>
+hipError_t norm_quant_fmt(const NormFwd& p, bool vec, hipStream_t st) {
+    const dim3 block(kBlock);
+    if (!vec) {
+        hipLaunchKernelGGL((k_norm_quant_row_any<F>), dim3(row_grid(p.rows)), block, 0, st, p);
+        return hipGetLastError();
+    }
+    const int64_t nch = p.cols / 8;
+    const bool wide = nch > 256 || (nch > 64 && p.rows < 1024);
+    const dim3 grid((unsigned)(wide ? p.rows : (p.rows + kWaves - 1) / kWaves));
+#define FP8_NORM_CASE(C, W) hipLaunchKernelGGL((k_norm_quant_row<F, C, W>), grid, block, 0, st, p)
+    if (wide) {
+        if (nch <= 256) FP8_NORM_CASE(1, 4);
+        else if (nch <= 512) FP8_NORM_CASE(2, 4);
+        else if (nch <= 1024) FP8_NORM_CASE(4, 4);
+        else FP8_NORM_CASE(8, 4);
+    } else {
+        if (nch <= 64) FP8_NORM_CASE(1, 1);
+        else if (nch <= 128) FP8_NORM_CASE(2, 1);
+        else FP8_NORM_CASE(4, 1);
+    }
+#undef FP8_NORM_CASE
+    return hipGetLastError();
+}
+
+bool norm_vector_layout(const NormFwd& p) {
+    return p.cols % 8 == 0 && p.cols <= kNormMaxVecCols && p.ldx % 8 == 0 && aligned16(p.x) && aligned16(p.gamma) &&
+           aligned16(p.beta) && (!p.q || (p.ldq % 8 == 0 && (reinterpret_cast<uintptr_t>(p.q) & 7) == 0)) &&
+           (!p.y || (p.ldy % 8 == 0 && aligned16(p.y)));
+}
+
+bool norm_vector_layout(const NormBwd& p) {
+    return p.cols % 8 == 0 && p.cols <= kNormMaxVecCols && p.lddy % 8 == 0 && p.lddx % 8 == 0 && aligned16(p.dy) &&
+           aligned16(p.dx) && aligned16(p.gamma) && aligned16(p.beta) &&
+           (p.xq || (p.ldx % 8 == 0 && aligned16(p.x))) && (!p.y || (p.ldy % 8 == 0 && aligned16(p.y)));
+}
+
+hipError_t launch_norm_quant_row(const NormFwd& p, int fmt, hipStream_t st) {
+    if (p.rows == 0 || p.cols == 0) return hipSuccess;
+    const bool vec = norm_vector_layout(p);
+    switch (fmt) {
+        case kE4M3: return norm_quant_fmt<kE4M3>(p, vec, st);
+        case kE5M2: return norm_quant_fmt<kE5M2>(p, vec, st);
+        case kE4M3Fnuz: return norm_quant_fmt<kE4M3Fnuz>(p, vec, st);
+        default: return norm_quant_fmt<kE5M2Fnuz>(p, vec, st);
+    }
+}
+
+template <int SRC>
+hipError_t norm_grad_src(NormBwd p, hipStream_t st) {
+    const int64_t nch = p.cols / 8;
+    const int tpr = nch <= 128 ? 64 : (nch <= 256 ? 128 : (nch <= 512 ? 256 : (nch <= 1024 ? 512 : 1024)));
+    const int64_t teams = tpr < 512 ? 512 / tpr : 1;
+    const int64_t max_bands = tpr < 1024 ? kNormMaxBands : kNormMaxBands / 2;
+    int64_t band = (p.rows + max_bands - 1) / max_bands;
+    p.band = (band + teams - 1) / teams * teams;
+    p.bands = (p.rows + p.band - 1) / p.band;
+    const dim3 grid((unsigned)p.bands);
+#define FP8_NORM_CASE(T, C) \
+    hipLaunchKernelGGL((k_norm_grad<SRC, T, C>), grid, dim3(T < 512 ? 512 : T), 0, st, p)
+    if (nch <= 64) FP8_NORM_CASE(64, 1);
+    else if (nch <= 128) FP8_NORM_CASE(64, 2);
+    else if (nch <= 256) FP8_NORM_CASE(128, 2);
+    else if (nch <= 512) FP8_NORM_CASE(256, 2);
+    else if (nch <= 1024) FP8_NORM_CASE(512, 2);
+    else FP8_NORM_CASE(1024, 2);
+#undef FP8_NORM_CASE
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && (p.dgamma || p.dbeta) && p.bands > 1) {
+        hipLaunchKernelGGL(k_norm_weight_grad, dim3((unsigned)((p.cols + kSliceCols - 1) / kSliceCols), 2),
+                           dim3(kBlock), 0, st, p.partial, p.bands, p.cols, p.dgamma, p.dbeta);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+hipError_t launch_norm_backward(const NormBwd& p0, hipStream_t st) {
+    NormBwd p = p0;
+    hipError_t e = hipSuccess;
+    if (p.cols == 0) return e;
+    if (p.rows == 0) {                                      // empty sums
+        if (p.dgamma) e = launch_fill(p.dgamma, p.cols, 0.0f, st);
+        if (p.dbeta && e == hipSuccess) e = launch_fill(p.dbeta, p.cols, 0.0f, st);
+        return e;
+    }
+    if (p.xq) return p.ckpt_e5m2 ? norm_grad_src<2>(p, st) : norm_grad_src<1>(p, st);
+    if (norm_vector_layout(p)) return norm_grad_src<0>(p, st);
+    hipLaunchKernelGGL(k_norm_grad_row_any, dim3(row_grid(p.rows)), dim3(kBlock), 0, st, p);
+    e = hipGetLastError();
+    if (e != hipSuccess || (!p.dgamma && !p.dbeta)) return e;
+    p.band = (p.rows + kNormMaxBands - 1) / kNormMaxBands;
+    if (p.band < 32) p.band = 32;
+    p.bands = (p.rows + p.band - 1) / p.band;
+    hipLaunchKernelGGL(k_norm_grad_cols_any, dim3((unsigned)((p.cols + kBlock - 1) / kBlock), (unsigned)p.bands),
+                       dim3(kBlock), 0, st, p);
+    e = hipGetLastError();
+    if (e == hipSuccess && p.bands > 1) {
+        hipLaunchKernelGGL(k_norm_weight_grad, dim3((unsigned)((p.cols + kSliceCols - 1) / kSliceCols), 2),
+                           dim3(kBlock), 0, st, p.partial, p.bands, p.cols, p.dgamma, p.dbeta);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+}  // namespace fp8amax

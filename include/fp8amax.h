@@ -23,7 +23,8 @@
  *
  * Conventions common to every entry point
  *  - Pointers named x, q, qt, amax*, scale*, history, head, a, b, d and
- *    group_offsets are DEVICE pointers owned by the caller. The library
+ *    group_offsets, and those of the entry points from fp8_norm_quantize_row
+ *    on, are DEVICE pointers owned by the caller. The library
  *    allocates nothing and keeps no state between calls except a per-device
  *    properties cache.
  *  - Matrices are row-major with an explicit leading dimension counted in
@@ -494,6 +495,150 @@ fp8_status_t fp8_swiglu_quantize_row(const uint16_t* h, int64_t rows, int64_t in
 fp8_status_t fp8_moe_unpermute_combine(const uint16_t* y, int64_t rows, int64_t cols, int64_t ldy,
                                        const int32_t* dest, const float* weights, int64_t tokens, int32_t topk,
                                        uint16_t* out, int64_t ldo, void* stream);
+
+/* ----------------------------------------------- the layer's norm and its gradient --
+ * Layer norm, or its RMS form, in front of an FP8 product, fused with the
+ * rowwise cast, and the backward pass ([Flux] and [Titan] train transformer
+ * layers whose linears take a norm's output; the pages define no norm, the
+ * formulas here are the usual ones). Row r of N = cols values:
+ *   mu = sum x / N (FP8_NORM_RMS: 0), v = sum (x - mu)^2 / N,
+ *   rstd = 1 / sqrt(v + eps), xhat = (x - mu) * rstd, y = xhat * gamma + beta.
+ * All in fp32 from the bf16 inputs; every output is rounded once. */
+typedef enum { FP8_NORM_LAYER = 0, FP8_NORM_RMS = 1 } fp8_norm_t;
+
+/* Forward. x: bf16 [rows x cols] (ldx). gamma, beta [cols]: NULL for 1 and 0;
+ * their type is w_type (FP8_OUT_BF16 or FP8_OUT_F32), both alike. Outputs, at
+ * least one of q and y:
+ *  - q: codes [rows x cols] (ldq) of y, cast rowwise from fp32 (the scale rule
+ *    of fp8_quantize_row with max |y| of the row), with scale_inv_out [rows]
+ *    (required with q; both NULL to skip);
+ *  - y: bf16 [rows x cols] (ldy), or NULL;
+ *  - mean_out, rstd_out [rows] fp32, or NULL: what the backward pass takes
+ *    (mean_out is 0 for FP8_NORM_RMS);
+ *  - xhat_q, xhat_scale: an 8-bit checkpoint of xhat for the backward pass, in
+ *    the MX format (above): codes xhat_fmt (OCP e4m3 or e5m2) [rows x cols]
+ *    (ldxq) and scale records (ld_scale >= rows); both NULL to skip (xhat_fmt
+ *    is then ignored). Saving xhat instead of x keeps the checkpoint's error
+ *    relative to the normalised value whatever the row's mean and scale.
+ * cols >= 1; rows < 2^30 (else FP8_ERR_UNSUPPORTED); eps >= 0 and finite;
+ * margin 0..32; x, y 2-byte aligned, gamma / beta to their type. Vector path
+ * when x, y, gamma, beta are 16-byte and q 8-byte aligned, ldx, ldy, ldq, cols
+ * multiples of 8 and cols <= 16384; any other layout takes a scalar path. The
+ * checkpoint needs the vector path (else FP8_ERR_ALIGNMENT, or
+ * FP8_ERR_UNSUPPORTED for cols > 16384), cols % 32 == 0 (else
+ * FP8_ERR_INVALID_ARG), xhat_q 8-byte aligned, ldxq % 8 == 0 and xhat_scale
+ * 4-byte aligned. Outputs do not overlap each other or the inputs. */
+fp8_status_t fp8_norm_quantize_row(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, const void* gamma,
+                                   const void* beta, fp8_out_t w_type, float eps, fp8_norm_t kind, fp8_format_t fmt,
+                                   int32_t margin, uint8_t* q, int64_t ldq, float* scale_inv_out, uint16_t* y,
+                                   int64_t ldy, float* mean_out, float* rstd_out, uint8_t* xhat_q,
+                                   fp8_format_t xhat_fmt, int64_t ldxq, uint8_t* xhat_scale, int64_t ld_scale,
+                                   void* stream);
+
+/* Bytes of workspace that the backward passes below need for these sizes (they
+ * hold the partial sums of dgamma and dbeta, summed in a fixed order); 0 for
+ * sizes that are not valid. */
+int64_t fp8_norm_backward_workspace(int64_t rows, int64_t cols);
+
+/* Backward from x: with w = dy * gamma,
+ *   dx = rstd * (w - mean(w) - xhat * mean(w * xhat))   (FP8_NORM_RMS: without mean(w))
+ *   dgamma[c] = sum over rows of dy * xhat, dbeta[c] = sum over rows of dy,
+ * means over the row. dy, x: bf16 [rows x cols]; mean (ignored for
+ * FP8_NORM_RMS, may be NULL there), rstd: fp32 [rows] of the forward pass; dx:
+ * bf16 [rows x cols]; dgamma, dbeta: fp32 [cols], either or both NULL to skip;
+ * overwritten (0 for rows == 0). gamma as in the forward pass. workspace:
+ * 16-byte aligned, workspace_bytes >= fp8_norm_backward_workspace(rows, cols);
+ * may be NULL when dgamma and dbeta are. It is free for other use once the
+ * call's work is done; calls that may run at the same time need one each.
+ * Results do not depend on timing (no atomics). Sizes and layouts as the
+ * forward pass (vector and scalar path). Outputs do not overlap each other or
+ * the inputs. */
+fp8_status_t fp8_norm_backward(const uint16_t* dy, int64_t rows, int64_t cols, int64_t lddy, const uint16_t* x,
+                               int64_t ldx, const void* gamma, fp8_out_t w_type, const float* mean, const float* rstd,
+                               fp8_norm_t kind, uint16_t* dx, int64_t lddx, float* dgamma, float* dbeta,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Backward from the forward pass's checkpoint: as fp8_norm_backward with xhat =
+ * the value the checkpoint holds, code * 2^(byte - 127) (NaN for byte 255). y
+ * (bf16 [rows x cols], or NULL): xhat * gamma + beta from the same read, what
+ * the colwise cast for the next product's weight gradient takes; beta is used
+ * for y alone. Needs the layout the checkpoint's forward pass needs (dy, dx, y,
+ * gamma, beta 16-byte aligned, lddy, lddx, ldy multiples of 8, cols % 32 == 0
+ * and <= 16384). */
+fp8_status_t fp8_mx_norm_backward(const uint16_t* dy, int64_t rows, int64_t cols, int64_t lddy, const uint8_t* xhat_q,
+                                  fp8_format_t xhat_fmt, int64_t ldxq, const uint8_t* xhat_scale, int64_t ld_scale,
+                                  const void* gamma, const void* beta, fp8_out_t w_type, const float* rstd,
+                                  fp8_norm_t kind, uint16_t* dx, int64_t lddx, float* dgamma, float* dbeta,
+                                  uint16_t* y, int64_t ldy, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------- SwiGLU with an 8-bit checkpoint --
+ * fp8_swiglu_quantize_row for a training step: the same definition (a =
+ * silu(gate) * up of h = [gate | up], cast rowwise from fp32), and from the
+ * same read of h an 8-bit checkpoint of it, exactly as fp8_mx_quantize_row(h)
+ * gives it: codes hq (h_fmt, OCP e4m3 or e5m2) [rows x 2 inter] (ldhq) and scale
+ * records h_scale (ld_scale >= rows), both required. The logistic function is
+ * evaluated to fp32 accuracy (a few units in the last place); exp(-|gate|)
+ * below 2^-126 counts as 0. Requirements: inter % 32 == 0 (else
+ * FP8_ERR_INVALID_ARG), inter <= 16384, rows < 2^26 (else
+ * FP8_ERR_UNSUPPORTED); h 16-byte aligned, ldh % 8 == 0; q, hq 8-byte aligned,
+ * ldq, ldhq multiples of 8; h_scale 4-byte aligned. */
+fp8_status_t fp8_swiglu_quantize_row_mx(const uint16_t* h, int64_t rows, int64_t inter, int64_t ldh, fp8_format_t fmt,
+                                        int32_t margin, uint8_t* q, int64_t ldq, float* scale_inv_out, uint8_t* hq,
+                                        fp8_format_t h_fmt, int64_t ldhq, uint8_t* h_scale, int64_t ld_scale,
+                                        void* stream);
+
+/* SwiGLU's backward pass: with s = 1 / (1 + exp(-gate)),
+ *   d(up) = da * gate * s,   d(gate) = da * up * s * (1 + gate * (1 - s)),
+ * from h bf16 [rows x 2 inter] (ldh). da: bf16 [rows x inter] (ldda); dh: bf16
+ * [rows x 2 inter] (lddh) = [d(gate) | d(up)]; a (bf16 [rows x inter] (lda), or
+ * NULL): silu(gate) * up from the same read, what the colwise cast for the down
+ * product's weight gradient takes. Evaluated in fp32, rounded once; an infinite
+ * gate follows that arithmetic (s * (1 + gate * (1 - s)) of +Inf is NaN).
+ * Requirements: inter % 8 == 0; da, h, dh, a 16-byte aligned, ldda, ldh, lddh,
+ * lda multiples of 8; rows < 2^30 (else FP8_ERR_UNSUPPORTED). dh and a do not
+ * overlap each other or the inputs. */
+fp8_status_t fp8_swiglu_backward(const uint16_t* da, int64_t rows, int64_t inter, int64_t ldda, const uint16_t* h,
+                                 int64_t ldh, uint16_t* dh, int64_t lddh, uint16_t* a, int64_t lda, void* stream);
+
+/* The same from the checkpoint of fp8_swiglu_quantize_row_mx (or of
+ * fp8_mx_quantize_row or fp8_blockwise_quantize_act of h): gate and up are the
+ * values it holds, code * 2^(byte - 127), NaN for byte 255. inter % 32 == 0;
+ * hq 8-byte aligned, ldhq % 8 == 0; h_scale 4-byte aligned; otherwise as
+ * fp8_swiglu_backward. */
+fp8_status_t fp8_mx_swiglu_backward(const uint16_t* da, int64_t rows, int64_t inter, int64_t ldda, const uint8_t* hq,
+                                    fp8_format_t h_fmt, int64_t ldhq, const uint8_t* h_scale, int64_t ld_scale,
+                                    uint16_t* dh, int64_t lddh, uint16_t* a, int64_t lda, void* stream);
+
+/* ------------------------------------------------ the MoE layer for a few tokens --
+ * The MoE layer (its definition above) for decode-sized batches, in two
+ * launches that read the weights of each expert in use once; no routing pass,
+ * no permutation, activations not cast to FP8:
+ *   g, u = the two halves of x_t W1_e^T, e = expert_idx[t, j];
+ *   out[t] = bf16( sum over j of weights[t, j] * (silu(g) * u) W2_e^T )
+ * with fp32 sums. x: bf16 [tokens x hidden] (ldx); expert_idx int32, weights
+ * fp32 [tokens x topk] (device); W1: codes [num_experts x 2 inter x hidden]
+ * (gate rows, then up rows; row stride ld1, expert stride w1_expert_stride)
+ * times w1_scale_inv [num_experts x 2 inter]; W2: codes [num_experts x hidden x
+ * inter] likewise with w2_scale_inv [num_experts x hidden]: the operands that
+ * fp8_grouped_gemm_scaled takes. out: bf16 [tokens x hidden] (ldo). Entries
+ * whose expert index is outside [0, num_experts) add nothing; a token without a
+ * valid entry gets zeros; an expert named twice by a token counts with the sum
+ * of the two weights. Each token's result depends on its own row alone.
+ * workspace: tokens * topk * inter * 4 bytes, 16-byte aligned, workspace_bytes
+ * at least that; free for other use once the call's work is done, and calls
+ * that may run at the same time need one each. Formats: OCP e4m3 / e5m2 (fnuz:
+ * FP8_ERR_UNSUPPORTED). Limits: tokens 0..FP8_MOE_FEW_TOKENS (more:
+ * FP8_ERR_UNSUPPORTED; use the layer's own entry points), topk 1..64,
+ * num_experts 1..1024, hidden and inter >= 16, multiples of 16, < 2^20. x, w1,
+ * w2 16-byte aligned; ldx % 8 == 0; ld1, ld2 and the expert strides multiples
+ * of 16. */
+#define FP8_MOE_FEW_TOKENS 64
+fp8_status_t fp8_moe_few_tokens(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t ldx,
+                                const int32_t* expert_idx, const float* weights, int32_t topk, int32_t num_experts,
+                                const uint8_t* w1, fp8_format_t f1, int64_t ld1, int64_t w1_expert_stride,
+                                const float* w1_scale_inv, const uint8_t* w2, fp8_format_t f2, int64_t ld2,
+                                int64_t w2_expert_stride, const float* w2_scale_inv, int64_t inter, uint16_t* out,
+                                int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
