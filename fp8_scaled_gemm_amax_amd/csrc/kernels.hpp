@@ -178,8 +178,18 @@ struct NormBwd {
     int64_t band, bands;
 };
 
-bool norm_vector_layout(const NormFwd& p);
-bool norm_vector_layout(const NormBwd& p);
+// Whether the register kernels take these operands (16-byte chunks everywhere).
+inline bool chunked(const void* p, int64_t ld, unsigned align) {
+    return !p || ((reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0 && ld % 8 == 0);
+}
+inline bool norm_vector_layout(const NormFwd& p) {
+    return p.cols % 8 == 0 && p.cols <= kNormMaxVecCols && chunked(p.x, p.ldx, 16) && chunked(p.gamma, 0, 16) &&
+           chunked(p.beta, 0, 16) && chunked(p.q, p.ldq, 8) && chunked(p.y, p.ldy, 16);
+}
+inline bool norm_vector_layout(const NormBwd& p) {
+    return p.cols % 8 == 0 && p.cols <= kNormMaxVecCols && chunked(p.dy, p.lddy, 16) && chunked(p.dx, p.lddx, 16) &&
+           chunked(p.gamma, 0, 16) && chunked(p.beta, 0, 16) && chunked(p.x, p.ldx, 16) && chunked(p.y, p.ldy, 16);
+}
 hipError_t launch_norm_quant_row(const NormFwd& p, int fmt, hipStream_t st);
 hipError_t launch_norm_backward(const NormBwd& p, hipStream_t st);
 

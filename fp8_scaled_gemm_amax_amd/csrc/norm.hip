@@ -500,8 +500,6 @@ __global__ __launch_bounds__(kBlock) void k_norm_grad_cols_any(NormBwd p) {
     if (p.dbeta) ob[c] = db;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 unsigned row_grid(int64_t rows) { return (unsigned)(rows < (1 << 20) ? rows : (1 << 20)); }
 
 }  // namespace
@@ -529,18 +527,6 @@ hipError_t norm_quant_fmt(const NormFwd& p, bool vec, hipStream_t st) {
     }
 #undef FP8_NORM_CASE
     return hipGetLastError();
-}
-
-bool norm_vector_layout(const NormFwd& p) {
-    return p.cols % 8 == 0 && p.cols <= kNormMaxVecCols && p.ldx % 8 == 0 && aligned16(p.x) && aligned16(p.gamma) &&
-           aligned16(p.beta) && (!p.q || (p.ldq % 8 == 0 && (reinterpret_cast<uintptr_t>(p.q) & 7) == 0)) &&
-           (!p.y || (p.ldy % 8 == 0 && aligned16(p.y)));
-}
-
-bool norm_vector_layout(const NormBwd& p) {
-    return p.cols % 8 == 0 && p.cols <= kNormMaxVecCols && p.lddy % 8 == 0 && p.lddx % 8 == 0 && aligned16(p.dy) &&
-           aligned16(p.dx) && aligned16(p.gamma) && aligned16(p.beta) &&
-           (p.xq || (p.ldx % 8 == 0 && aligned16(p.x))) && (!p.y || (p.ldy % 8 == 0 && aligned16(p.y)));
 }
 
 hipError_t launch_norm_quant_row(const NormFwd& p, int fmt, hipStream_t st) {

@@ -1,0 +1,232 @@
+"""GPU parity of the MoE layer for a few tokens against its fp64 definition
+(oracle/layer.py): every output within fp32 rounding of the sums plus half a
+step of bf16. One to 64 tokens (every tile count), one to 64 slots, experts
+that nobody names, names out of range, names twice; lengths of K that end
+inside a load block; strided weights; NaN rows and NaN codes; graphs."""
+import numpy as np
+import pytest
+import torch
+
+import workloads
+from helpers import check_guard, dev_bf16, dev_f32, dev_u8, guarded, host_bits, say
+from oracle import layer
+from test_gpu_norm import within
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF = layer.BF16
+
+
+@pytest.fixture(scope="module")
+def fp8():
+    import fp8_scaled_gemm_amax_amd as m
+    return m
+
+
+def make(orc, rng, T, k, E, H, inter, f1=0, f2=0):
+    """Inputs on the host: bf16 x, indices, weights, codes and factors; the fp64
+    weights they stand for."""
+    d = {"x": workloads.bf16_bits(rng.standard_normal((T, H)).astype(np.float32)),
+         "idx": np.stack([rng.permutation(E)[:k] if k <= E else rng.integers(0, E, k) for _ in range(T)]).astype(
+             np.int32).reshape(T, k),
+         "w": rng.uniform(-1, 1, (T, k)).astype(np.float32)}
+    for name, fmt, rows, cols in (("w1", f1, 2 * inter, H), ("w2", f2, H, inter)):
+        b = workloads.bf16_bits(rng.standard_normal((E * rows, cols)).astype(np.float32) / np.sqrt(cols))
+        q, si, _ = orc.quantize_row(b, fmt)
+        d[name], d["s" + name] = q.reshape(E, rows, cols), si.reshape(E, rows)
+        d["v" + name] = (orc.decode(fmt, q).astype(np.float64) * si.astype(np.float64)[:, None]).reshape(E, rows, cols)
+    return d
+
+
+def call(fp8, d, f1=0, f2=0, out=None, ws=None, w1=None, w2=None):
+    T, H = d["x"].shape
+    k, inter = d["idx"].shape[1], d["w2"].shape[2]
+    if out is None:
+        out = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ws = fp8.moe_few_workspace(T, k, inter) if ws is None else ws
+    fp8.fp8_moe_few_tokens(dev_bf16(d["x"]), torch.from_numpy(d["idx"]).to(DEV), dev_f32(d["w"]),
+                           dev_u8(d["w1"]) if w1 is None else w1, f1, dev_f32(d["sw1"]),
+                           dev_u8(d["w2"]) if w2 is None else w2, f2, dev_f32(d["sw2"]), out, ws)
+    torch.cuda.synchronize()
+    return out
+
+
+def check(d, out, what):
+    want, tol = layer.moe_few(layer.values(d["x"]), d["idx"], d["w"], d["vw1"], d["vw2"])
+    within(layer.values(host_bits(out)), want, tol * (1 + BF), what, rel=BF)
+
+
+CASES = [  # T, k, E, H, inter, f1, f2
+    (1, 1, 1, 16, 16, 0, 0), (1, 8, 32, 256, 128, 0, 0), (5, 2, 16, 1024, 512, 1, 1), (3, 2, 8, 272, 80, 0, 1),
+    (16, 4, 8, 512, 272, 1, 0), (17, 2, 4, 304, 144, 0, 0), (32, 8, 32, 256, 256, 0, 0), (33, 3, 4, 528, 64, 0, 0),
+    (64, 2, 3, 1040, 112, 0, 1), (64, 64, 64, 64, 32, 0, 0), (2, 64, 1024, 32, 16, 0, 0), (7, 3, 2, 96, 48, 0, 0),
+    (1, 2, 2, 7168, 2048, 0, 0), (4, 1, 8, 2064, 1040, 0, 0),
+]
+
+
+@pytest.mark.parametrize("T,k,E,H,inter,f1,f2", CASES)
+def test_moe_few_parity(fp8, orc, T, k, E, H, inter, f1, f2):
+    rng = np.random.default_rng(T * 5 + H)
+    d = make(orc, rng, T, k, E, H, inter, f1, f2)
+    out, buf, o = guarded(T, H, torch.bfloat16)
+    n = T * k * inter
+    ws = torch.full((n + 64,), 5.0, device=DEV)
+    say("moe few", T, k, E, H, inter, f1, f2)
+    call(fp8, d, f1, f2, out, ws[:n])
+    check(d, out, "out")
+    check_guard(buf, o, T, H)
+    assert (ws[n:] == 5.0).all(), "writes past the workspace"
+    # the same bits whatever the workspace held before
+    again = call(fp8, d, f1, f2, ws=torch.full((n,), float("nan"), device=DEV))
+    assert torch.equal(again, out)
+
+
+def test_moe_few_every_code(fp8, orc):
+    """Every finite code of both formats decodes exactly: one-hot tokens read the
+    columns of W1 = all codes back through a large gate (silu = identity)."""
+    for fmt in (0, 1):
+        table = orc.decode_table(fmt)
+        codes = np.arange(256, dtype=np.uint8)
+        codes = codes[np.isfinite(table)]
+        n = len(codes)
+        inter, H, T = 16, 256, 16
+        w1 = np.zeros((1, 2 * inter, H), np.uint8)
+        one = orc.encode(fmt, np.array([1.0], np.float32))[0]
+        top = orc.encode(fmt, np.array([64.0], np.float32))[0]
+        w1[0, :inter, :] = top                                          # gate 64: silu(64) = 64 in fp32
+        w1[0, inter, :n] = codes
+        w2 = np.zeros((1, H, inter), np.uint8)
+        w2[0, 0, 0] = one
+        got = []
+        for t0 in range(0, H, T):
+            x = np.zeros((T, H), np.float32)
+            x[np.arange(T), t0 + np.arange(T)] = 1.0
+            d = {"x": workloads.bf16_bits(x), "idx": np.zeros((T, 1), np.int32), "w": np.full((T, 1), 1 / 64, np.float32),
+                 "w1": w1, "w2": w2, "sw1": np.ones((1, 2 * inter), np.float32), "sw2": np.ones((1, H), np.float32)}
+            say("moe few codes", fmt, t0)
+            got.append(call(fp8, d, fmt, fmt).float().cpu().numpy()[:, 0])
+        got = np.concatenate(got)[:n]
+        assert np.array_equal(got.astype(np.float64), table[codes].astype(np.float64))
+
+
+def test_moe_few_indices(fp8, orc):
+    """Indices out of range add nothing (a token with no valid one gets zeros), an
+    expert named twice counts with both weights."""
+    rng = np.random.default_rng(11)
+    d = make(orc, rng, 9, 3, 5, 128, 64)
+    d["idx"][0] = [-1, 5, 1 << 30]
+    d["idx"][1] = [2, 2, 2]
+    d["idx"][2] = [4, -7, 4]
+    d["idx"][3] = [0, 1, 0]
+    say("moe few indices")
+    out = call(fp8, d)
+    check(d, out, "out")
+    assert not out[0].any()
+    # no valid index at all
+    d["idx"][:] = -1
+    assert not call(fp8, d).any()
+
+
+def test_moe_few_nan_stays_in_its_token(fp8, orc):
+    """A NaN in one token's row and a NaN code in one expert's W1 and another's W2
+    reach the tokens that use them and no others, for every tile of tokens."""
+    rng = np.random.default_rng(12)
+    T, k, E, H, inter = 40, 2, 6, 128, 64
+    d = make(orc, rng, T, k, E, H, inter)
+    say("moe few NaN")
+    clean = call(fp8, d).float().cpu().numpy()
+    d["x"][7, 3] = 0x7FC0
+    d["w1"][1, 5, 9] = 0x7F
+    d["w2"][2, 3, 4] = 0x7F
+    got = call(fp8, d).float().cpu().numpy()
+    uses1 = (d["idx"] == 1).any(1)
+    uses1[7] = True
+    uses2 = (d["idx"] == 2).any(1)
+    assert np.isnan(got[uses1]).all()
+    assert np.isnan(got[uses2 & ~uses1, 3]).all()
+    rest = np.ones_like(got, bool)
+    rest[uses1] = False
+    rest[uses2, 3] = False
+    assert np.array_equal(got[rest], clean[rest])
+
+
+def test_moe_few_strided_operands(fp8, orc):
+    """x and out as columns of wider tensors, weights with padded rows, experts
+    apart or shared (stride 0): the same bits as contiguous ones."""
+    rng = np.random.default_rng(13)
+    T, k, E, H, inter = 6, 2, 4, 160, 96
+    d = make(orc, rng, T, k, E, H, inter)
+    say("moe few strides")
+    want = call(fp8, d)
+    w1 = torch.zeros((E, 2 * inter + 3, H + 16), dtype=torch.uint8, device=DEV)
+    w1[:, :2 * inter, :H] = dev_u8(d["w1"])
+    w2 = torch.zeros((E, H, inter + 32), dtype=torch.uint8, device=DEV)
+    w2[:, :, :inter] = dev_u8(d["w2"])
+    got = call(fp8, d, w1=w1[:, :2 * inter, :H], w2=w2[:, :, :inter])
+    assert torch.equal(got, want)
+    shared = dict(d, w1=np.repeat(d["w1"][:1], E, 0), w2=np.repeat(d["w2"][:1], E, 0))
+    a = call(fp8, shared)
+    b = call(fp8, shared, w1=dev_u8(d["w1"][:1]).expand(E, -1, -1), w2=dev_u8(d["w2"][:1]).expand(E, -1, -1))
+    assert torch.equal(a, b)
+
+
+def test_moe_few_token_alone(fp8, orc):
+    """A token's result does not depend on the other tokens of the call beyond the
+    order of the experts' sums: alone and in a batch of 20 both are within the bound."""
+    rng = np.random.default_rng(14)
+    d = make(orc, rng, 20, 2, 8, 256, 128)
+    say("moe few alone")
+    check(d, call(fp8, d), "batch")
+    one = dict(d, x=d["x"][3:4], idx=d["idx"][3:4].copy(), w=d["w"][3:4].copy())
+    check(one, call(fp8, one), "alone")
+
+
+def test_moe_few_no_tokens(fp8):
+    say("moe few empty")
+    z = torch.empty((0, 32), dtype=torch.bfloat16, device=DEV)
+    fp8.fp8_moe_few_tokens(z, torch.empty((0, 2), dtype=torch.int32, device=DEV), torch.empty((0, 2), device=DEV),
+                           torch.zeros((2, 32, 32), dtype=torch.uint8, device=DEV), 0, torch.ones((2, 32), device=DEV),
+                           torch.zeros((2, 32, 16), dtype=torch.uint8, device=DEV), 0, torch.ones((2, 32), device=DEV),
+                           z, fp8.moe_few_workspace(0, 2, 16))
+    torch.cuda.synchronize()
+
+
+def test_moe_few_in_graphs(fp8, orc):
+    """Captured and replayed: two graphs that share a workspace, replayed in turn with
+    eager calls and new inputs in the same buffers between, give the eager bits."""
+    rng = np.random.default_rng(15)
+    T, k, E, H, inter = 4, 2, 6, 256, 128
+    d = make(orc, rng, T, k, E, H, inter)
+    x, idx, w = dev_bf16(d["x"]), torch.from_numpy(d["idx"]).to(DEV), dev_f32(d["w"])
+    w1, s1, w2, s2 = dev_u8(d["w1"]), dev_f32(d["sw1"]), dev_u8(d["w2"]), dev_f32(d["sw2"])
+    ws = fp8.moe_few_workspace(T, k, inter)
+    outs = [torch.empty((T, H), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    say("moe few graphs")
+
+    def run(n, out, ws):
+        fp8.fp8_moe_few_tokens(x[:n], idx[:n], w[:n], w1, 0, s1, w2, 0, s2, out[:n], ws)
+
+    sizes = (4, 1)
+    for n, o in zip(sizes, outs):
+        run(n, o, ws)
+    torch.cuda.synchronize()
+    graphs = []
+    for n, o in zip(sizes, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(n, o, ws)
+        graphs.append(g)
+    for it in range(4):
+        x.copy_(dev_bf16(workloads.bf16_bits(rng.standard_normal((T, H)).astype(np.float32))))
+        idx.copy_(torch.from_numpy(np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)))
+        for o in outs:
+            o.fill_(float("nan"))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for n, o in zip(sizes, outs):
+            eager = torch.empty_like(o)
+            run(n, eager, fp8.moe_few_workspace(T, k, inter))
+            torch.cuda.synchronize()
+            assert torch.equal(o[:n], eager[:n]), (it, n)
