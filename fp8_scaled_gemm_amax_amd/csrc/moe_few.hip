@@ -56,13 +56,34 @@ __device__ __forceinline__ v4f mfma(v8bf a, v8bf b, v4f c) {
 constexpr int kStep = 64;                   // bytes of a weight row per load of a wavefront
 constexpr int kMaxWords = kMoeMaxExperts / 32;
 
-// Bitmap of the experts that some entry names, in LDS (all threads).
-__device__ __forceinline__ void mark_experts(const MoeFew& p, uint32_t* bits) {
+__device__ __forceinline__ uint4 load_weights(const uint8_t* p) {
+    return load_stream(reinterpret_cast<const uint4*>(p));
+}
+__device__ __forceinline__ v8bf load_acts(const uint16_t* p) {
+    return __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(p));
+}
+// The same where `in`, zeros elsewhere (nothing is read there).
+__device__ __forceinline__ uint4 load_weights_if(bool in, const uint8_t* p) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (in) v = load_weights(p);
+    return v;
+}
+__device__ __forceinline__ v8bf load_acts_if(bool in, const uint16_t* p) {
+    v4u v = {0u, 0u, 0u, 0u};
+    if (in) v = *reinterpret_cast<const v4u*>(p);
+    return __builtin_bit_cast(v8bf, v);
+}
+
+// Copies the entries' experts to LDS (-1 for one out of range) and sets the bits
+// of those named (all threads; ends with a barrier).
+__device__ __forceinline__ void read_entries(const MoeFew& p, int16_t* idx, uint32_t* bits) {
     for (int i = threadIdx.x; i < kMaxWords; i += blockDim.x) bits[i] = 0u;
     __syncthreads();
     for (int i = threadIdx.x; i < p.tokens * p.topk; i += blockDim.x) {
         const int e = p.idx[i];
-        if (e >= 0 && e < p.experts) atomicOr(&bits[e >> 5], 1u << (e & 31));
+        const bool valid = e >= 0 && e < p.experts;
+        idx[i] = (int16_t)(valid ? e : -1);
+        if (valid) atomicOr(&bits[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
 }
@@ -74,83 +95,91 @@ __device__ __forceinline__ int words_below(uint32_t word, int* total) {
     const int pc = lane < kMaxWords ? __popc(word) : 0;
     int incl = pc;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
+    for (int o = 1; o < kMaxWords; o <<= 1) {
         const int y = __shfl_up(incl, o, 64);
         if (lane >= o) incl += y;
     }
-    *total = __shfl(incl, 63, 64);
+    *total = __shfl(incl, kMaxWords - 1, 64);
     return incl - pc;
 }
 
-// Token `lane`'s first slot that names expert e, -1 if none; the sum of the
-// weights of all its slots that do in *share.
-__device__ __forceinline__ int token_slot(const MoeFew& p, int e, float* share) {
+// The tokens of one expert, in token order, lane r holding the r-th: token |
+// (its first slot that names the expert) << 8. Lanes past count hold other
+// tokens' numbers.
+struct Entries {
+    int item, count;
+    __device__ __forceinline__ int token(int r) const { return __shfl(item, r, 64) & 0xff; }
+    __device__ __forceinline__ int slot(int r) const { return __shfl(item, r, 64) >> 8; }
+};
+__device__ __forceinline__ Entries find_entries(const MoeFew& p, const int16_t* idx, int e) {
     const int t = threadIdx.x & 63;
     int first = -1;
-    float s = 0.0f;
     if (t < p.tokens)
-        for (int j = 0; j < p.topk; ++j) {
-            const int i = t * p.topk + j;
-            if (p.idx[i] != e) continue;
-            if (share) s += p.weights[i];
-            if (first < 0) first = j;
-        }
-    if (share) *share = s;
-    return first;
-}
-
-__device__ __forceinline__ uint4 load_weights(const uint8_t* p) {
-    return load_stream(reinterpret_cast<const uint4*>(p));
-}
-// The same where `in`, zeros elsewhere (nothing is read there).
-__device__ __forceinline__ uint4 load_weights_if(bool in, const uint8_t* p) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (in) v = load_weights(p);
-    return v;
-}
-__device__ __forceinline__ v8bf load_bf16x8_if(bool in, const uint16_t* p) {
-    v4u v = {0u, 0u, 0u, 0u};
-    if (in) v = *reinterpret_cast<const v4u*>(p);
-    return __builtin_bit_cast(v8bf, v);
+        for (int j = p.topk - 1; j >= 0; --j) first = idx[t * p.topk + j] == e ? j : first;
+    const uint64_t has = __ballot(first >= 0), below = (1ull << t) - 1ull;
+    Entries en;
+    en.count = __popcll(has);
+    const int to = first >= 0 ? __popcll(has & below) : en.count + __popcll(~has & below);
+    en.item = __builtin_amdgcn_ds_permute(4 * to, t | ((first < 0 ? 0 : first) << 8));
+    return en;
 }
 
 // ------------------------------------------------------------- gate and up --
 // Workgroup (tile, a): 16 columns of the a-th expert in use. Its wavefronts
-// split K in blocks of kStep * U bytes, and their sums meet in LDS.
+// split K in blocks of kStep * U bytes, and their sums meet in LDS. The next
+// block's weights are on their way while a block is multiplied; the tokens'
+// values (from L2) are asked for before them, since loads return in order.
 constexpr int kUpWaves = 4;
 
 // Sums of 16 gate rows and 16 up rows against the tokens of tiles 0 .. NT-1
 // (NT * 16 entries) over this wavefront's share of K.
 template <int F, int NT, int U>
-__device__ __forceinline__ void up_sums(const MoeFew& p, const uint8_t* gp, const uint8_t* up, const uint16_t* const* xp,
-                                        int wave, v4f* ag, v4f* au) {
+__device__ __forceinline__ void up_sums(const uint8_t* gp, const uint8_t* up, const uint16_t* const* xp, int K, int wave,
+                                        v4f* ag, v4f* au) {
     const int j16 = ((threadIdx.x & 63) >> 4) * 16;
-    const int K = p.hidden, whole = K / (kStep * U);
-    for (int b = wave; b < whole; b += kUpWaves) {
-        const int k0 = b * (kStep * U) + j16;
-        uint4 g[U], u[U], x[NT][U][2];
+    const int whole = K / (kStep * U);
+    uint4 g[U], u[U];
+    if (wave < whole) {
 #pragma unroll
         for (int s = 0; s < U; ++s) {
-            g[s] = load_weights(gp + k0 + s * kStep);
-            u[s] = load_weights(up + k0 + s * kStep);
+            g[s] = load_weights(gp + wave * (kStep * U) + j16 + s * kStep);
+            u[s] = load_weights(up + wave * (kStep * U) + j16 + s * kStep);
+        }
+    }
+    for (int b = wave; b < whole; b += kUpWaves) {
+        const int k0 = b * (kStep * U) + j16;
+        const int kn = k0 + kUpWaves * (kStep * U);
+        v8bf x[NT][U][2];
+        uint4 gn[U], un[U];
+#pragma unroll
+        for (int s = 0; s < U; ++s)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                x[n][s][0] = *reinterpret_cast<const uint4*>(xp[n] + k0 + s * kStep);
-                x[n][s][1] = *reinterpret_cast<const uint4*>(xp[n] + k0 + s * kStep + 8);
+                x[n][s][0] = load_acts(xp[n] + k0 + s * kStep);
+                x[n][s][1] = load_acts(xp[n] + k0 + s * kStep + 8);
+            }
+        __builtin_amdgcn_sched_barrier(0);
+        if (b + kUpWaves < whole) {
+#pragma unroll
+            for (int s = 0; s < U; ++s) {
+                gn[s] = load_weights(gp + kn + s * kStep);
+                un[s] = load_weights(up + kn + s * kStep);
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int s = 0; s < U; ++s) {
             const v8bf g0 = decode_bf16<F>(g[s].x, g[s].y), g1 = decode_bf16<F>(g[s].z, g[s].w);
             const v8bf u0 = decode_bf16<F>(u[s].x, u[s].y), u1 = decode_bf16<F>(u[s].z, u[s].w);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const v8bf x0 = __builtin_bit_cast(v8bf, x[n][s][0]), x1 = __builtin_bit_cast(v8bf, x[n][s][1]);
-                ag[n] = mfma(g0, x0, ag[n]);
-                au[n] = mfma(u0, x0, au[n]);
-                ag[n] = mfma(g1, x1, ag[n]);
-                au[n] = mfma(u1, x1, au[n]);
+                ag[n] = mfma(g0, x[n][s][0], ag[n]);
+                au[n] = mfma(u0, x[n][s][0], au[n]);
+                ag[n] = mfma(g1, x[n][s][1], ag[n]);
+                au[n] = mfma(u1, x[n][s][1], au[n]);
             }
+            g[s] = gn[s];
+            u[s] = un[s];
         }
     }
     // what is left of K, 64 bytes a step, the last step's lanes past K zero on both sides
@@ -158,12 +187,12 @@ __device__ __forceinline__ void up_sums(const MoeFew& p, const uint8_t* gp, cons
     for (int st = left0 + (wave + kUpWaves - whole % kUpWaves) % kUpWaves; st < steps; st += kUpWaves) {
         const int k = st * kStep + j16;
         const bool in = k < K;
-        const uint4 g = load_weights_if(in, gp + k), u = load_weights_if(in, up + k);
-        const v8bf g0 = decode_bf16<F>(g.x, g.y), g1 = decode_bf16<F>(g.z, g.w);
-        const v8bf u0 = decode_bf16<F>(u.x, u.y), u1 = decode_bf16<F>(u.z, u.w);
+        const uint4 gl = load_weights_if(in, gp + k), ul = load_weights_if(in, up + k);
+        const v8bf g0 = decode_bf16<F>(gl.x, gl.y), g1 = decode_bf16<F>(gl.z, gl.w);
+        const v8bf u0 = decode_bf16<F>(ul.x, ul.y), u1 = decode_bf16<F>(ul.z, ul.w);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const v8bf x0 = load_bf16x8_if(in, xp[n] + k), x1 = load_bf16x8_if(in, xp[n] + k + 8);
+            const v8bf x0 = load_acts_if(in, xp[n] + k), x1 = load_acts_if(in, xp[n] + k + 8);
             ag[n] = mfma(g0, x0, ag[n]);
             au[n] = mfma(u0, x0, au[n]);
             ag[n] = mfma(g1, x1, ag[n]);
@@ -172,15 +201,9 @@ __device__ __forceinline__ void up_sums(const MoeFew& p, const uint8_t* gp, cons
     }
 }
 
-struct Entries {
-    int token[kMoeFewTokens];
-    int slot[kMoeFewTokens];
-    float share[kMoeFewTokens];
-    int count;
-};
-
 template <int F, int NT, int U>
-__device__ __forceinline__ void up_tile(const MoeFew& p, int e, int c0, const Entries& ent, float* red) {
+__device__ __forceinline__ void up_tile(const MoeFew& p, const int16_t* idx, int e, int c0, const Entries& ent,
+                                        float* red) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint8_t* we = p.w1 + (int64_t)e * p.gs1;
     const uint8_t* gp = we + (int64_t)(c0 + (lane & 15)) * p.ld1;
@@ -190,10 +213,26 @@ __device__ __forceinline__ void up_tile(const MoeFew& p, int e, int c0, const En
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int c = n * 16 + (lane & 15);
-        xp[n] = p.x + (int64_t)ent.token[c < ent.count ? c : 0] * p.ldx;     // (columns past the entries are not used)
+        xp[n] = p.x + (int64_t)ent.token(c < ent.count ? c : 0) * p.ldx;     // (columns past the entries are not used)
         ag[n] = au[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    up_sums<F, NT, U>(p, gp, up, xp, wave, ag, au);
+    // for the end: factors of the rows, and the weights of the columns' tokens
+    // (the sum over all slots of the token that name the expert)
+    const int row = threadIdx.x & 15;
+    const float sg = p.s1[(int64_t)e * 2 * p.inter + c0 + row], su = p.s1[(int64_t)e * 2 * p.inter + p.inter + c0 + row];
+    int token[NT], slot[NT];
+    float share[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int c = n * 16 + (threadIdx.x >> 4);
+        token[n] = ent.token(c);
+        slot[n] = ent.slot(c);
+        if (c >= ent.count) continue;
+        share[n] = p.weights[token[n] * p.topk + slot[n]];
+        for (int j = slot[n] + 1; j < p.topk; ++j)
+            if (idx[token[n] * p.topk + j] == e) share[n] += p.weights[token[n] * p.topk + j];
+    }
+    up_sums<F, NT, U>(gp, up, xp, p.hidden, wave, ag, au);
     // red[wave][tile][gate | up][column * 16 + row], row = 4 (lane / 16) + i
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -202,8 +241,6 @@ __device__ __forceinline__ void up_tile(const MoeFew& p, int e, int c0, const En
         *reinterpret_cast<v4f*>(r + 256) = au[n];
     }
     __syncthreads();
-    const int row = threadIdx.x & 15;
-    const float sg = p.s1[(int64_t)e * 2 * p.inter + c0 + row], su = p.s1[(int64_t)e * 2 * p.inter + p.inter + c0 + row];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int c = n * 16 + (threadIdx.x >> 4);
@@ -214,12 +251,12 @@ __device__ __forceinline__ void up_tile(const MoeFew& p, int e, int c0, const En
             g += red[((w * NT + n) * 2) * 256 + threadIdx.x];
             u += red[((w * NT + n) * 2 + 1) * 256 + threadIdx.x];
         }
-        const float a = silu_fast(g * sg) * (u * su) * ent.share[c];
+        const float a = silu_fast(g * sg) * (u * su) * share[n];
         const uint32_t hi = f32_to_bf16(a);
         const float rest = a - __uint_as_float(hi << 16);
         // (an Inf or NaN is carried by the high part alone)
         const uint32_t lo = __builtin_isfinite(a) && __builtin_isfinite(rest) ? f32_to_bf16(rest) : 0u;
-        uint16_t* dst = p.ws + ((int64_t)ent.token[c] * p.topk + ent.slot[c]) * 2 * p.inter + c0 + row;
+        uint16_t* dst = p.ws + ((int64_t)token[n] * p.topk + slot[n]) * 2 * p.inter + c0 + row;
         dst[0] = (uint16_t)hi;
         dst[p.inter] = (uint16_t)lo;
     }
@@ -228,10 +265,10 @@ __device__ __forceinline__ void up_tile(const MoeFew& p, int e, int c0, const En
 template <int F, int NTMAX>
 __global__ __launch_bounds__(kUpWaves * 64) void k_moe_few_up(MoeFew p) {
     __shared__ uint32_t bits[kMaxWords];
-    __shared__ Entries ent;
+    __shared__ int16_t idx[NTMAX * 16 * kMoeMaxTopk];
     __shared__ __attribute__((aligned(16))) float red[kUpWaves * NTMAX * 2 * 256];
     const int lane = threadIdx.x & 63;
-    mark_experts(p, bits);
+    read_entries(p, idx, bits);
     const uint32_t word = lane < kMaxWords ? bits[lane] : 0u;
     int total;
     const int below = words_below(word, &total);
@@ -241,172 +278,209 @@ __global__ __launch_bounds__(kUpWaves * 64) void k_moe_few_up(MoeFew p) {
     uint32_t w = word;
     for (int i = below; mine && i < a; ++i) w &= w - 1u;    // drop the experts before it
     const int owner = __ffsll((unsigned long long)__ballot(mine)) - 1;
-    const int e = __shfl(lane * 32 + __ffs((int)w) - 1, owner, 64);
-    float share;
-    const int slot = token_slot(p, e, &share);
-    const uint64_t has = __ballot(slot >= 0);
-    if (threadIdx.x < 64) {
-        if (slot >= 0) {
-            const int r = __popcll(has & ((1ull << lane) - 1ull));
-            ent.token[r] = lane;
-            ent.slot[r] = slot;
-            ent.share[r] = share;
-        }
-        if (lane == 0) ent.count = __popcll(has);
-    }
-    __syncthreads();
+    const int e = __builtin_amdgcn_readfirstlane(__shfl(lane * 32 + __ffs((int)w) - 1, owner, 64));
+    const Entries ent = find_entries(p, idx, e);
     const int c0 = blockIdx.x * 16;
     if constexpr (NTMAX >= 4) {
         if (ent.count > 32) {
-            up_tile<F, 4, 1>(p, e, c0, ent, red);
+            up_tile<F, 4, 2>(p, idx, e, c0, ent, red);
             return;
         }
     }
     if constexpr (NTMAX >= 2) {
         if (ent.count > 16) {
-            up_tile<F, 2, 2>(p, e, c0, ent, red);
+            up_tile<F, 2, 4>(p, idx, e, c0, ent, red);
             return;
         }
     }
-    up_tile<F, 1, 4>(p, e, c0, ent, red);
+    up_tile<F, 1, 4>(p, idx, e, c0, ent, red);
 }
 
 // -------------------------------------------------------------------- down --
-// Workgroup: 16 output columns of every token. The units of work are pieces of
-// K of the experts in use, dealt to the wavefronts in order; a wavefront adds
-// an expert's sums, times the weight rows' factors, to the sums of the tokens
-// that use the expert and to no others (the products of the others are with a
-// token's values of another expert; NaN codes do not reach them). The
-// wavefronts' sums meet in LDS and are added in order.
+// Workgroup: RT * 16 output columns of every token. The units of work are
+// pieces of K of the experts in use, dealt to the wavefronts in order. A
+// wavefront multiplies the expert's rows with the expert's tokens, 16 at a
+// time, and adds the sums, times the rows' factors, to its own sums of those
+// tokens in LDS; at the end the wavefronts' sums are added in order. A token's
+// sums are never touched by an expert that it does not use.
 constexpr int kDownWaves = 8;
 
-template <int F, int NT, int U>
+// Products of RT * 16 weight rows with the entries of tiles 0 .. NT-1 over the
+// blocks b0, b0 + db, .. of K.
+template <int F, int RT, int NT, int U>
+__device__ __forceinline__ void down_sums(const uint8_t* const* wp, const uint16_t* const* ap, int K, int b0, int db,
+                                          v4f (*acc)[NT]) {
+    const int j16 = ((threadIdx.x & 63) >> 4) * 16;
+    const int whole = K / (kStep * U);
+    uint4 w[RT][U];
+    if (b0 < whole) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int s = 0; s < U; ++s) w[r][s] = load_weights(wp[r] + b0 * (kStep * U) + s * kStep + j16);
+    }
+    int b = b0;
+    for (; b < whole; b += db) {
+        const int k0 = b * (kStep * U) + j16;
+        const int kn = k0 + db * (kStep * U);
+        v8bf a[NT][U][4];
+        uint4 wn[RT][U];
+#pragma unroll
+        for (int s = 0; s < U; ++s)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                a[n][s][0] = load_acts(ap[n] + k0 + s * kStep);
+                a[n][s][1] = load_acts(ap[n] + k0 + s * kStep + 8);
+                a[n][s][2] = load_acts(ap[n] + K + k0 + s * kStep);
+                a[n][s][3] = load_acts(ap[n] + K + k0 + s * kStep + 8);
+            }
+        __builtin_amdgcn_sched_barrier(0);
+        if (b + db < whole) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int s = 0; s < U; ++s) wn[r][s] = load_weights(wp[r] + kn + s * kStep);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < U; ++s)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const v8bf w0 = decode_bf16<F>(w[r][s].x, w[r][s].y), w1 = decode_bf16<F>(w[r][s].z, w[r][s].w);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    acc[r][n] = mfma(w0, a[n][s][0], acc[r][n]);
+                    acc[r][n] = mfma(w1, a[n][s][1], acc[r][n]);
+                    acc[r][n] = mfma(w0, a[n][s][2], acc[r][n]);
+                    acc[r][n] = mfma(w1, a[n][s][3], acc[r][n]);
+                }
+                w[r][s] = wn[r][s];
+            }
+    }
+    if (b * (kStep * U) >= K) return;                       // (the last, partial block is this wavefront's or another's)
+    for (int k = b * (kStep * U) + j16; k - j16 < K; k += kStep) {
+        const bool in = k < K;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const uint4 wl = load_weights_if(in, wp[r] + k);
+            const v8bf w0 = decode_bf16<F>(wl.x, wl.y), w1 = decode_bf16<F>(wl.z, wl.w);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                acc[r][n] = mfma(w0, load_acts_if(in, ap[n] + k), acc[r][n]);
+                acc[r][n] = mfma(w1, load_acts_if(in, ap[n] + k + 8), acc[r][n]);
+                acc[r][n] = mfma(w0, load_acts_if(in, ap[n] + K + k), acc[r][n]);
+                acc[r][n] = mfma(w1, load_acts_if(in, ap[n] + K + k + 8), acc[r][n]);
+            }
+        }
+    }
+}
+
+// One unit for NT tiles of entries; sums: this wavefront's [token][RT * 16].
+template <int F, int RT, int NT, int U>
+__device__ __forceinline__ void down_unit(const MoeFew& p, int e, int row0, const Entries& ent, int b0, int db,
+                                          float* sums) {
+    const int lane = threadIdx.x & 63;
+    const uint8_t* we = p.w2 + (int64_t)e * p.gs2;
+    const uint8_t* wp[RT];
+    const uint16_t* ap[NT];
+    v4f acc[RT][NT], sc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        wp[r] = we + (int64_t)(row0 + r * 16 + (lane & 15)) * p.ld2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[r][i] = p.s2[(int64_t)e * p.hidden + row0 + r * 16 + (lane >> 4) * 4 + i];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[r][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int c = n * 16 + (lane & 15), cc = c < ent.count ? c : 0;      // (columns past the entries are not used)
+        ap[n] = p.ws + ((int64_t)ent.token(cc) * p.topk + ent.slot(cc)) * 2 * p.inter;
+    }
+    down_sums<F, RT, NT, U>(wp, ap, p.inter, b0, db, acc);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int c = n * 16 + (lane & 15);
+        const int t = ent.token(c);
+        if (c >= ent.count) continue;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            v4f* d = reinterpret_cast<v4f*>(sums + t * (RT * 16) + r * 16 + (lane >> 4) * 4);
+            v4f v = *d;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = fmaf(acc[r][n][i], sc[r][i], v[i]);
+            *d = v;
+        }
+    }
+}
+
+// TT: the tokens, rounded up to 16, 32 or 64.
+template <int F, int RT, int TT>
 __global__ __launch_bounds__(kDownWaves * 64) void k_moe_few_down(MoeFew p) {
+    constexpr int W = TT * RT * 16;                          // a wavefront's sums
     __shared__ uint32_t bits[kMaxWords];
+    __shared__ int16_t idx[TT * kMoeMaxTopk];
     __shared__ uint16_t list[kMoeMaxExperts];
-    __shared__ __attribute__((aligned(16))) float red[kDownWaves * NT * 256];
+    __shared__ __attribute__((aligned(16))) float red[kDownWaves * W];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    mark_experts(p, bits);
+    for (int i = threadIdx.x; i < kDownWaves * W; i += kDownWaves * 64) red[i] = 0.0f;
+    read_entries(p, idx, bits);
     uint32_t word = lane < kMaxWords ? bits[lane] : 0u;
     int total;
     int at = words_below(word, &total);
     if (wave == 0)
         for (; word; word &= word - 1u) list[at++] = (uint16_t)(lane * 32 + __ffs((int)word) - 1);
     __syncthreads();
-    const int row0 = blockIdx.x * 16, K = p.inter, j16 = (lane >> 4) * 16;
-    const int blocks = (K + kStep * U - 1) / (kStep * U);
+    const int row0 = blockIdx.x * (RT * 16);
+    const int blocks = (p.inter + 4 * kStep - 1) / (4 * kStep);
     int pieces = total > 0 ? kDownWaves / total : 1;
     pieces = pieces < 1 ? 1 : (pieces > blocks ? blocks : pieces);
-    v4f sum[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) sum[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    float* sums = red + wave * W;
     for (int unit = wave; unit < total * pieces; unit += kDownWaves) {
-        const int e = list[unit / pieces];
-        const int slot = token_slot(p, e, nullptr);         // of token `lane`
-        const uint64_t has = __ballot(slot >= 0);
-        const int any = __ffsll((unsigned long long)has) - 1;   // a token that uses it (there is one)
-        const uint16_t* ap[NT];
-        bool used[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int t = n * 16 + (lane & 15);
-            used[n] = (has >> t) & 1ull;
-            const int src = used[n] ? t : any;
-            ap[n] = p.ws + ((int64_t)src * p.topk + __shfl(slot, src, 64)) * 2 * K;
-        }
-        const uint8_t* wp = p.w2 + (int64_t)e * p.gs2 + (int64_t)(row0 + (lane & 15)) * p.ld2;
-        const float* sp = p.s2 + (int64_t)e * p.hidden + row0 + (lane >> 4) * 4;
-        v4f acc[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int b = unit % pieces; b < blocks; b += pieces) {
-            const int kb = b * (kStep * U);
-            if (kb + kStep * U <= K) {
-                uint4 w[U];
-#pragma unroll
-                for (int s = 0; s < U; ++s) w[s] = load_weights(wp + kb + s * kStep + j16);
-#pragma unroll
-                for (int s = 0; s < U; ++s) {
-                    const int k = kb + s * kStep + j16;
-                    const v8bf w0 = decode_bf16<F>(w[s].x, w[s].y), w1 = decode_bf16<F>(w[s].z, w[s].w);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const v8bf* hi = reinterpret_cast<const v8bf*>(ap[n] + k);
-                        const v8bf* lo = reinterpret_cast<const v8bf*>(ap[n] + K + k);
-                        acc[n] = mfma(w0, hi[0], acc[n]);
-                        acc[n] = mfma(w0, lo[0], acc[n]);
-                        acc[n] = mfma(w1, hi[1], acc[n]);
-                        acc[n] = mfma(w1, lo[1], acc[n]);
-                    }
-                }
-            } else {
-                for (int k = kb + j16; k - j16 < K; k += kStep) {
-                    const bool in = k < K;
-                    const uint4 w = load_weights_if(in, wp + k);
-                    const v8bf w0 = decode_bf16<F>(w.x, w.y), w1 = decode_bf16<F>(w.z, w.w);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        acc[n] = mfma(w0, load_bf16x8_if(in, ap[n] + k), acc[n]);
-                        acc[n] = mfma(w0, load_bf16x8_if(in, ap[n] + K + k), acc[n]);
-                        acc[n] = mfma(w1, load_bf16x8_if(in, ap[n] + k + 8), acc[n]);
-                        acc[n] = mfma(w1, load_bf16x8_if(in, ap[n] + K + k + 8), acc[n]);
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float s = sp[i];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) sum[n][i] = used[n] ? fmaf(acc[n][i], s, sum[n][i]) : sum[n][i];
-        }
+        const int e = __builtin_amdgcn_readfirstlane(list[unit / pieces]);
+        const Entries ent = find_entries(p, idx, e);
+        if (TT > 32 && ent.count > 32) down_unit<F, RT, 4, 1>(p, e, row0, ent, unit % pieces, pieces, sums);
+        else if (TT > 16 && ent.count > 16) down_unit<F, RT, 2, 2>(p, e, row0, ent, unit % pieces, pieces, sums);
+        else down_unit<F, RT, 1, 4>(p, e, row0, ent, unit % pieces, pieces, sums);
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-        *reinterpret_cast<v4f*>(red + (wave * NT + n) * 256 + (lane & 15) * 16 + (lane >> 4) * 4) = sum[n];
     __syncthreads();
-    for (int i = threadIdx.x; i < NT * 256; i += kDownWaves * 64) {
-        const int n = i >> 8, t = n * 16 + ((i & 255) >> 4), row = i & 15;
-        if (t >= p.tokens) continue;
+    for (int i = threadIdx.x; i < p.tokens * (RT * 16); i += kDownWaves * 64) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kDownWaves; ++w) s += red[(w * NT + n) * 256 + (i & 255)];
-        p.out[(int64_t)t * p.ldo + row0 + row] = (uint16_t)f32_to_bf16(s);
+        for (int w = 0; w < kDownWaves; ++w) s += red[w * W + i];
+        p.out[(int64_t)(i / (RT * 16)) * p.ldo + row0 + i % (RT * 16)] = (uint16_t)f32_to_bf16(s);
     }
 }
 
 }  // namespace
 
+template <int F>
+hipError_t moe_few_up(const MoeFew& p, hipStream_t st) {
+    const int entries = p.tokens * p.topk;
+    const dim3 grid((unsigned)(p.inter / 16), (unsigned)(entries < p.experts ? entries : p.experts));
+    const dim3 block(kUpWaves * 64);
+    if (p.tokens <= 16) hipLaunchKernelGGL((k_moe_few_up<F, 1>), grid, block, 0, st, p);
+    else if (p.tokens <= 32) hipLaunchKernelGGL((k_moe_few_up<F, 2>), grid, block, 0, st, p);
+    else hipLaunchKernelGGL((k_moe_few_up<F, 4>), grid, block, 0, st, p);
+    return hipGetLastError();
+}
+
+template <int F, int RT>
+hipError_t moe_few_down(const MoeFew& p, hipStream_t st) {
+    const dim3 grid((unsigned)(p.hidden / (RT * 16))), block(kDownWaves * 64);
+    if (p.tokens <= 16) hipLaunchKernelGGL((k_moe_few_down<F, RT, 16>), grid, block, 0, st, p);
+    else if (p.tokens <= 32) hipLaunchKernelGGL((k_moe_few_down<F, RT, 32>), grid, block, 0, st, p);
+    else hipLaunchKernelGGL((k_moe_few_down<F, RT, 64>), grid, block, 0, st, p);
+    return hipGetLastError();
+}
+
 hipError_t launch_moe_few_tokens(const MoeFew& p, int f1, int f2, hipStream_t st) {
     if (p.tokens == 0) return hipSuccess;
-    const int entries = p.tokens * p.topk;
-    const dim3 gu((unsigned)(p.inter / 16), (unsigned)(entries < p.experts ? entries : p.experts));
-    const dim3 gd((unsigned)(p.hidden / 16));
-#define FP8_UP(F, N) hipLaunchKernelGGL((k_moe_few_up<F, N>), gu, dim3(kUpWaves * 64), 0, st, p)
-#define FP8_DOWN(F, N, U) hipLaunchKernelGGL((k_moe_few_down<F, N, U>), gd, dim3(kDownWaves * 64), 0, st, p)
-    if (f1 == kE4M3) {
-        if (p.tokens <= 16) FP8_UP(kE4M3, 1);
-        else if (p.tokens <= 32) FP8_UP(kE4M3, 2);
-        else FP8_UP(kE4M3, 4);
-    } else {
-        if (p.tokens <= 16) FP8_UP(kE5M2, 1);
-        else if (p.tokens <= 32) FP8_UP(kE5M2, 2);
-        else FP8_UP(kE5M2, 4);
-    }
-    hipError_t e = hipGetLastError();
+    const hipError_t e = f1 == kE4M3 ? moe_few_up<kE4M3>(p, st) : moe_few_up<kE5M2>(p, st);
     if (e != hipSuccess) return e;
-    if (f2 == kE4M3) {
-        if (p.tokens <= 16) FP8_DOWN(kE4M3, 1, 4);
-        else if (p.tokens <= 32) FP8_DOWN(kE4M3, 2, 4);
-        else FP8_DOWN(kE4M3, 4, 2);
-    } else {
-        if (p.tokens <= 16) FP8_DOWN(kE5M2, 1, 4);
-        else if (p.tokens <= 32) FP8_DOWN(kE5M2, 2, 4);
-        else FP8_DOWN(kE5M2, 4, 2);
-    }
-#undef FP8_UP
-#undef FP8_DOWN
-    return hipGetLastError();
+    const bool wide = p.hidden % 32 == 0 && p.hidden >= 32 * 160;
+    if (f2 == kE4M3) return wide ? moe_few_down<kE4M3, 2>(p, st) : moe_few_down<kE4M3, 1>(p, st);
+    return wide ? moe_few_down<kE5M2, 2>(p, st) : moe_few_down<kE5M2, 1>(p, st);
 }
 
 }  // namespace fp8amax
