@@ -56,8 +56,11 @@ __device__ __forceinline__ v4f mfma(v8bf a, v8bf b, v4f c) {
 constexpr int kStep = 64;                   // bytes of a weight row per load of a wavefront
 constexpr int kMaxWords = kMoeMaxExperts / 32;
 
+// (Through the caches: a row's 64 bytes of one step and of the next share a
+// line, which a nontemporal load does not keep; 32 tokens, 32 experts of 7168 x
+// 2048: 384 us with nontemporal loads, 334 us without.)
 __device__ __forceinline__ uint4 load_weights(const uint8_t* p) {
-    return load_stream(reinterpret_cast<const uint4*>(p));
+    return *reinterpret_cast<const uint4*>(p);
 }
 __device__ __forceinline__ v8bf load_acts(const uint16_t* p) {
     return __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(p));
@@ -104,53 +107,87 @@ __device__ __forceinline__ int words_below(uint32_t word, int* total) {
 }
 
 // The tokens of one expert, in token order, lane r holding the r-th: token |
-// (its first slot that names the expert) << 8. Lanes past count hold other
-// tokens' numbers.
+// (its first slot that names the expert) << 8; lanes past count hold other
+// tokens' numbers. base: the entries of the experts before it.
 struct Entries {
-    int item, count;
+    int item, count, base;
     __device__ __forceinline__ int token(int r) const { return __shfl(item, r, 64) & 0xff; }
     __device__ __forceinline__ int slot(int r) const { return __shfl(item, r, 64) >> 8; }
 };
 __device__ __forceinline__ Entries find_entries(const MoeFew& p, const int16_t* idx, int e) {
     const int t = threadIdx.x & 63;
-    int first = -1;
+    int first = -1, before = 0;
     if (t < p.tokens)
-        for (int j = p.topk - 1; j >= 0; --j) first = idx[t * p.topk + j] == e ? j : first;
+        for (int j = p.topk - 1; j >= 0; --j) {
+            const int i = idx[t * p.topk + j];
+            first = i == e ? j : first;
+            before += (unsigned)i < (unsigned)e ? 1 : 0;    // (-1 is above every expert)
+        }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) before += __shfl_xor(before, o, 64);
     const uint64_t has = __ballot(first >= 0), below = (1ull << t) - 1ull;
     Entries en;
+    en.base = __builtin_amdgcn_readfirstlane(before);
     en.count = __popcll(has);
     const int to = first >= 0 ? __popcll(has & below) : en.count + __popcll(~has & below);
     en.item = __builtin_amdgcn_ds_permute(4 * to, t | ((first < 0 ? 0 : first) << 8));
     return en;
 }
 
+// The workspace between the two launches: an expert's activations as the down
+// product loads them. Tile n of an expert (16 of its tokens, w of them there)
+// has 2 * inter * w values from (base + 16 n) * 2 * inter on; its step kb of 64
+// values of K has w * 128 of them, as [high | low][half h][group j][token][8]
+// for K = 64 kb + 16 j + 8 h + 0..7: one load of a wavefront (a lane's token and
+// group) is 16 w * 4 consecutive bytes. (Rows of K per token instead made every
+// such load 16 lines: 32 tokens, 32 experts of 7168 x 2048: the down product 150
+// us, without its loads of activations 86.) The last step of K has K / 16 % 4
+// groups. The number of entries in a tile and the tiles of the experts before
+// it add up to at most tokens * topk rows of 2 * inter values.
+struct ActTile {
+    uint16_t* base;
+    int w, inter;
+    __device__ __forceinline__ void set(const MoeFew& p, const Entries& en, int n) {
+        w = en.count - n * 16 < 16 ? en.count - n * 16 : 16;
+        w = w < 1 ? 1 : w;                                  // (no tokens: not used)
+        inter = p.inter;
+        base = p.ws + (int64_t)(en.base + n * 16) * 2 * p.inter;
+    }
+    // values from the start of step kb, part q = 2 * low + half, group j, of column c
+    __device__ __forceinline__ int offset(int kb, int q, int j, int c) const {
+        const int left = inter / 16 - kb * 4, groups = left < 4 ? left : 4;
+        return kb * 128 * w + ((q * groups + j) * w + c) * 8;
+    }
+};
+
 // ------------------------------------------------------------- gate and up --
-// Workgroup (tile, a): 16 columns of the a-th expert in use. Its wavefronts
-// split K in blocks of kStep * U bytes, and their sums meet in LDS. The next
-// block's weights are on their way while a block is multiplied; the tokens'
-// values (from L2) are asked for before them, since loads return in order.
+// Workgroup (tile, a): RT * 16 columns of the a-th expert in use. Its
+// wavefronts split K in blocks of kStep * U bytes, and their sums meet in LDS.
+// The next block's weights are on their way while a block is multiplied; the
+// tokens' values (from L2) are asked for before them, since loads return in
+// order. A load of the tokens' values (16 rows, 64 bytes of each) costs the
+// caches as much as one of weights: with two row tiles it serves four of them.
 constexpr int kUpWaves = 4;
 
-// Sums of 16 gate rows and 16 up rows against the tokens of tiles 0 .. NT-1
-// (NT * 16 entries) over this wavefront's share of K.
-template <int F, int NT, int U>
-__device__ __forceinline__ void up_sums(const uint8_t* gp, const uint8_t* up, const uint16_t* const* xp, int K, int wave,
-                                        v4f* ag, v4f* au) {
+// Sums of 2 RT tiles of weight rows (gate and up) against the tokens of tiles
+// 0 .. NT-1 (NT * 16 entries) over this wavefront's share of K.
+template <int F, int RT, int NT, int U>
+__device__ __forceinline__ void up_sums(const uint8_t* const* wp, const uint16_t* const* xp, int K, int wave,
+                                        v4f (*acc)[NT]) {
     const int j16 = ((threadIdx.x & 63) >> 4) * 16;
     const int whole = K / (kStep * U);
-    uint4 g[U], u[U];
+    uint4 w[2 * RT][U];
     if (wave < whole) {
 #pragma unroll
-        for (int s = 0; s < U; ++s) {
-            g[s] = load_weights(gp + wave * (kStep * U) + j16 + s * kStep);
-            u[s] = load_weights(up + wave * (kStep * U) + j16 + s * kStep);
-        }
+        for (int s = 0; s < U; ++s)
+#pragma unroll
+            for (int r = 0; r < 2 * RT; ++r) w[r][s] = load_weights(wp[r] + wave * (kStep * U) + j16 + s * kStep);
     }
     for (int b = wave; b < whole; b += kUpWaves) {
         const int k0 = b * (kStep * U) + j16;
         const int kn = k0 + kUpWaves * (kStep * U);
         v8bf x[NT][U][2];
-        uint4 gn[U], un[U];
+        uint4 wn[2 * RT][U];
 #pragma unroll
         for (int s = 0; s < U; ++s)
 #pragma unroll
@@ -161,112 +198,117 @@ __device__ __forceinline__ void up_sums(const uint8_t* gp, const uint8_t* up, co
         __builtin_amdgcn_sched_barrier(0);
         if (b + kUpWaves < whole) {
 #pragma unroll
-            for (int s = 0; s < U; ++s) {
-                gn[s] = load_weights(gp + kn + s * kStep);
-                un[s] = load_weights(up + kn + s * kStep);
-            }
+            for (int s = 0; s < U; ++s)
+#pragma unroll
+                for (int r = 0; r < 2 * RT; ++r) wn[r][s] = load_weights(wp[r] + kn + s * kStep);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int s = 0; s < U; ++s) {
-            const v8bf g0 = decode_bf16<F>(g[s].x, g[s].y), g1 = decode_bf16<F>(g[s].z, g[s].w);
-            const v8bf u0 = decode_bf16<F>(u[s].x, u[s].y), u1 = decode_bf16<F>(u[s].z, u[s].w);
+        for (int s = 0; s < U; ++s)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                ag[n] = mfma(g0, x[n][s][0], ag[n]);
-                au[n] = mfma(u0, x[n][s][0], au[n]);
-                ag[n] = mfma(g1, x[n][s][1], ag[n]);
-                au[n] = mfma(u1, x[n][s][1], au[n]);
+            for (int r = 0; r < 2 * RT; ++r) {
+                const v8bf w0 = decode_bf16<F>(w[r][s].x, w[r][s].y), w1 = decode_bf16<F>(w[r][s].z, w[r][s].w);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    acc[r][n] = mfma(w0, x[n][s][0], acc[r][n]);
+                    acc[r][n] = mfma(w1, x[n][s][1], acc[r][n]);
+                }
+                w[r][s] = wn[r][s];
             }
-            g[s] = gn[s];
-            u[s] = un[s];
-        }
     }
     // what is left of K, 64 bytes a step, the last step's lanes past K zero on both sides
     const int left0 = whole * U, steps = (K + kStep - 1) / kStep;
     for (int st = left0 + (wave + kUpWaves - whole % kUpWaves) % kUpWaves; st < steps; st += kUpWaves) {
         const int k = st * kStep + j16;
         const bool in = k < K;
-        const uint4 gl = load_weights_if(in, gp + k), ul = load_weights_if(in, up + k);
-        const v8bf g0 = decode_bf16<F>(gl.x, gl.y), g1 = decode_bf16<F>(gl.z, gl.w);
-        const v8bf u0 = decode_bf16<F>(ul.x, ul.y), u1 = decode_bf16<F>(ul.z, ul.w);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const v8bf x0 = load_acts_if(in, xp[n] + k), x1 = load_acts_if(in, xp[n] + k + 8);
-            ag[n] = mfma(g0, x0, ag[n]);
-            au[n] = mfma(u0, x0, au[n]);
-            ag[n] = mfma(g1, x1, ag[n]);
-            au[n] = mfma(u1, x1, au[n]);
+        for (int r = 0; r < 2 * RT; ++r) {
+            const uint4 wl = load_weights_if(in, wp[r] + k);
+            const v8bf w0 = decode_bf16<F>(wl.x, wl.y), w1 = decode_bf16<F>(wl.z, wl.w);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                acc[r][n] = mfma(w0, load_acts_if(in, xp[n] + k), acc[r][n]);
+                acc[r][n] = mfma(w1, load_acts_if(in, xp[n] + k + 8), acc[r][n]);
+            }
         }
     }
 }
 
-template <int F, int NT, int U>
+// One workgroup's columns for NT tiles of entries.
+template <int F, int RT, int NT, int U>
 __device__ __forceinline__ void up_tile(const MoeFew& p, const int16_t* idx, int e, int c0, const Entries& ent,
                                         float* red) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint8_t* we = p.w1 + (int64_t)e * p.gs1;
-    const uint8_t* gp = we + (int64_t)(c0 + (lane & 15)) * p.ld1;
-    const uint8_t* up = we + (int64_t)(p.inter + c0 + (lane & 15)) * p.ld1;
+    const uint8_t* wp[2 * RT];                              // gate tile, up tile, gate tile, ..
+#pragma unroll
+    for (int r = 0; r < 2 * RT; ++r)
+        wp[r] = we + (int64_t)((r & 1) * p.inter + c0 + (r >> 1) * 16 + (lane & 15)) * p.ld1;
     const uint16_t* xp[NT];
-    v4f ag[NT], au[NT];
+    v4f acc[2 * RT][NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int c = n * 16 + (lane & 15);
         xp[n] = p.x + (int64_t)ent.token(c < ent.count ? c : 0) * p.ldx;     // (columns past the entries are not used)
-        ag[n] = au[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r) acc[r][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
     // for the end: factors of the rows, and the weights of the columns' tokens
     // (the sum over all slots of the token that name the expert)
     const int row = threadIdx.x & 15;
-    const float sg = p.s1[(int64_t)e * 2 * p.inter + c0 + row], su = p.s1[(int64_t)e * 2 * p.inter + p.inter + c0 + row];
-    int token[NT], slot[NT];
-    float share[NT];
+    float factor[2 * RT], share[NT];
+#pragma unroll
+    for (int r = 0; r < 2 * RT; ++r) factor[r] = p.s1[((int64_t)2 * e + (r & 1)) * p.inter + c0 + (r >> 1) * 16 + row];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int c = n * 16 + (threadIdx.x >> 4);
-        token[n] = ent.token(c);
-        slot[n] = ent.slot(c);
+        const int token = ent.token(c), slot = ent.slot(c);
+        share[n] = 0.0f;
         if (c >= ent.count) continue;
-        share[n] = p.weights[token[n] * p.topk + slot[n]];
-        for (int j = slot[n] + 1; j < p.topk; ++j)
-            if (idx[token[n] * p.topk + j] == e) share[n] += p.weights[token[n] * p.topk + j];
+        share[n] = p.weights[token * p.topk + slot];
+        for (int j = slot + 1; j < p.topk; ++j)
+            if (idx[token * p.topk + j] == e) share[n] += p.weights[token * p.topk + j];
     }
-    up_sums<F, NT, U>(gp, up, xp, p.hidden, wave, ag, au);
-    // red[wave][tile][gate | up][column * 16 + row], row = 4 (lane / 16) + i
+    up_sums<F, RT, NT, U>(wp, xp, p.hidden, wave, acc);
+    // red[wave][tile of entries][row tile][column * 16 + row], row = 4 (lane / 16) + i
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float* r = red + ((wave * NT + n) * 2) * 256 + (lane & 15) * 16 + (lane >> 4) * 4;
-        *reinterpret_cast<v4f*>(r) = ag[n];
-        *reinterpret_cast<v4f*>(r + 256) = au[n];
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r)
+            *reinterpret_cast<v4f*>(red + ((wave * NT + n) * 2 * RT + r) * 256 + (lane & 15) * 16 + (lane >> 4) * 4) =
+                acc[r][n];
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int c = n * 16 + (threadIdx.x >> 4);
-        if (c >= ent.count) continue;
-        float g = 0.0f, u = 0.0f;
+        const int col = threadIdx.x >> 4;
+        if (n * 16 + col >= ent.count) continue;
+        ActTile tile;
+        tile.set(p, ent, n);
 #pragma unroll
-        for (int w = 0; w < kUpWaves; ++w) {
-            g += red[((w * NT + n) * 2) * 256 + threadIdx.x];
-            u += red[((w * NT + n) * 2 + 1) * 256 + threadIdx.x];
+        for (int r = 0; r < RT; ++r) {
+            float g = 0.0f, u = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kUpWaves; ++w) {
+                g += red[((w * NT + n) * 2 * RT + 2 * r) * 256 + threadIdx.x];
+                u += red[((w * NT + n) * 2 * RT + 2 * r + 1) * 256 + threadIdx.x];
+            }
+            const float a = silu_fast(g * factor[2 * r]) * (u * factor[2 * r + 1]) * share[n];
+            const uint32_t hi = f32_to_bf16(a);
+            const float rest = a - __uint_as_float(hi << 16);
+            // (an Inf or NaN is carried by the high part alone)
+            const uint32_t lo = __builtin_isfinite(a) && __builtin_isfinite(rest) ? f32_to_bf16(rest) : 0u;
+            const int k = c0 + r * 16, kb = k >> 6, j = (k >> 4) & 3, half = row >> 3;
+            tile.base[tile.offset(kb, half, j, col) + (row & 7)] = (uint16_t)hi;
+            tile.base[tile.offset(kb, 2 + half, j, col) + (row & 7)] = (uint16_t)lo;
         }
-        const float a = silu_fast(g * sg) * (u * su) * share[n];
-        const uint32_t hi = f32_to_bf16(a);
-        const float rest = a - __uint_as_float(hi << 16);
-        // (an Inf or NaN is carried by the high part alone)
-        const uint32_t lo = __builtin_isfinite(a) && __builtin_isfinite(rest) ? f32_to_bf16(rest) : 0u;
-        uint16_t* dst = p.ws + ((int64_t)token[n] * p.topk + slot[n]) * 2 * p.inter + c0 + row;
-        dst[0] = (uint16_t)hi;
-        dst[p.inter] = (uint16_t)lo;
     }
 }
 
-template <int F, int NTMAX>
+template <int F, int RT, int NTMAX>
 __global__ __launch_bounds__(kUpWaves * 64) void k_moe_few_up(MoeFew p) {
     __shared__ uint32_t bits[kMaxWords];
     __shared__ int16_t idx[NTMAX * 16 * kMoeMaxTopk];
-    __shared__ __attribute__((aligned(16))) float red[kUpWaves * NTMAX * 2 * 256];
+    __shared__ __attribute__((aligned(16))) float red[kUpWaves * NTMAX * 2 * RT * 256];
     const int lane = threadIdx.x & 63;
     read_entries(p, idx, bits);
     const uint32_t word = lane < kMaxWords ? bits[lane] : 0u;
@@ -280,20 +322,20 @@ __global__ __launch_bounds__(kUpWaves * 64) void k_moe_few_up(MoeFew p) {
     const int owner = __ffsll((unsigned long long)__ballot(mine)) - 1;
     const int e = __builtin_amdgcn_readfirstlane(__shfl(lane * 32 + __ffs((int)w) - 1, owner, 64));
     const Entries ent = find_entries(p, idx, e);
-    const int c0 = blockIdx.x * 16;
+    const int c0 = blockIdx.x * (RT * 16);
     if constexpr (NTMAX >= 4) {
         if (ent.count > 32) {
-            up_tile<F, 4, 2>(p, idx, e, c0, ent, red);
+            up_tile<F, RT, 4, 1>(p, idx, e, c0, ent, red);
             return;
         }
     }
     if constexpr (NTMAX >= 2) {
         if (ent.count > 16) {
-            up_tile<F, 2, 4>(p, idx, e, c0, ent, red);
+            up_tile<F, RT, 2, 2>(p, idx, e, c0, ent, red);
             return;
         }
     }
-    up_tile<F, 1, 4>(p, idx, e, c0, ent, red);
+    up_tile<F, RT, 1, RT == 1 ? 4 : 2>(p, idx, e, c0, ent, red);
 }
 
 // -------------------------------------------------------------------- down --
@@ -308,9 +350,9 @@ constexpr int kDownWaves = 8;
 // Products of RT * 16 weight rows with the entries of tiles 0 .. NT-1 over the
 // blocks b0, b0 + db, .. of K.
 template <int F, int RT, int NT, int U>
-__device__ __forceinline__ void down_sums(const uint8_t* const* wp, const uint16_t* const* ap, int K, int b0, int db,
-                                          v4f (*acc)[NT]) {
-    const int j16 = ((threadIdx.x & 63) >> 4) * 16;
+__device__ __forceinline__ void down_sums(const uint8_t* const* wp, const ActTile* tile, const int* col, int K, int b0,
+                                          int db, v4f (*acc)[NT]) {
+    const int j = (threadIdx.x & 63) >> 4, j16 = j * 16;
     const int whole = K / (kStep * U);
     uint4 w[RT][U];
     if (b0 < whole) {
@@ -328,12 +370,10 @@ __device__ __forceinline__ void down_sums(const uint8_t* const* wp, const uint16
 #pragma unroll
         for (int s = 0; s < U; ++s)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                a[n][s][0] = load_acts(ap[n] + k0 + s * kStep);
-                a[n][s][1] = load_acts(ap[n] + k0 + s * kStep + 8);
-                a[n][s][2] = load_acts(ap[n] + K + k0 + s * kStep);
-                a[n][s][3] = load_acts(ap[n] + K + k0 + s * kStep + 8);
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)                 // (a whole step: 4 groups)
+                    a[n][s][q] = load_acts(tile[n].base + (b * U + s) * 128 * tile[n].w + q * 32 * tile[n].w + col[n]);
         __builtin_amdgcn_sched_barrier(0);
         if (b + db < whole) {
 #pragma unroll
@@ -361,15 +401,19 @@ __device__ __forceinline__ void down_sums(const uint8_t* const* wp, const uint16
     for (int k = b * (kStep * U) + j16; k - j16 < K; k += kStep) {
         const bool in = k < K;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const uint4 wl = load_weights_if(in, wp[r] + k);
-            const v8bf w0 = decode_bf16<F>(wl.x, wl.y), w1 = decode_bf16<F>(wl.z, wl.w);
+        for (int n = 0; n < NT; ++n) {
+            v8bf a[4];
+            const int c = col[n] / 8 - j * tile[n].w;       // (the column)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                acc[r][n] = mfma(w0, load_acts_if(in, ap[n] + k), acc[r][n]);
-                acc[r][n] = mfma(w1, load_acts_if(in, ap[n] + k + 8), acc[r][n]);
-                acc[r][n] = mfma(w0, load_acts_if(in, ap[n] + K + k), acc[r][n]);
-                acc[r][n] = mfma(w1, load_acts_if(in, ap[n] + K + k + 8), acc[r][n]);
+            for (int q = 0; q < 4; ++q) a[q] = load_acts_if(in, tile[n].base + tile[n].offset(k >> 6, q, j, c));
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const uint4 wl = load_weights_if(in, wp[r] + k);
+                const v8bf w0 = decode_bf16<F>(wl.x, wl.y), w1 = decode_bf16<F>(wl.z, wl.w);
+                acc[r][n] = mfma(w0, a[0], acc[r][n]);
+                acc[r][n] = mfma(w1, a[1], acc[r][n]);
+                acc[r][n] = mfma(w0, a[2], acc[r][n]);
+                acc[r][n] = mfma(w1, a[3], acc[r][n]);
             }
         }
     }
@@ -382,7 +426,6 @@ __device__ __forceinline__ void down_unit(const MoeFew& p, int e, int row0, cons
     const int lane = threadIdx.x & 63;
     const uint8_t* we = p.w2 + (int64_t)e * p.gs2;
     const uint8_t* wp[RT];
-    const uint16_t* ap[NT];
     v4f acc[RT][NT], sc[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -392,12 +435,16 @@ __device__ __forceinline__ void down_unit(const MoeFew& p, int e, int row0, cons
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[r][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
+    ActTile tile[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) tile[n].set(p, ent, n);
+    int col[NT];                                            // this lane's place in a part of a whole step
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int c = n * 16 + (lane & 15), cc = c < ent.count ? c : 0;      // (columns past the entries are not used)
-        ap[n] = p.ws + ((int64_t)ent.token(cc) * p.topk + ent.slot(cc)) * 2 * p.inter;
+        const int c = lane & 15;
+        col[n] = ((lane >> 4) * tile[n].w + (c < tile[n].w ? c : 0)) * 8;     // (columns past the entries are not used)
     }
-    down_sums<F, RT, NT, U>(wp, ap, p.inter, b0, db, acc);
+    down_sums<F, RT, NT, U>(wp, tile, col, p.inter, b0, db, acc);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int c = n * 16 + (lane & 15);
@@ -457,11 +504,22 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_moe_few_down(MoeFew p) {
 template <int F>
 hipError_t moe_few_up(const MoeFew& p, hipStream_t st) {
     const int entries = p.tokens * p.topk;
-    const dim3 grid((unsigned)(p.inter / 16), (unsigned)(entries < p.experts ? entries : p.experts));
-    const dim3 block(kUpWaves * 64);
-    if (p.tokens <= 16) hipLaunchKernelGGL((k_moe_few_up<F, 1>), grid, block, 0, st, p);
-    else if (p.tokens <= 32) hipLaunchKernelGGL((k_moe_few_up<F, 2>), grid, block, 0, st, p);
-    else hipLaunchKernelGGL((k_moe_few_up<F, 4>), grid, block, 0, st, p);
+    const unsigned experts = (unsigned)(entries < p.experts ? entries : p.experts);
+    // Two row tiles where that leaves four workgroups per CU and an expert has
+    // four tokens or more on average (32 experts of 7168 x 2048: 64 tokens 383 us
+    // for both launches with one tile, 338 with two; 4096 x 1536, 8 tokens, 128 and
+    // 131 us).
+    const bool two = p.inter % 32 == 0 && (int64_t)(p.inter / 32) * experts >= 1024 && entries >= 4 * (int)experts;
+    const dim3 grid((unsigned)(p.inter / (two ? 32 : 16)), experts), block(kUpWaves * 64);
+#define FP8_UP(R, N) hipLaunchKernelGGL((k_moe_few_up<F, R, N>), grid, block, 0, st, p)
+    if (p.tokens <= 16) {
+        if (two) FP8_UP(2, 1); else FP8_UP(1, 1);
+    } else if (p.tokens <= 32) {
+        if (two) FP8_UP(2, 2); else FP8_UP(1, 2);
+    } else {
+        if (two) FP8_UP(2, 4); else FP8_UP(1, 4);
+    }
+#undef FP8_UP
     return hipGetLastError();
 }
 
@@ -478,6 +536,10 @@ hipError_t launch_moe_few_tokens(const MoeFew& p, int f1, int f2, hipStream_t st
     if (p.tokens == 0) return hipSuccess;
     const hipError_t e = f1 == kE4M3 ? moe_few_up<kE4M3>(p, st) : moe_few_up<kE5M2>(p, st);
     if (e != hipSuccess) return e;
+    // 32 rows a workgroup where that leaves most CUs one: an activation load serves
+    // two of weights (32 tokens, 32 experts of 7168 x 2048: 290 us for both
+    // launches, 322 with 16 rows); below, twice the workgroups count for more (4096 x
+    // 1536, 8 tokens: 142 us with 32 rows, 128 with 16).
     const bool wide = p.hidden % 32 == 0 && p.hidden >= 32 * 160;
     if (f2 == kE4M3) return wide ? moe_few_down<kE4M3, 2>(p, st) : moe_few_down<kE4M3, 1>(p, st);
     return wide ? moe_few_down<kE5M2, 2>(p, st) : moe_few_down<kE5M2, 1>(p, st);
