@@ -484,32 +484,40 @@ def fp8_blockwise_quantize_weight(w, fmt, q, scale_records):
     _blockwise(lib.fp8_blockwise_quantize_weight, w, fmt, q, scale_records)
 
 
-def _on(dev, **tensors):
-    """Every tensor that is not None is on the device dev, a GPU (a kernel given
-    another device's or the host's address would fault)."""
-    if dev.type != "cuda":
-        raise ValueError(f"the tensors must be on a GPU, got {dev}")
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _on(first, *tensors):
+    """Index of the GPU that first and every other tensor that is not None are on (a
+    kernel given another device's or the host's address would fault)."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError(f"the tensors must be on a GPU, got {first.device}")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"the tensors must be on one GPU: got {first.device} and {t.device} "
+                             f"({tuple(t.shape)} {t.dtype})")
+    return dev
 
 
-class _device:
-    """Makes dev the current device for a call (a launch goes to the current
-    device); free where it is the current one already."""
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
-    def __init__(self, dev):
-        self.dev, self.prev = dev, None
 
-    def __enter__(self):
-        current = torch.cuda.current_device()
-        if self.dev.index is not None and self.dev.index != current:
-            self.prev = current
-            torch.cuda.set_device(self.dev)
+# The current stream's handle without the Stream object around it (1 us of a call).
+_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
+
+def _call(fn, dev, *args):
+    """fn(*args, stream) with dev, a device index, as the current device (a launch
+    goes to the current device) and its current stream."""
+    current = torch.cuda.current_device()
+    if dev == current:
+        _check(fn(*args, _stream_handle(dev)))
+        return
+    torch.cuda.set_device(dev)
+    try:
+        _check(fn(*args, _stream_handle(dev)))
+    finally:
+        torch.cuda.set_device(current)
 
 
 def _vec(t, name, n, dtype=torch.float32):
@@ -521,12 +529,22 @@ def _rows(t, name, elem_size=None):
     """(rows, cols, ld) of a bf16 tensor (or one of codes, elem_size bytes each)
     whose rows do not overlap: a row stride below cols, such as an expanded
     tensor's 0, has no leading dimension."""
-    rows, cols, ld = _mat(t, name, elem_size) if elem_size is not None else _bf16(t, name)
+    if elem_size is None:
+        if t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    elif t.element_size() != elem_size:
+        raise ValueError(f"{name} must have {elem_size}-byte elements, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1 and rows > 0:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
     if rows <= 1:
-        return rows, cols, max(cols, 1)
-    if cols > 1 and t.stride(0) < cols:
-        raise ValueError(f"{name}'s rows overlap (row stride {t.stride(0)}, {cols} columns): make it contiguous")
-    return rows, cols, ld
+        return rows, cols, cols if cols > 0 else 1
+    if ld < cols:
+        raise ValueError(f"{name}'s rows overlap (row stride {ld}, {cols} columns): make it contiguous")
+    return rows, cols, ld if ld > 0 else 1
 
 
 def _like(t, name, rows, cols, elem_size=None):
@@ -580,14 +598,10 @@ def fp8_norm_quantize_row(x, gamma, beta, eps, kind, fmt, margin, q, scale_inv_o
         if xhat_q is None:
             raise ValueError("xhat_scale needs xhat_q")
         ldxq, lds = _checkpoint(xhat_q, "xhat_q", xhat_scale, rows, cols)
-    dev = x.device
-    _on(dev, gamma=gamma, beta=beta, q=q, scale_inv_out=scale_inv_out, y=y, mean_out=mean_out, rstd_out=rstd_out,
-        xhat_q=xhat_q, xhat_scale=xhat_scale)
-    with _device(dev):
-        _check(lib.fp8_norm_quantize_row(_ptr(x), rows, cols, ldx, _ptr(gamma), _ptr(beta), w_type, eps, kind, fmt,
-                                         margin, _ptr(q), ldq, _ptr(scale_inv_out), _ptr(y), ldy, _ptr(mean_out),
-                                         _ptr(rstd_out), _ptr(xhat_q), xhat_fmt, ldxq, _ptr(xhat_scale), lds,
-                                         _stream(x)))
+    dev = _on(x, gamma, beta, q, scale_inv_out, y, mean_out, rstd_out, xhat_q, xhat_scale)
+    _call(lib.fp8_norm_quantize_row, dev, _addr(x), rows, cols, ldx, _addr(gamma), _addr(beta), w_type, eps, kind,
+          fmt, margin, _addr(q), ldq, _addr(scale_inv_out), _addr(y), ldy, _addr(mean_out), _addr(rstd_out),
+          _addr(xhat_q), xhat_fmt, ldxq, _addr(xhat_scale), lds)
 
 
 def norm_workspace(rows, cols, device="cuda:0"):
@@ -600,7 +614,7 @@ def _workspace(t):
         return None, 0
     if not t.is_contiguous():
         raise ValueError("the workspace must be contiguous")
-    return _ptr(t), t.numel() * t.element_size()
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def fp8_norm_backward(dy, x, gamma, mean, rstd, kind, dx, dgamma=None, dbeta=None, workspace=None):
@@ -616,12 +630,9 @@ def fp8_norm_backward(dy, x, gamma, mean, rstd, kind, dx, dgamma=None, dbeta=Non
     _vec(dgamma, "dgamma", cols)
     _vec(dbeta, "dbeta", cols)
     ws, ws_bytes = _workspace(workspace)
-    dev = dy.device
-    _on(dev, x=x, gamma=gamma, mean=mean, rstd=rstd, dx=dx, dgamma=dgamma, dbeta=dbeta, workspace=workspace)
-    with _device(dev):
-        _check(lib.fp8_norm_backward(_ptr(dy), rows, cols, lddy, _ptr(x), ldx, _ptr(gamma), w_type, _ptr(mean),
-                                     _ptr(rstd), kind, _ptr(dx), lddx, _ptr(dgamma), _ptr(dbeta), ws, ws_bytes,
-                                     _stream(dy)))
+    dev = _on(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace)
+    _call(lib.fp8_norm_backward, dev, _addr(dy), rows, cols, lddy, _addr(x), ldx, _addr(gamma), w_type, _addr(mean),
+          _addr(rstd), kind, _addr(dx), lddx, _addr(dgamma), _addr(dbeta), ws, ws_bytes)
 
 
 def fp8_mx_norm_backward(dy, xhat_q, xhat_fmt, xhat_scale, gamma, beta, rstd, kind, dx, dgamma=None, dbeta=None,
@@ -637,13 +648,10 @@ def fp8_mx_norm_backward(dy, xhat_q, xhat_fmt, xhat_scale, gamma, beta, rstd, ki
     _vec(dgamma, "dgamma", cols)
     _vec(dbeta, "dbeta", cols)
     ws, ws_bytes = _workspace(workspace)
-    dev = dy.device
-    _on(dev, xhat_q=xhat_q, xhat_scale=xhat_scale, gamma=gamma, beta=beta, rstd=rstd, dx=dx, dgamma=dgamma,
-        dbeta=dbeta, y=y, workspace=workspace)
-    with _device(dev):
-        _check(lib.fp8_mx_norm_backward(_ptr(dy), rows, cols, lddy, _ptr(xhat_q), xhat_fmt, ldxq, _ptr(xhat_scale),
-                                        lds, _ptr(gamma), _ptr(beta), w_type, _ptr(rstd), kind, _ptr(dx), lddx,
-                                        _ptr(dgamma), _ptr(dbeta), _ptr(y), ldy, ws, ws_bytes, _stream(dy)))
+    dev = _on(dy, xhat_q, xhat_scale, gamma, beta, rstd, dx, dgamma, dbeta, y, workspace)
+    _call(lib.fp8_mx_norm_backward, dev, _addr(dy), rows, cols, lddy, _addr(xhat_q), xhat_fmt, ldxq,
+          _addr(xhat_scale), lds, _addr(gamma), _addr(beta), w_type, _addr(rstd), kind, _addr(dx), lddx,
+          _addr(dgamma), _addr(dbeta), _addr(y), ldy, ws, ws_bytes)
 
 
 def fp8_swiglu_quantize_row_mx(h, fmt, margin, q, scale_inv_out, hq, h_fmt, h_scale):
@@ -655,12 +663,9 @@ def fp8_swiglu_quantize_row_mx(h, fmt, margin, q, scale_inv_out, hq, h_fmt, h_sc
     ldq = _like(q, "q", rows, two_i // 2, 1)
     _vec(scale_inv_out, "scale_inv_out", rows)
     ldhq, lds = _checkpoint(hq, "hq", h_scale, rows, two_i)
-    dev = h.device
-    _on(dev, q=q, scale_inv_out=scale_inv_out, hq=hq, h_scale=h_scale)
-    with _device(dev):
-        _check(lib.fp8_swiglu_quantize_row_mx(_ptr(h), rows, two_i // 2, ldh, fmt, margin, _ptr(q), ldq,
-                                              _ptr(scale_inv_out), _ptr(hq), h_fmt, ldhq, _ptr(h_scale), lds,
-                                              _stream(h)))
+    dev = _on(h, q, scale_inv_out, hq, h_scale)
+    _call(lib.fp8_swiglu_quantize_row_mx, dev, _addr(h), rows, two_i // 2, ldh, fmt, margin, _addr(q), ldq,
+          _addr(scale_inv_out), _addr(hq), h_fmt, ldhq, _addr(h_scale), lds)
 
 
 def fp8_swiglu_backward(da, h, dh, a=None):
@@ -669,11 +674,8 @@ def fp8_swiglu_backward(da, h, dh, a=None):
     rows, inter, ldda = _rows(da, "da")
     ldh, lddh = _like(h, "h", rows, 2 * inter), _like(dh, "dh", rows, 2 * inter)
     lda = _like(a, "a", rows, inter) if a is not None else inter
-    dev = da.device
-    _on(dev, h=h, dh=dh, a=a)
-    with _device(dev):
-        _check(lib.fp8_swiglu_backward(_ptr(da), rows, inter, ldda, _ptr(h), ldh, _ptr(dh), lddh, _ptr(a), lda,
-                                       _stream(da)))
+    dev = _on(da, h, dh, a)
+    _call(lib.fp8_swiglu_backward, dev, _addr(da), rows, inter, ldda, _addr(h), ldh, _addr(dh), lddh, _addr(a), lda)
 
 
 def fp8_mx_swiglu_backward(da, hq, h_fmt, h_scale, dh, a=None):
@@ -683,11 +685,9 @@ def fp8_mx_swiglu_backward(da, hq, h_fmt, h_scale, dh, a=None):
     lddh = _like(dh, "dh", rows, 2 * inter)
     lda = _like(a, "a", rows, inter) if a is not None else inter
     ldhq, lds = _checkpoint(hq, "hq", h_scale, rows, 2 * inter)
-    dev = da.device
-    _on(dev, hq=hq, h_scale=h_scale, dh=dh, a=a)
-    with _device(dev):
-        _check(lib.fp8_mx_swiglu_backward(_ptr(da), rows, inter, ldda, _ptr(hq), h_fmt, ldhq, _ptr(h_scale), lds,
-                                          _ptr(dh), lddh, _ptr(a), lda, _stream(da)))
+    dev = _on(da, hq, h_scale, dh, a)
+    _call(lib.fp8_mx_swiglu_backward, dev, _addr(da), rows, inter, ldda, _addr(hq), h_fmt, ldhq, _addr(h_scale), lds,
+          _addr(dh), lddh, _addr(a), lda)
 
 
 def moe_few_workspace(tokens, topk, inter, device="cuda:0"):
@@ -718,11 +718,7 @@ def fp8_moe_few_tokens(x, expert_idx, weights, w1, f1, w1_scale_inv, w2, f2, w2_
             raise ValueError(f"{name} must be a contiguous float32 [{E} x {n}] tensor")
     ldo = _like(out, "out", T, H)
     ws, ws_bytes = _workspace(workspace)
-    dev = x.device
-    _on(dev, expert_idx=expert_idx, weights=weights, w1=w1, w1_scale_inv=w1_scale_inv, w2=w2,
-        w2_scale_inv=w2_scale_inv, out=out, workspace=workspace)
-    with _device(dev):
-        _check(lib.fp8_moe_few_tokens(_ptr(x), T, H, ldx, _ptr(expert_idx), _ptr(weights), k, E, _ptr(w1), f1,
-                                      w1.stride(1), w1.stride(0) if E > 1 else 0, _ptr(w1_scale_inv), _ptr(w2), f2,
-                                      w2.stride(1), w2.stride(0) if E > 1 else 0, _ptr(w2_scale_inv), inter, _ptr(out),
-                                      ldo, ws, ws_bytes, _stream(x)))
+    dev = _on(x, expert_idx, weights, w1, w1_scale_inv, w2, w2_scale_inv, out, workspace)
+    _call(lib.fp8_moe_few_tokens, dev, _addr(x), T, H, ldx, _addr(expert_idx), _addr(weights), k, E, _addr(w1), f1,
+          w1.stride(1), w1.stride(0) if E > 1 else 0, _addr(w1_scale_inv), _addr(w2), f2, w2.stride(1),
+          w2.stride(0) if E > 1 else 0, _addr(w2_scale_inv), inter, _addr(out), ldo, ws, ws_bytes)

@@ -44,9 +44,8 @@ __device__ __forceinline__ float load_weight(const void* w, int w_f32, int64_t c
 // (sum of (x - mu)^2), so a row whose mean is large against its deviation
 // loses nothing. y is formed in fp32 and cast from there.
 template <int F, int MAXC, int WPR>
-__global__ __launch_bounds__(kBlock) void k_norm_quant_row(NormFwd p) {
-    __shared__ float red[2][kWaves];
-    __shared__ uint32_t redu[kWaves];
+__global__ __launch_bounds__(WPR == 1 ? kBlock : WPR * 64) void k_norm_quant_row(NormFwd p) {
+    __shared__ float red[3][WPR];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int t = WPR == 1 ? lane : (int)threadIdx.x;
     constexpr int TPR = WPR * 64;
@@ -62,49 +61,49 @@ __global__ __launch_bounds__(kBlock) void k_norm_quant_row(NormFwd p) {
         raw[c] = load_stream(xr + (ch < nch ? ch : nch - 1));
     }
     float v[MAXC][8];
-    float s = 0.0f;
 #pragma unroll
     for (int c = 0; c < MAXC; ++c) {
+        if (t + c * TPR >= nch) raw[c] = make_uint4(0u, 0u, 0u, 0u);        // past the row: zeros
         unpack8(raw[c], v[c]);
-        const bool live = t + c * TPR < nch;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[c][i] = live ? v[c][i] : 0.0f;
-            s += v[c][i];
-        }
     }
     float mean = 0.0f;
     if (!p.rms) {
+        float s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < MAXC; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += v[c][i];
         s = wave_sum(s);
         if (WPR > 1) {
             if (lane == 0) red[0][wave] = s;
             __syncthreads();
-            s = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
+            s = sum_of<WPR>(red[0]);
         }
         mean = s * inv_n;
+#pragma unroll
+        for (int c = 0; c < MAXC; ++c) {
+            const float m = t + c * TPR < nch ? mean : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] -= m;
+        }
     }
     float ss = 0.0f;
 #pragma unroll
-    for (int c = 0; c < MAXC; ++c) {
-        const bool live = t + c * TPR < nch;
+    for (int c = 0; c < MAXC; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[c][i] = live ? v[c][i] - mean : 0.0f;
-            ss = fmaf(v[c][i], v[c][i], ss);
-        }
-    }
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[c][i], v[c][i], ss);
     ss = wave_sum(ss);
     if (WPR > 1) {
         if (lane == 0) red[1][wave] = ss;
         __syncthreads();
-        ss = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+        ss = sum_of<WPR>(red[1]);
     }
     const float rstd = 1.0f / __builtin_sqrtf(ss * inv_n + p.eps);
     if (t == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
-    uint32_t mx = 0;
+    float mx = 0.0f;
 #pragma unroll
     for (int c = 0; c < MAXC; ++c) {
         const int ch = t + c * TPR;
@@ -116,7 +115,7 @@ __global__ __launch_bounds__(kBlock) void k_norm_quant_row(NormFwd p) {
             uint32_t record;
             const uint2 code = p.ckpt_e5m2 ? mx_chunk<kE5M2>(v[c], live, &record) : mx_chunk<kE4M3>(v[c], live, &record);
             if (live) {
-                reinterpret_cast<uint2*>(p.xq + row * p.ldxq)[ch] = code;
+                store_checkpoint(p.xq + row * p.ldxq + 8 * ch, code);
                 if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.xs + 4 * ((int64_t)(ch >> 4) * p.ldxs + row)) = record;
             }
         }
@@ -132,30 +131,34 @@ __global__ __launch_bounds__(kBlock) void k_norm_quant_row(NormFwd p) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[c][i] += b[i];
         }
-        if (live) {
-            if (p.y) reinterpret_cast<uint4*>(p.y + row * p.ldy)[ch] = pack8(v[c]);
-            const uint32_t m = absmax8(v[c]);
-            mx = m > mx ? m : mx;
-        }
+        // (a chunk past the row holds a value of xh = 0 at the row's last
+        // columns: kept out of the maximum)
+        const float m = absmax8(v[c]);
+        mx = __builtin_elementwise_maximum(mx, live ? m : 0.0f);
+        if (p.y && live) reinterpret_cast<uint4*>(p.y + row * p.ldy)[ch] = pack8(v[c]);
     }
     if (!p.q) return;
-    mx = wave_max_u32(mx);
+    mx = wave_max(mx);
     if (WPR > 1) {
-        if (lane == 0) redu[wave] = mx;
+        if (lane == 0) red[2][wave] = mx;
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) mx = redu[w] > mx ? redu[w] : mx;
+        mx = max_of<WPR>(red[2]);
     }
-    const float amax = __uint_as_float(mx);
-    const float sc = scale_from_amax<F>(amax, p.margin);
+    const float sc = scale_from_amax<F>(mx, p.margin);
     if (t == 0) p.scale_inv[row] = 1.0f / sc;
     uint2* qr = reinterpret_cast<uint2*>(p.q + row * p.ldq);
-    const bool nan_free = !__builtin_isnan(amax);
+    if (__builtin_isfinite(mx)) {
 #pragma unroll
-    for (int c = 0; c < MAXC; ++c) {
-        const int ch = t + c * TPR;
-        const uint2 o = nan_free ? encode8f<F, true>(v[c], sc) : encode8f<F, false>(v[c], sc);
-        if (ch < nch) qr[ch] = o;
+        for (int c = 0; c < MAXC; ++c) {
+            const int ch = t + c * TPR;
+            if (ch < nch) qr[ch] = encode8_scaled<F>(v[c], sc);
+        }
+    } else {        // an Inf or NaN in the row (then the scale is 1): the bit-level encoder
+#pragma unroll
+        for (int c = 0; c < MAXC; ++c) {
+            const int ch = t + c * TPR;
+            if (ch < nch) qr[ch] = encode8f<F, false>(v[c], sc);
+        }
     }
 }
 
@@ -246,7 +249,7 @@ __device__ __forceinline__ void load_row(const NormBwd& p, int row, uint32_t tt,
 #pragma unroll
     for (int c = 0; c < MAXC; ++c) {
         const uint32_t ch = tt + c * TPR;
-        const uint32_t cc = ch < nch ? ch : nch - 1;
+        const uint32_t cc = ch < nch ? ch : nch - 1;    // (past the row: a duplicate, never stored)
         d->dy[c] = load_stream(at<uint4>(dr, cc * 16));
         if constexpr (SRC == 0) {
             const uint4 x = load_stream(at<uint4>(p.x + row * p.ldx, cc * 16));
@@ -269,9 +272,9 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
     for (int i = 0; i < 8; ++i) p[i] = v[i];
 }
 
-// Chunk c of the row as fp32: xh and dy, zeros where it is not live.
+// Chunk c of the row as fp32.
 template <int SRC, int MAXC>
-__device__ __forceinline__ void row_values(const RowData<SRC, MAXC>& d, int c, bool live, float* xh, float* dy) {
+__device__ __forceinline__ void row_values(const RowData<SRC, MAXC>& d, int c, float* xh, float* dy) {
     unpack8(d.dy[c], dy);
     if constexpr (SRC == 0) {
         unpack8(make_uint4(d.x[c][0], d.x[c][1], d.x[c][2], d.x[c][3]), xh);
@@ -284,16 +287,11 @@ __device__ __forceinline__ void row_values(const RowData<SRC, MAXC>& d, int c, b
 #pragma unroll
         for (int i = 0; i < 8; ++i) xh[i] *= bs;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        xh[i] = live ? xh[i] : 0.0f;
-        dy[i] = live ? dy[i] : 0.0f;
-    }
 }
 
-template <int SRC, int TPR, int MAXC>
-__global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_norm_grad(NormBwd p) {
-    constexpr int WG = TPR < 512 ? 512 : TPR, TEAMS = WG / TPR, NW = TPR / 64;
+template <int SRC, int TPR, int MAXC, int WG>
+__global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
+    constexpr int TEAMS = WG / TPR, NW = TPR / 64;
     __shared__ float2 red[2][WG / 64];
     __shared__ float fold[TEAMS > 1 ? 2 * MAXC * 8 * TPR : 1];
     __shared__ float beta[SRC > 0 ? MAXC * 8 * TPR : 1];
@@ -341,8 +339,11 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_norm_grad(NormBwd 
         for (int c = 0; c < MAXC; ++c) {
             const uint32_t ch = tt + c * TPR;
             const bool live = live_row && ch < nch;
+            // Past the row (or the band) dy counts as 0: every term of the sums is then
+            // 0, or NaN where the row's own duplicated values give NaN anyway.
+            if (!live) cur.dy[c] = make_uint4(0u, 0u, 0u, 0u);
             float xh[8], dy[8];
-            row_values<SRC>(cur, c, live, xh, dy);
+            row_values<SRC>(cur, c, xh, dy);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float w = dy[i] * g[c][i];
@@ -378,12 +379,12 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_norm_grad(NormBwd 
             const bool live = live_row && ch < nch;
             // the row's values again from its raw words (made opaque here, so
             // that they are not kept): holding them across the reduction took
-            // 178 VGPRs, one workgroup of 512 threads per CU instead of two
+            // 178 VGPRs, half the wavefronts a CU holds
             asm volatile("" : "+v"(cur.dy[c].x), "+v"(cur.dy[c].y), "+v"(cur.dy[c].z), "+v"(cur.dy[c].w));
             asm volatile("" : "+v"(cur.x[c][0]), "+v"(cur.x[c][1]));
             if constexpr (SRC == 0) asm volatile("" : "+v"(cur.x[c][2]), "+v"(cur.x[c][3]));
             float xh[8], dy[8], o[8];
-            row_values<SRC>(cur, c, live, xh, dy);
+            row_values<SRC>(cur, c, xh, dy);
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = cur.rstd * (fmaf(-c1, xh[i], dy[i] * g[c][i]) - c2);
             if (live) *at<uint4>(p.dx + row * p.lddx, ch * 16) = pack8(o);
@@ -481,23 +482,33 @@ __global__ __launch_bounds__(kBlock) void k_norm_grad_row_any(NormBwd p) {
     }
 }
 
-__global__ __launch_bounds__(kBlock) void k_norm_grad_cols_any(NormBwd p) {
-    const int64_t c = (int64_t)blockIdx.x * kBlock + threadIdx.x;
-    if (c >= p.cols) return;
+// 32 columns x 32 slices of the band's rows per workgroup, the slices added in
+// order. (One thread per column over bands of 32 rows: a third launch for every
+// size, 333 x 1111: 4.6 + 2.6 us.)
+constexpr int kAnyCols = 32, kAnySlices = 32;
+__global__ __launch_bounds__(kAnyCols * kAnySlices) void k_norm_grad_cols_any(NormBwd p) {
+    __shared__ float red[2][kAnySlices][kAnyCols];
+    const int cl = threadIdx.x % kAnyCols, sl = threadIdx.x / kAnyCols;
+    const int64_t c = (int64_t)blockIdx.x * kAnyCols + cl, cc = c < p.cols ? c : p.cols - 1;
     const int64_t r0 = (int64_t)blockIdx.y * p.band;
     const int64_t r1 = r0 + p.band < p.rows ? r0 + p.band : p.rows;
     float dg = 0.0f, db = 0.0f;
-#pragma unroll 4
-    for (int64_t r = r0; r < r1; ++r) {
-        const float xh = (load_bf16(p.x + r * p.ldx + c) - (p.mean ? p.mean[r] : 0.0f)) * p.rstd[r];
-        const float dy = load_bf16(p.dy + r * p.lddy + c);
+#pragma unroll 8
+    for (int64_t r = r0 + sl; r < r1; r += kAnySlices) {
+        const float xh = (load_bf16(p.x + r * p.ldx + cc) - (p.mean ? p.mean[r] : 0.0f)) * p.rstd[r];
+        const float dy = load_bf16(p.dy + r * p.lddy + cc);
         dg = fmaf(dy, xh, dg);
         db += dy;
     }
-    float* og = p.bands == 1 ? p.dgamma : p.partial + (int64_t)blockIdx.y * 2 * p.cols;
-    float* ob = p.bands == 1 ? p.dbeta : p.partial + (int64_t)blockIdx.y * 2 * p.cols + p.cols;
-    if (p.dgamma) og[c] = dg;
-    if (p.dbeta) ob[c] = db;
+    red[0][sl][cl] = dg;
+    red[1][sl][cl] = db;
+    __syncthreads();
+    if (sl > 1 || c >= p.cols) return;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < kAnySlices; ++i) s += red[sl][i][cl];
+    float* out = sl == 0 ? p.dgamma : p.dbeta;
+    if (out) (p.bands == 1 ? out : p.partial + ((int64_t)blockIdx.y * 2 + sl) * p.cols)[c] = s;
 }
 
 unsigned row_grid(int64_t rows) { return (unsigned)(rows < (1 << 20) ? rows : (1 << 20)); }
@@ -514,12 +525,13 @@ hipError_t norm_quant_fmt(const NormFwd& p, bool vec, hipStream_t st) {
     const int64_t nch = p.cols / 8;
     const bool wide = nch > 256 || (nch > 64 && p.rows < 1024);
     const dim3 grid((unsigned)(wide ? p.rows : (p.rows + kWaves - 1) / kWaves));
-#define FP8_NORM_CASE(C, W) hipLaunchKernelGGL((k_norm_quant_row<F, C, W>), grid, block, 0, st, p)
+#define FP8_NORM_CASE(C, W) \
+    hipLaunchKernelGGL((k_norm_quant_row<F, C, W>), grid, dim3(W == 1 ? kBlock : W * 64), 0, st, p)
     if (wide) {
         if (nch <= 256) FP8_NORM_CASE(1, 4);
         else if (nch <= 512) FP8_NORM_CASE(2, 4);
         else if (nch <= 1024) FP8_NORM_CASE(4, 4);
-        else FP8_NORM_CASE(8, 4);
+        else FP8_NORM_CASE(4, 8);
     } else {
         if (nch <= 64) FP8_NORM_CASE(1, 1);
         else if (nch <= 128) FP8_NORM_CASE(2, 1);
@@ -543,21 +555,27 @@ hipError_t launch_norm_quant_row(const NormFwd& p, int fmt, hipStream_t st) {
 template <int SRC>
 hipError_t norm_grad_src(NormBwd p, hipStream_t st) {
     const int64_t nch = p.cols / 8;
+    // 16 wavefronts a CU either way: as one workgroup they leave half as many
+    // partial sums (8192 x 4096: 42.4 us with 1024 threads, 44.8 with 512), as two
+    // they spread few rows wider (300 x 4096: 10.5 and 9.2 us) and need fewer
+    // rounds to add up narrow teams (16384 x 1024: 28.1 and 26.5 us).
+    const bool tall = p.rows >= 2048 && nch > 256;
     const int tpr = nch <= 128 ? 64 : (nch <= 256 ? 128 : (nch <= 512 ? 256 : (nch <= 1024 ? 512 : 1024)));
-    const int64_t teams = tpr < 512 ? 512 / tpr : 1;
-    const int64_t max_bands = tpr < 1024 ? kNormMaxBands : kNormMaxBands / 2;
-    int64_t band = (p.rows + max_bands - 1) / max_bands;
+    const int wg = tall || tpr == 1024 ? 1024 : 512;
+    const int64_t teams = wg / tpr, max_bands = wg == 512 ? kNormMaxBands : kNormMaxBands / 2;
+    const int64_t band = (p.rows + max_bands - 1) / max_bands;
     p.band = (band + teams - 1) / teams * teams;
     p.bands = (p.rows + p.band - 1) / p.band;
     const dim3 grid((unsigned)p.bands);
-#define FP8_NORM_CASE(T, C) \
-    hipLaunchKernelGGL((k_norm_grad<SRC, T, C>), grid, dim3(T < 512 ? 512 : T), 0, st, p)
-    if (nch <= 64) FP8_NORM_CASE(64, 1);
-    else if (nch <= 128) FP8_NORM_CASE(64, 2);
-    else if (nch <= 256) FP8_NORM_CASE(128, 2);
-    else if (nch <= 512) FP8_NORM_CASE(256, 2);
-    else if (nch <= 1024) FP8_NORM_CASE(512, 2);
-    else FP8_NORM_CASE(1024, 2);
+#define FP8_NORM_CASE(T, C, W) hipLaunchKernelGGL((k_norm_grad<SRC, T, C, W>), grid, dim3(W), 0, st, p)
+    if (nch <= 64) FP8_NORM_CASE(64, 1, 512);
+    else if (nch <= 128) FP8_NORM_CASE(64, 2, 512);
+    else if (nch <= 256) FP8_NORM_CASE(128, 2, 512);
+    else if (nch <= 512 && !tall) FP8_NORM_CASE(256, 2, 512);
+    else if (nch <= 512) FP8_NORM_CASE(256, 2, 1024);
+    else if (nch <= 1024 && !tall) FP8_NORM_CASE(512, 2, 512);
+    else if (nch <= 1024) FP8_NORM_CASE(512, 2, 1024);
+    else FP8_NORM_CASE(1024, 2, 1024);
 #undef FP8_NORM_CASE
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && (p.dgamma || p.dbeta) && p.bands > 1) {
@@ -582,11 +600,13 @@ hipError_t launch_norm_backward(const NormBwd& p0, hipStream_t st) {
     hipLaunchKernelGGL(k_norm_grad_row_any, dim3(row_grid(p.rows)), dim3(kBlock), 0, st, p);
     e = hipGetLastError();
     if (e != hipSuccess || (!p.dgamma && !p.dbeta)) return e;
+    // one band up to 1024 rows (32 a thread); beyond, bands of as many rows until
+    // they are kNormMaxBands
     p.band = (p.rows + kNormMaxBands - 1) / kNormMaxBands;
-    if (p.band < 32) p.band = 32;
+    if (p.band < kAnySlices * 32) p.band = kAnySlices * 32;
     p.bands = (p.rows + p.band - 1) / p.band;
-    hipLaunchKernelGGL(k_norm_grad_cols_any, dim3((unsigned)((p.cols + kBlock - 1) / kBlock), (unsigned)p.bands),
-                       dim3(kBlock), 0, st, p);
+    hipLaunchKernelGGL(k_norm_grad_cols_any, dim3((unsigned)((p.cols + kAnyCols - 1) / kAnyCols), (unsigned)p.bands),
+                       dim3(kAnyCols * kAnySlices), 0, st, p);
     e = hipGetLastError();
     if (e == hipSuccess && p.bands > 1) {
         hipLaunchKernelGGL(k_norm_weight_grad, dim3((unsigned)((p.cols + kSliceCols - 1) / kSliceCols), 2),

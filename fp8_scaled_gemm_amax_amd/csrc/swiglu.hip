@@ -21,8 +21,8 @@ constexpr int kWaves = kBlock / 64;
 // of both where inter is no multiple of 128, so each block's byte is stored
 // by itself there.
 template <int F, int MAXC, int WPR>
-__global__ __launch_bounds__(kBlock) void k_swiglu_quant_row_mx(SwigluFwd p) {
-    __shared__ uint32_t redu[kWaves];
+__global__ __launch_bounds__(WPR == 1 ? kBlock : WPR * 64) void k_swiglu_quant_row_mx(SwigluFwd p) {
+    __shared__ float red[WPR];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int t = WPR == 1 ? lane : (int)threadIdx.x;
     constexpr int TPR = WPR * 64;
@@ -41,7 +41,7 @@ __global__ __launch_bounds__(kBlock) void k_swiglu_quant_row_mx(SwigluFwd p) {
     }
     const bool whole = p.inter % 128 == 0;
     float a[MAXC][8];
-    uint32_t mx = 0;
+    float mx = 0.0f;
 #pragma unroll
     for (int c = 0; c < MAXC; ++c) {
         const int ch = t + c * TPR;
@@ -60,8 +60,8 @@ __global__ __launch_bounds__(kBlock) void k_swiglu_quant_row_mx(SwigluFwd p) {
         }
         if (live) {
             uint8_t* hr = p.hq + row * p.ldhq;
-            reinterpret_cast<uint2*>(hr)[ch] = cg;
-            reinterpret_cast<uint2*>(hr + p.inter)[ch] = cu;
+            store_checkpoint(hr + 8 * ch, cg);
+            store_checkpoint(hr + p.inter + 8 * ch, cu);
             if (whole) {
                 if ((lane & 15) == 0) {
                     *reinterpret_cast<uint32_t*>(p.hs + 4 * ((int64_t)(ch >> 4) * p.ldhs + row)) = rg;
@@ -78,28 +78,29 @@ __global__ __launch_bounds__(kBlock) void k_swiglu_quant_row_mx(SwigluFwd p) {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) a[c][i] = silu_fast(g[i]) * u[i];
-        if (live) {
-            const uint32_t m = absmax8(a[c]);
-            mx = m > mx ? m : mx;
-        }
+        mx = __builtin_elementwise_maximum(mx, absmax8(a[c]));      // (past the row: a duplicate of its last chunk)
     }
-    mx = wave_max_u32(mx);
+    mx = wave_max(mx);
     if (WPR > 1) {
-        if (lane == 0) redu[wave] = mx;
+        if (lane == 0) red[wave] = mx;
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) mx = redu[w] > mx ? redu[w] : mx;
+        mx = max_of<WPR>(red);
     }
-    const float amax = __uint_as_float(mx);
-    const float s = scale_from_amax<F>(amax, p.margin);
+    const float s = scale_from_amax<F>(mx, p.margin);
     if (t == 0) p.scale_inv[row] = 1.0f / s;
     uint2* qr = reinterpret_cast<uint2*>(p.q + row * p.ldq);
-    const bool nan_free = !__builtin_isnan(amax);
+    if (__builtin_isfinite(mx)) {
 #pragma unroll
-    for (int c = 0; c < MAXC; ++c) {
-        const int ch = t + c * TPR;
-        const uint2 o = nan_free ? encode8f<F, true>(a[c], s) : encode8f<F, false>(a[c], s);
-        if (ch < nch) qr[ch] = o;
+        for (int c = 0; c < MAXC; ++c) {
+            const int ch = t + c * TPR;
+            if (ch < nch) qr[ch] = encode8_scaled<F>(a[c], s);
+        }
+    } else {        // an Inf or NaN in the row (then the scale is 1): the bit-level encoder
+#pragma unroll
+        for (int c = 0; c < MAXC; ++c) {
+            const int ch = t + c * TPR;
+            if (ch < nch) qr[ch] = encode8f<F, false>(a[c], s);
+        }
     }
 }
 
@@ -163,13 +164,14 @@ template <int F>
 hipError_t swiglu_quant_fmt(const SwigluFwd& p, hipStream_t st) {
     const int64_t nch = p.inter / 8;
     const bool wide = nch > 256 || (nch > 64 && p.rows < 1024);
-    const dim3 block(kBlock), grid((unsigned)(wide ? p.rows : (p.rows + kWaves - 1) / kWaves));
-#define FP8_SW_CASE(C, W) hipLaunchKernelGGL((k_swiglu_quant_row_mx<F, C, W>), grid, block, 0, st, p)
+    const dim3 grid((unsigned)(wide ? p.rows : (p.rows + kWaves - 1) / kWaves));
+#define FP8_SW_CASE(C, W) \
+    hipLaunchKernelGGL((k_swiglu_quant_row_mx<F, C, W>), grid, dim3(W == 1 ? kBlock : W * 64), 0, st, p)
     if (wide) {
         if (nch <= 256) FP8_SW_CASE(1, 4);
         else if (nch <= 512) FP8_SW_CASE(2, 4);
         else if (nch <= 1024) FP8_SW_CASE(4, 4);
-        else FP8_SW_CASE(8, 4);
+        else FP8_SW_CASE(4, 8);
     } else {
         if (nch <= 64) FP8_SW_CASE(1, 1);
         else if (nch <= 128) FP8_SW_CASE(2, 1);
