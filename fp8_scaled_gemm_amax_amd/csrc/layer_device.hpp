@@ -235,6 +235,86 @@ __device__ __forceinline__ void store_checkpoint(uint8_t* p, uint2 v) {
     __builtin_nontemporal_store((u32x2_nt{v.x, v.y}), reinterpret_cast<u32x2_nt*>(p));
 }
 
+// Chunks of 8 values of a row of n: 16-byte accesses where the layout allows
+// them (LOOSE = false: the row starts on 16 bytes and n is a multiple of 8), else
+// 16 bytes at the row's own alignment (n >= 8). The last, cut chunk is loaded as
+// the row's last 8 values and shifted into place when it is used, zeros behind
+// it: no load waits in a branch (by elements in a branch, the gradient of 333 x
+// 1111 took 17 us instead of 10).
+template <typename V, int A>
+struct __attribute__((packed, aligned(A))) Loose {
+    V v;
+};
+template <bool LOOSE>
+__device__ __forceinline__ uint4 load_chunk(const uint16_t* row, uint32_t ch, uint32_t n) {
+    if constexpr (!LOOSE) return load_stream(at<uint4>(row, ch * 16));
+    return at<Loose<uint4, 2>>(row, (ch * 8 + 8 <= n ? ch * 8 : n - 8) * 2)->v;
+}
+// What load_chunk gave for chunk ch, its values in place.
+template <bool LOOSE>
+__device__ __forceinline__ void place_chunk(uint4* v, uint32_t ch, uint32_t n) {
+    if constexpr (LOOSE) {
+        if (ch * 8 + 8 > n) {
+            const uint32_t s = ch * 8 + 8 - n;              // values to drop: 1 .. 7
+            if (s & 4) *v = make_uint4(v->z, v->w, 0u, 0u);
+            if (s & 2) *v = make_uint4(v->y, v->z, v->w, 0u);
+            if (s & 1)
+                *v = make_uint4((v->x >> 16) | (v->y << 16), (v->y >> 16) | (v->z << 16), (v->z >> 16) | (v->w << 16),
+                                v->w >> 16);
+        }
+    }
+}
+template <bool LOOSE>
+__device__ __forceinline__ void store_chunk(uint16_t* row, uint32_t ch, uint32_t n, const float* f) {
+    uint4 v = pack8(f);
+    if constexpr (!LOOSE) {
+        *at<uint4>(row, ch * 16) = v;
+        return;
+    }
+    if (ch * 8 + 8 <= n) {
+        at<Loose<uint4, 2>>(row, ch * 16)->v = v;
+        return;
+    }
+    const uint32_t m = n - ch * 8;                          // 4 + 2 + 1 of the 1 .. 7 values there
+    uint32_t o = ch * 16;
+    if (m & 4) {
+        at<Loose<uint2, 2>>(row, o)->v = make_uint2(v.x, v.y);
+        v.x = v.z;
+        v.y = v.w;
+        o += 8;
+    }
+    if (m & 2) {
+        at<Loose<uint32_t, 2>>(row, o)->v = v.x;
+        v.x = v.y;
+        o += 4;
+    }
+    if (m & 1) *at<uint16_t>(row, o) = (uint16_t)v.x;
+}
+template <bool LOOSE>
+__device__ __forceinline__ void store_codes(uint8_t* row, uint32_t ch, uint32_t n, uint2 v) {
+    if constexpr (!LOOSE) {
+        *at<uint2>(row, ch * 8) = v;
+        return;
+    }
+    if (ch * 8 + 8 <= n) {
+        at<Loose<uint2, 1>>(row, ch * 8)->v = v;
+        return;
+    }
+    const uint32_t m = n - ch * 8;
+    uint32_t o = ch * 8;
+    if (m & 4) {
+        at<Loose<uint32_t, 1>>(row, o)->v = v.x;
+        v.x = v.y;
+        o += 4;
+    }
+    if (m & 2) {
+        at<Loose<uint16_t, 1>>(row, o)->v = (uint16_t)v.x;
+        v.x >>= 16;
+        o += 2;
+    }
+    if (m & 1) row[o] = (uint8_t)v.x;
+}
+
 // Workgroup -> index of its rows such that the workgroups of one XCD (every
 // eighth one in dispatch order) work on neighbouring rows at a time: what
 // neighbouring rows write into one line (the scale records, 4 bytes a row) then

@@ -19,10 +19,13 @@ namespace {
 constexpr int kBlock = 256;   // 4 wavefronts
 constexpr int kWaves = kBlock / 64;
 
-// Eight of gamma's or beta's values (bf16 or fp32), chunk ch.
-__device__ __forceinline__ void load_weights8(const void* w, int w_f32, uint32_t ch, float* o) {
+// Eight of gamma's or beta's values (bf16 or fp32), chunk ch of n.
+template <bool LOOSE>
+__device__ __forceinline__ void load_weights8(const void* w, int w_f32, uint32_t ch, uint32_t n, float* o) {
+    const uint32_t first = !LOOSE || ch * 8 + 8 <= n ? ch * 8 : n - 8;
     if (w_f32) {
-        const float4 a = *at<float4>(w, ch * 32), b = *at<float4>(w, ch * 32 + 16);
+        const float4 a = LOOSE ? at<Loose<float4, 4>>(w, first * 4)->v : *at<float4>(w, first * 4);
+        const float4 b = LOOSE ? at<Loose<float4, 4>>(w, first * 4 + 16)->v : *at<float4>(w, first * 4 + 16);
         o[0] = a.x;
         o[1] = a.y;
         o[2] = a.z;
@@ -31,8 +34,21 @@ __device__ __forceinline__ void load_weights8(const void* w, int w_f32, uint32_t
         o[5] = b.y;
         o[6] = b.z;
         o[7] = b.w;
+        if constexpr (LOOSE) {
+            const uint32_t s = ch * 8 - first;
+            if (s > 0) {
+#pragma unroll
+                for (int k = 4; k >= 1; k >>= 1)
+                    if (s & k) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = i + k < 8 ? o[i + k] : 0.0f;
+                    }
+            }
+        }
     } else {
-        unpack8(*at<uint4>(w, ch * 16), o);
+        uint4 v = LOOSE ? at<Loose<uint4, 2>>(w, first * 2)->v : *at<uint4>(w, first * 2);
+        place_chunk<LOOSE>(&v, ch, n);
+        unpack8(v, o);
     }
 }
 __device__ __forceinline__ float load_weight(const void* w, int w_f32, int64_t c) {
@@ -43,7 +59,7 @@ __device__ __forceinline__ float load_weight(const void* w, int w_f32, int64_t c
 // WPR wavefronts per row. The variance is the second pass over the registers
 // (sum of (x - mu)^2), so a row whose mean is large against its deviation
 // loses nothing. y is formed in fp32 and cast from there.
-template <int F, int MAXC, int WPR>
+template <int F, int MAXC, int WPR, bool LOOSE>
 __global__ __launch_bounds__(WPR == 1 ? kBlock : WPR * 64) void k_norm_quant_row(NormFwd p) {
     __shared__ float red[3][WPR];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -51,18 +67,20 @@ __global__ __launch_bounds__(WPR == 1 ? kBlock : WPR * 64) void k_norm_quant_row
     constexpr int TPR = WPR * 64;
     const int64_t row = WPR == 1 ? xcd_block(blockIdx.x, gridDim.x) * kWaves + wave : xcd_block(blockIdx.x, gridDim.x);
     if (row >= p.rows) return;                              // (uniform over the wavefronts of a row)
-    const int nch = (int)(p.cols >> 3);
+    const uint32_t n = (uint32_t)p.cols;
+    const int nch = (int)((n + 7) >> 3);
     const float inv_n = 1.0f / (float)p.cols;
-    const uint4* xr = reinterpret_cast<const uint4*>(p.x + row * p.ldx);
+    const uint16_t* xr = p.x + row * p.ldx;
     uint4 raw[MAXC];
 #pragma unroll
     for (int c = 0; c < MAXC; ++c) {
         const int ch = t + c * TPR;
-        raw[c] = load_stream(xr + (ch < nch ? ch : nch - 1));
+        raw[c] = load_chunk<LOOSE>(xr, (uint32_t)(ch < nch ? ch : nch - 1), n);
     }
     float v[MAXC][8];
 #pragma unroll
     for (int c = 0; c < MAXC; ++c) {
+        place_chunk<LOOSE>(&raw[c], (uint32_t)(t + c * TPR), n);
         if (t + c * TPR >= nch) raw[c] = make_uint4(0u, 0u, 0u, 0u);        // past the row: zeros
         unpack8(raw[c], v[c]);
     }
@@ -82,9 +100,10 @@ __global__ __launch_bounds__(WPR == 1 ? kBlock : WPR * 64) void k_norm_quant_row
         mean = s * inv_n;
 #pragma unroll
         for (int c = 0; c < MAXC; ++c) {
-            const float m = t + c * TPR < nch ? mean : 0.0f;
+            const int ch = t + c * TPR;
+            const float m = ch < nch ? mean : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] -= m;
+            for (int i = 0; i < 8; ++i) v[c][i] -= !LOOSE || (uint32_t)(ch * 8 + i) < n ? m : 0.0f;
         }
     }
     float ss = 0.0f;
@@ -111,7 +130,7 @@ __global__ __launch_bounds__(WPR == 1 ? kBlock : WPR * 64) void k_norm_quant_row
         const uint32_t cc = (uint32_t)(live ? ch : nch - 1);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[c][i] *= rstd;
-        if (p.xq) {
+        if (!LOOSE && p.xq) {
             uint32_t record;
             const uint2 code = p.ckpt_e5m2 ? mx_chunk<kE5M2>(v[c], live, &record) : mx_chunk<kE4M3>(v[c], live, &record);
             if (live) {
@@ -121,13 +140,13 @@ __global__ __launch_bounds__(WPR == 1 ? kBlock : WPR * 64) void k_norm_quant_row
         }
         if (p.gamma) {
             float g[8];
-            load_weights8(p.gamma, p.w_f32, cc, g);
+            load_weights8<LOOSE>(p.gamma, p.w_f32, cc, n, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[c][i] *= g[i];
         }
         if (p.beta) {
             float b[8];
-            load_weights8(p.beta, p.w_f32, cc, b);
+            load_weights8<LOOSE>(p.beta, p.w_f32, cc, n, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[c][i] += b[i];
         }
@@ -135,7 +154,7 @@ __global__ __launch_bounds__(WPR == 1 ? kBlock : WPR * 64) void k_norm_quant_row
         // columns: kept out of the maximum)
         const float m = absmax8(v[c]);
         mx = __builtin_elementwise_maximum(mx, live ? m : 0.0f);
-        if (p.y && live) reinterpret_cast<uint4*>(p.y + row * p.ldy)[ch] = pack8(v[c]);
+        if (p.y && live) store_chunk<LOOSE>(p.y + row * p.ldy, cc, n, v[c]);
     }
     if (!p.q) return;
     mx = wave_max(mx);
@@ -146,24 +165,24 @@ __global__ __launch_bounds__(WPR == 1 ? kBlock : WPR * 64) void k_norm_quant_row
     }
     const float sc = scale_from_amax<F>(mx, p.margin);
     if (t == 0) p.scale_inv[row] = 1.0f / sc;
-    uint2* qr = reinterpret_cast<uint2*>(p.q + row * p.ldq);
+    uint8_t* qr = p.q + row * p.ldq;
     if (__builtin_isfinite(mx)) {
 #pragma unroll
         for (int c = 0; c < MAXC; ++c) {
             const int ch = t + c * TPR;
-            if (ch < nch) qr[ch] = encode8_scaled<F>(v[c], sc);
+            if (ch < nch) store_codes<LOOSE>(qr, (uint32_t)ch, n, encode8_scaled<F>(v[c], sc));
         }
     } else {        // an Inf or NaN in the row (then the scale is 1): the bit-level encoder
 #pragma unroll
         for (int c = 0; c < MAXC; ++c) {
             const int ch = t + c * TPR;
-            if (ch < nch) qr[ch] = encode8f<F, false>(v[c], sc);
+            if (ch < nch) store_codes<LOOSE>(qr, (uint32_t)ch, n, encode8f<F, false>(v[c], sc));
         }
     }
 }
 
-// Any layout (columns, strides and pointers of any alignment, rows of any
-// length): one workgroup per row, element loads, the row read again from the
+// Rows of fewer than 8 or more than kNormMaxVecCols columns, in any layout: one
+// workgroup per row, element loads, the row read again from the
 // caches for each pass.
 __device__ __forceinline__ float block_sum(float v, float* red) {
     v = wave_sum(v);
@@ -241,8 +260,9 @@ struct RowData {
     float mean, rstd;
 };
 
-template <int SRC, int TPR, int MAXC>
+template <int SRC, int TPR, int MAXC, bool LOOSE>
 __device__ __forceinline__ void load_row(const NormBwd& p, int row, uint32_t tt, uint32_t nch, RowData<SRC, MAXC>* d) {
+    const uint32_t n = (uint32_t)p.cols;
     d->rstd = p.rstd[row];
     d->mean = SRC == 0 && p.mean ? p.mean[row] : 0.0f;
     const uint16_t* dr = p.dy + row * p.lddy;
@@ -250,9 +270,9 @@ __device__ __forceinline__ void load_row(const NormBwd& p, int row, uint32_t tt,
     for (int c = 0; c < MAXC; ++c) {
         const uint32_t ch = tt + c * TPR;
         const uint32_t cc = ch < nch ? ch : nch - 1;    // (past the row: a duplicate, never stored)
-        d->dy[c] = load_stream(at<uint4>(dr, cc * 16));
+        d->dy[c] = load_chunk<LOOSE>(dr, cc, n);
         if constexpr (SRC == 0) {
-            const uint4 x = load_stream(at<uint4>(p.x + row * p.ldx, cc * 16));
+            const uint4 x = load_chunk<LOOSE>(p.x + row * p.ldx, cc, n);
             d->x[c][0] = x.x;
             d->x[c][1] = x.y;
             d->x[c][2] = x.z;
@@ -266,10 +286,17 @@ __device__ __forceinline__ void load_row(const NormBwd& p, int row, uint32_t tt,
     }
 }
 
-// (4-byte stores: dgamma and dbeta have no alignment of their own)
-__device__ __forceinline__ void store8(float* p, const float* v) {
+// (dgamma and dbeta have no alignment but their type's)
+template <bool LOOSE>
+__device__ __forceinline__ void store_sums(float* p, uint32_t ch, uint32_t n, const float* v) {
+    if (!LOOSE || ch * 8 + 8 <= n) {
+        at<Loose<float4, 4>>(p, ch * 32)->v = make_float4(v[0], v[1], v[2], v[3]);
+        at<Loose<float4, 4>>(p, ch * 32 + 16)->v = make_float4(v[4], v[5], v[6], v[7]);
+        return;
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = v[i];
+    for (uint32_t i = 0; i < 7; ++i)
+        if (ch * 8 + i < n) p[ch * 8 + i] = v[i];
 }
 
 // Chunk c of the row as fp32.
@@ -289,7 +316,7 @@ __device__ __forceinline__ void row_values(const RowData<SRC, MAXC>& d, int c, f
     }
 }
 
-template <int SRC, int TPR, int MAXC, int WG>
+template <int SRC, int TPR, int MAXC, int WG, bool LOOSE>
 __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
     constexpr int TEAMS = WG / TPR, NW = TPR / 64;
     __shared__ float2 red[2][WG / 64];
@@ -299,7 +326,7 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
     const int tid = threadIdx.x, team = __builtin_amdgcn_readfirstlane(tid / TPR);
     const int wave = tid >> 6, lane = tid & 63;
     uint32_t tt = (uint32_t)tid % TPR;
-    const uint32_t nch = (uint32_t)(p.cols >> 3);
+    const uint32_t n = (uint32_t)p.cols, nch = (n + 7) >> 3;
     const float inv_n = 1.0f / (float)p.cols;
     const int r0 = (int)(blockIdx.x * p.band);
     const int r1 = r0 + p.band < p.rows ? (int)(r0 + p.band) : (int)p.rows;
@@ -313,18 +340,18 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
             g[c][i] = 1.0f;
             dg[c][i] = db[c][i] = 0.0f;
         }
-        if (p.gamma) load_weights8(p.gamma, p.w_f32, cc, g[c]);
+        if (p.gamma) load_weights8<LOOSE>(p.gamma, p.w_f32, cc, n, g[c]);
         // beta in LDS: the addresses of its two forms, kept over the loop, spilled
         if (SRC > 0 && p.y && p.beta && team == 0) {
             float b[8];
-            load_weights8(p.beta, p.w_f32, cc, b);
+            load_weights8<LOOSE>(p.beta, p.w_f32, cc, n, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) beta[(c * TPR + tt) * 8 + i] = b[i];
         }
     }
     if (SRC > 0) __syncthreads();
     RowData<SRC, MAXC> cur, nxt;
-    load_row<SRC, TPR, MAXC>(p, r0 + team < r1 ? r0 + team : r1 - 1, tt, nch, &cur);
+    load_row<SRC, TPR, MAXC, LOOSE>(p, r0 + team < r1 ? r0 + team : r1 - 1, tt, nch, &cur);
     int buf = 0;
     for (int r = r0; r < r1; r += TEAMS, buf ^= 1) {
         const int row = r + team;
@@ -333,7 +360,7 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
         // tt opaque in every step: offsets are then formed where they are used,
         // next to scalar bases, and not kept as 64-bit pairs over the loop
         asm volatile("" : "+v"(tt));
-        load_row<SRC, TPR, MAXC>(p, next < r1 ? next : r1 - 1, tt, nch, &nxt);
+        load_row<SRC, TPR, MAXC, LOOSE>(p, next < r1 ? next : r1 - 1, tt, nch, &nxt);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int c = 0; c < MAXC; ++c) {
@@ -341,6 +368,15 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
             const bool live = live_row && ch < nch;
             // Past the row (or the band) dy counts as 0: every term of the sums is then
             // 0, or NaN where the row's own duplicated values give NaN anyway.
+            if (LOOSE && live) {
+                uint4 x = make_uint4(cur.x[c][0], cur.x[c][1], cur.x[c][SRC == 0 ? 2 : 0], cur.x[c][SRC == 0 ? 3 : 0]);
+                place_chunk<LOOSE>(&cur.dy[c], ch, n);
+                place_chunk<LOOSE>(&x, ch, n);
+                cur.x[c][0] = x.x;
+                cur.x[c][1] = x.y;
+                cur.x[c][SRC == 0 ? 2 : 0] = x.z;
+                cur.x[c][SRC == 0 ? 3 : 0] = x.w;
+            }
             if (!live) cur.dy[c] = make_uint4(0u, 0u, 0u, 0u);
             float xh[8], dy[8];
             row_values<SRC>(cur, c, xh, dy);
@@ -387,7 +423,7 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
             row_values<SRC>(cur, c, xh, dy);
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = cur.rstd * (fmaf(-c1, xh[i], dy[i] * g[c][i]) - c2);
-            if (live) *at<uint4>(p.dx + row * p.lddx, ch * 16) = pack8(o);
+            if (live) store_chunk<LOOSE>(p.dx + row * p.lddx, ch, n, o);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dg[c][i] = fmaf(dy[i], xh[i], dg[c][i]);
@@ -429,8 +465,8 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
     for (int c = 0; c < MAXC; ++c) {
         const uint32_t ch = tt + c * TPR;
         if (ch >= nch) continue;
-        if (p.dgamma) store8(og + (int64_t)ch * 8, dg[c]);
-        if (p.dbeta) store8(ob + (int64_t)ch * 8, db[c]);
+        if (p.dgamma) store_sums<LOOSE>(og, ch, n, dg[c]);
+        if (p.dbeta) store_sums<LOOSE>(ob, ch, n, db[c]);
     }
 }
 
@@ -459,8 +495,8 @@ __global__ __launch_bounds__(kBlock) void k_norm_weight_grad(const float* __rest
     }
 }
 
-// Any layout, from x: one workgroup per row for dx; for the weights' gradients
-// one thread per column over a band of rows.
+// Rows of fewer than 8 or more than kNormMaxVecCols columns, in any layout, from x:
+// one workgroup per row for dx, another kernel for the weights' gradients.
 __global__ __launch_bounds__(kBlock) void k_norm_grad_row_any(NormBwd p) {
     __shared__ float red[kWaves];
     const int tid = threadIdx.x;
@@ -515,18 +551,13 @@ unsigned row_grid(int64_t rows) { return (unsigned)(rows < (1 << 20) ? rows : (1
 
 }  // namespace
 
-template <int F>
-hipError_t norm_quant_fmt(const NormFwd& p, bool vec, hipStream_t st) {
-    const dim3 block(kBlock);
-    if (!vec) {
-        hipLaunchKernelGGL((k_norm_quant_row_any<F>), dim3(row_grid(p.rows)), block, 0, st, p);
-        return hipGetLastError();
-    }
-    const int64_t nch = p.cols / 8;
+template <int F, bool LOOSE>
+hipError_t norm_quant_reg(const NormFwd& p, hipStream_t st) {
+    const int64_t nch = (p.cols + 7) / 8;
     const bool wide = nch > 256 || (nch > 64 && p.rows < 1024);
     const dim3 grid((unsigned)(wide ? p.rows : (p.rows + kWaves - 1) / kWaves));
 #define FP8_NORM_CASE(C, W) \
-    hipLaunchKernelGGL((k_norm_quant_row<F, C, W>), grid, dim3(W == 1 ? kBlock : W * 64), 0, st, p)
+    hipLaunchKernelGGL((k_norm_quant_row<F, C, W, LOOSE>), grid, dim3(W == 1 ? kBlock : W * 64), 0, st, p)
     if (wide) {
         if (nch <= 256) FP8_NORM_CASE(1, 4);
         else if (nch <= 512) FP8_NORM_CASE(2, 4);
@@ -541,20 +572,27 @@ hipError_t norm_quant_fmt(const NormFwd& p, bool vec, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <int F>
+hipError_t norm_quant_fmt(const NormFwd& p, hipStream_t st) {
+    if (norm_vector_layout(p)) return norm_quant_reg<F, false>(p, st);
+    if (p.cols >= 8 && p.cols <= kNormMaxVecCols) return norm_quant_reg<F, true>(p, st);
+    hipLaunchKernelGGL((k_norm_quant_row_any<F>), dim3(row_grid(p.rows)), dim3(kBlock), 0, st, p);
+    return hipGetLastError();
+}
+
 hipError_t launch_norm_quant_row(const NormFwd& p, int fmt, hipStream_t st) {
     if (p.rows == 0 || p.cols == 0) return hipSuccess;
-    const bool vec = norm_vector_layout(p);
     switch (fmt) {
-        case kE4M3: return norm_quant_fmt<kE4M3>(p, vec, st);
-        case kE5M2: return norm_quant_fmt<kE5M2>(p, vec, st);
-        case kE4M3Fnuz: return norm_quant_fmt<kE4M3Fnuz>(p, vec, st);
-        default: return norm_quant_fmt<kE5M2Fnuz>(p, vec, st);
+        case kE4M3: return norm_quant_fmt<kE4M3>(p, st);
+        case kE5M2: return norm_quant_fmt<kE5M2>(p, st);
+        case kE4M3Fnuz: return norm_quant_fmt<kE4M3Fnuz>(p, st);
+        default: return norm_quant_fmt<kE5M2Fnuz>(p, st);
     }
 }
 
-template <int SRC>
+template <int SRC, bool LOOSE>
 hipError_t norm_grad_src(NormBwd p, hipStream_t st) {
-    const int64_t nch = p.cols / 8;
+    const int64_t nch = (p.cols + 7) / 8;
     // 16 wavefronts a CU either way: as one workgroup they leave half as many
     // partial sums (8192 x 4096: 42.4 us with 1024 threads, 44.8 with 512), as two
     // they spread few rows wider (300 x 4096: 10.5 and 9.2 us) and need fewer
@@ -567,7 +605,7 @@ hipError_t norm_grad_src(NormBwd p, hipStream_t st) {
     p.band = (band + teams - 1) / teams * teams;
     p.bands = (p.rows + p.band - 1) / p.band;
     const dim3 grid((unsigned)p.bands);
-#define FP8_NORM_CASE(T, C, W) hipLaunchKernelGGL((k_norm_grad<SRC, T, C, W>), grid, dim3(W), 0, st, p)
+#define FP8_NORM_CASE(T, C, W) hipLaunchKernelGGL((k_norm_grad<SRC, T, C, W, LOOSE>), grid, dim3(W), 0, st, p)
     if (nch <= 64) FP8_NORM_CASE(64, 1, 512);
     else if (nch <= 128) FP8_NORM_CASE(64, 2, 512);
     else if (nch <= 256) FP8_NORM_CASE(128, 2, 512);
@@ -595,8 +633,9 @@ hipError_t launch_norm_backward(const NormBwd& p0, hipStream_t st) {
         if (p.dbeta && e == hipSuccess) e = launch_fill(p.dbeta, p.cols, 0.0f, st);
         return e;
     }
-    if (p.xq) return p.ckpt_e5m2 ? norm_grad_src<2>(p, st) : norm_grad_src<1>(p, st);
-    if (norm_vector_layout(p)) return norm_grad_src<0>(p, st);
+    if (p.xq) return p.ckpt_e5m2 ? norm_grad_src<2, false>(p, st) : norm_grad_src<1, false>(p, st);
+    if (norm_vector_layout(p)) return norm_grad_src<0, false>(p, st);
+    if (p.cols >= 8 && p.cols <= kNormMaxVecCols) return norm_grad_src<0, true>(p, st);
     hipLaunchKernelGGL(k_norm_grad_row_any, dim3(row_grid(p.rows)), dim3(kBlock), 0, st, p);
     e = hipGetLastError();
     if (e != hipSuccess || (!p.dgamma && !p.dbeta)) return e;

@@ -56,7 +56,7 @@ FORWARD = [  # rows, cols, rms, gamma, beta, fmt
     (1030, 512, True, "f32", "none", 0), (1025, 1000, False, "bf16", "bf16", 2), (1024, 2048, False, "none", "none", 3),
     (9, 2056, True, "none", "f32", 0), (33, 7168, True, "bf16", "none", 0), (3, 16384, False, "bf16", "bf16", 1),
     (4, 1, False, "bf16", "bf16", 0), (7, 1111, False, "bf16", "bf16", 0), (3, 20000, True, "f32", "none", 1),
-    (2, 17, True, "none", "none", 3),
+    (2, 17, True, "none", "none", 3), (1030, 1021, False, "f32", "bf16", 0), (2, 16383, True, "bf16", "none", 0),
 ]
 
 
@@ -173,7 +173,8 @@ BACKWARD = [  # rows, cols, rms, gamma
     (1, 8, False, "bf16"), (1, 512, True, "none"), (3, 520, False, "f32"), (700, 1024, False, "bf16"),
     (65, 2048, True, "bf16"), (1100, 2056, False, "none"), (40, 4096, False, "f32"), (515, 7168, True, "bf16"),
     (5, 8200, False, "bf16"), (300, 16384, True, "f32"), (333, 1111, False, "bf16"), (2, 1, False, "none"),
-    (1, 20000, False, "bf16"), (70, 33, True, "f32"),
+    (1, 20000, False, "bf16"), (70, 33, True, "f32"), (2100, 2051, True, "bf16"), (3, 16381, False, "f32"),
+    (2050, 4096, False, "bf16"), (1100, 16392, True, "bf16"),
 ]
 
 
