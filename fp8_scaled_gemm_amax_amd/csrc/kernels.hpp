@@ -156,8 +156,8 @@ struct NormFwd {
 };
 
 // x (with mean and rstd) or xq / xs (with rstd): where the normalised rows come
-// from. partial: kNormMaxBands * 2 * cols floats at most; band and bands are
-// the launcher's.
+// from. partial: kNormMaxBands * 2 * cols floats at most; band, longer and bands
+// are the launcher's.
 struct NormBwd {
     const uint16_t* dy;
     int64_t rows, cols, lddy;
@@ -175,7 +175,7 @@ struct NormBwd {
     uint16_t* y;
     int64_t ldy;
     float *dgamma, *dbeta, *partial;
-    int64_t band, bands;
+    int64_t band, longer, bands;
 };
 
 // Whether the register kernels take these operands (16-byte chunks everywhere).
