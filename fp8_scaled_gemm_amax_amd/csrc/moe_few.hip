@@ -135,28 +135,31 @@ __device__ __forceinline__ Entries find_entries(const MoeFew& p, const int16_t* 
 }
 
 // The workspace between the two launches: an expert's activations as the down
-// product loads them. Tile n of an expert (16 of its tokens, w of them there)
-// has 2 * inter * w values from (base + 16 n) * 2 * inter on; its step kb of 64
-// values of K has w * 128 of them, as [high | low][half h][group j][token][8]
-// for K = 64 kb + 16 j + 8 h + 0..7: one load of a wavefront (a lane's token and
-// group) is 16 w * 4 consecutive bytes. (Rows of K per token instead made every
-// such load 16 lines: 32 tokens, 32 experts of 7168 x 2048: the down product 150
-// us, without its loads of activations 86.) The last step of K has K / 16 % 4
-// groups. The number of entries in a tile and the tiles of the experts before
-// it add up to at most tokens * topk rows of 2 * inter values.
+// product loads them. Tile n of an expert (8 of its tokens, w of them there)
+// has 2 * inter * w values from (base + 8 n) * 2 * inter on; its step kb of 64
+// values of K has w * 128 of them, as [half h][group j][high | low][token][8]
+// for K = 64 kb + 16 j + 8 h + 0..7. A load of a wavefront (lane: token, part and
+// group) is 128 w consecutive bytes and holds both parts: the high ones are
+// columns 0..7 of the product, the low ones columns 8..15. (Rows of K per token
+// made every load 16 lines: 32 tokens, 32 experts of 7168 x 2048, the down
+// product 150 us, without its loads of activations 86; tiles of 16 tokens with
+// one load for either part 108, these 105; one token 30 and 25.) The last step of K has K / 16 % 4
+// groups. The tiles of all experts add up to at most tokens * topk rows of
+// 2 * inter values.
+constexpr int kActTile = 8;
 struct ActTile {
     uint16_t* base;
     int w, inter;
     __device__ __forceinline__ void set(const MoeFew& p, const Entries& en, int n) {
-        w = en.count - n * 16 < 16 ? en.count - n * 16 : 16;
+        w = en.count - n * kActTile < kActTile ? en.count - n * kActTile : kActTile;
         w = w < 1 ? 1 : w;                                  // (no tokens: not used)
         inter = p.inter;
-        base = p.ws + (int64_t)(en.base + n * 16) * 2 * p.inter;
+        base = p.ws + (int64_t)(en.base + n * kActTile) * 2 * p.inter;
     }
-    // values from the start of step kb, part q = 2 * low + half, group j, of column c
-    __device__ __forceinline__ int offset(int kb, int q, int j, int c) const {
+    // values from the start to step kb, half h, group j, part (0 high, 1 low), token c
+    __device__ __forceinline__ int offset(int kb, int h, int j, int part, int c) const {
         const int left = inter / 16 - kb * 4, groups = left < 4 ? left : 4;
-        return kb * 128 * w + ((q * groups + j) * w + c) * 8;
+        return kb * 128 * w + (((h * groups + j) * 2 + part) * w + c) * 8;
     }
 };
 
@@ -282,8 +285,9 @@ __device__ __forceinline__ void up_tile(const MoeFew& p, const int16_t* idx, int
     for (int n = 0; n < NT; ++n) {
         const int col = threadIdx.x >> 4;
         if (n * 16 + col >= ent.count) continue;
+        const int c = n * 16 + col;
         ActTile tile;
-        tile.set(p, ent, n);
+        tile.set(p, ent, c / kActTile);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             float g = 0.0f, u = 0.0f;
@@ -298,8 +302,8 @@ __device__ __forceinline__ void up_tile(const MoeFew& p, const int16_t* idx, int
             // (an Inf or NaN is carried by the high part alone)
             const uint32_t lo = __builtin_isfinite(a) && __builtin_isfinite(rest) ? f32_to_bf16(rest) : 0u;
             const int k = c0 + r * 16, kb = k >> 6, j = (k >> 4) & 3, half = row >> 3;
-            tile.base[tile.offset(kb, half, j, col) + (row & 7)] = (uint16_t)hi;
-            tile.base[tile.offset(kb, 2 + half, j, col) + (row & 7)] = (uint16_t)lo;
+            tile.base[tile.offset(kb, half, j, 0, c % kActTile) + (row & 7)] = (uint16_t)hi;
+            tile.base[tile.offset(kb, half, j, 1, c % kActTile) + (row & 7)] = (uint16_t)lo;
         }
     }
 }
@@ -341,7 +345,7 @@ __global__ __launch_bounds__(kUpWaves * 64) void k_moe_few_up(MoeFew p) {
 // -------------------------------------------------------------------- down --
 // Workgroup: RT * 16 output columns of every token. The units of work are
 // pieces of K of the experts in use, dealt to the wavefronts in order. A
-// wavefront multiplies the expert's rows with the expert's tokens, 16 at a
+// wavefront multiplies the expert's rows with the expert's tokens, 8 at a
 // time, and adds the sums, times the rows' factors, to its own sums of those
 // tokens in LDS; at the end the wavefronts' sums are added in order. A token's
 // sums are never touched by an expert that it does not use.
@@ -365,15 +369,15 @@ __device__ __forceinline__ void down_sums(const uint8_t* const* wp, const ActTil
     for (; b < whole; b += db) {
         const int k0 = b * (kStep * U) + j16;
         const int kn = k0 + db * (kStep * U);
-        v8bf a[NT][U][4];
+        v8bf a[NT][U][2];
         uint4 wn[RT][U];
 #pragma unroll
         for (int s = 0; s < U; ++s)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)                 // (a whole step: 4 groups)
-                    a[n][s][q] = load_acts(tile[n].base + (b * U + s) * 128 * tile[n].w + q * 32 * tile[n].w + col[n]);
+                for (int h = 0; h < 2; ++h)                 // (a whole step: 4 groups)
+                    a[n][s][h] = load_acts(tile[n].base + (b * U + s) * 128 * tile[n].w + h * 64 * tile[n].w + col[n]);
         __builtin_amdgcn_sched_barrier(0);
         if (b + db < whole) {
 #pragma unroll
@@ -391,8 +395,6 @@ __device__ __forceinline__ void down_sums(const uint8_t* const* wp, const ActTil
                 for (int n = 0; n < NT; ++n) {
                     acc[r][n] = mfma(w0, a[n][s][0], acc[r][n]);
                     acc[r][n] = mfma(w1, a[n][s][1], acc[r][n]);
-                    acc[r][n] = mfma(w0, a[n][s][2], acc[r][n]);
-                    acc[r][n] = mfma(w1, a[n][s][3], acc[r][n]);
                 }
                 w[r][s] = wn[r][s];
             }
@@ -402,18 +404,17 @@ __device__ __forceinline__ void down_sums(const uint8_t* const* wp, const ActTil
         const bool in = k < K;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            v8bf a[4];
-            const int c = col[n] / 8 - j * tile[n].w;       // (the column)
+            const int part = ((threadIdx.x & 63) >> 3) & 1;
+            const int c = col[n] / 8 - (j * 2 + part) * tile[n].w;      // (the token)
+            v8bf a[2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) a[q] = load_acts_if(in, tile[n].base + tile[n].offset(k >> 6, q, j, c));
+            for (int h = 0; h < 2; ++h) a[h] = load_acts_if(in, tile[n].base + tile[n].offset(k >> 6, h, j, part, c));
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 const uint4 wl = load_weights_if(in, wp[r] + k);
                 const v8bf w0 = decode_bf16<F>(wl.x, wl.y), w1 = decode_bf16<F>(wl.z, wl.w);
                 acc[r][n] = mfma(w0, a[0], acc[r][n]);
                 acc[r][n] = mfma(w1, a[1], acc[r][n]);
-                acc[r][n] = mfma(w0, a[2], acc[r][n]);
-                acc[r][n] = mfma(w1, a[3], acc[r][n]);
             }
         }
     }
@@ -441,15 +442,19 @@ __device__ __forceinline__ void down_unit(const MoeFew& p, int e, int row0, cons
     int col[NT];                                            // this lane's place in a part of a whole step
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int c = lane & 15;
-        col[n] = ((lane >> 4) * tile[n].w + (c < tile[n].w ? c : 0)) * 8;     // (columns past the entries are not used)
+        const int c = lane & 7, part = (lane >> 3) & 1;     // (columns past the entries are not used)
+        col[n] = (((lane >> 4) * 2 + part) * tile[n].w + (c < tile[n].w ? c : 0)) * 8;
     }
     down_sums<F, RT, NT, U>(wp, tile, col, p.inter, b0, db, acc);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int c = n * 16 + (lane & 15);
+        const int c = n * kActTile + (lane & 7);
         const int t = ent.token(c);
-        if (c >= ent.count) continue;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][n][i] += __shfl_xor(acc[r][n][i], 8, 64);   // high and low columns
+        if (c >= ent.count || (lane & 8)) continue;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             v4f* d = reinterpret_cast<v4f*>(sums + t * (RT * 16) + r * 16 + (lane >> 4) * 4);
@@ -486,9 +491,11 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_moe_few_down(MoeFew p) {
     for (int unit = wave; unit < total * pieces; unit += kDownWaves) {
         const int e = __builtin_amdgcn_readfirstlane(list[unit / pieces]);
         const Entries ent = find_entries(p, idx, e);
-        if (TT > 32 && ent.count > 32) down_unit<F, RT, 4, 1>(p, e, row0, ent, unit % pieces, pieces, sums);
-        else if (TT > 16 && ent.count > 16) down_unit<F, RT, 2, 2>(p, e, row0, ent, unit % pieces, pieces, sums);
-        else down_unit<F, RT, 1, 4>(p, e, row0, ent, unit % pieces, pieces, sums);
+        const int b0 = unit % pieces;
+        if (TT > 32 && ent.count > 32) down_unit<F, RT, 8, 1>(p, e, row0, ent, b0, pieces, sums);
+        else if (TT > 16 && ent.count > 16) down_unit<F, RT, 4, 2>(p, e, row0, ent, b0, pieces, sums);
+        else if (ent.count > 8) down_unit<F, RT, 2, 4>(p, e, row0, ent, b0, pieces, sums);
+        else down_unit<F, RT, 1, 4>(p, e, row0, ent, b0, pieces, sums);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < p.tokens * (RT * 16); i += kDownWaves * 64) {
