@@ -555,6 +555,9 @@ unsigned row_grid(int64_t rows) { return (unsigned)(rows < (1 << 20) ? rows : (1
 template <int F, bool LOOSE>
 hipError_t norm_quant_reg(const NormFwd& p, hipStream_t st) {
     const int64_t nch = (p.cols + 7) / 8;
+    // four wavefronts a row where the row is long (16384 x 2048: 38.0 us, with one
+    // 32.0; more than 2048 columns do not fit one) or the rows are few (1000 x 2048:
+    // 4.7 and 6.2; 16 x 2048: 3.4 and 5.4)
     const bool wide = nch > 256 || (nch > 64 && p.rows < 1024);
     const dim3 grid((unsigned)(wide ? p.rows : (p.rows + kWaves - 1) / kWaves));
 #define FP8_NORM_CASE(C, W) \

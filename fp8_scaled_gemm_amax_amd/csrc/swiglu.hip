@@ -163,7 +163,10 @@ __global__ __launch_bounds__(kBlock) void k_swiglu_grad(SwigluBwd p, uint32_t ma
 template <int F>
 hipError_t swiglu_quant_fmt(const SwigluFwd& p, hipStream_t st) {
     const int64_t nch = p.inter / 8;
-    const bool wide = nch > 256 || (nch > 64 && p.rows < 1024);
+    // four wavefronts a row where the row is long (16384 x 2048: 40.9 us, with one
+    // 46.5; 16384 x 1024: 37.3 and 24.9) or the rows are few (1000 x 2048: 5.4 and
+    // 6.5), eight above 8192 columns, whose row in four took 160 VGPRs
+    const bool wide = nch > 128 || (nch > 64 && p.rows < 1024);
     const dim3 grid((unsigned)(wide ? p.rows : (p.rows + kWaves - 1) / kWaves));
 #define FP8_SW_CASE(C, W) \
     hipLaunchKernelGGL((k_swiglu_quant_row_mx<F, C, W>), grid, dim3(W == 1 ? kBlock : W * 64), 0, st, p)
@@ -174,8 +177,7 @@ hipError_t swiglu_quant_fmt(const SwigluFwd& p, hipStream_t st) {
         else FP8_SW_CASE(4, 8);
     } else {
         if (nch <= 64) FP8_SW_CASE(1, 1);
-        else if (nch <= 128) FP8_SW_CASE(2, 1);
-        else FP8_SW_CASE(4, 1);
+        else FP8_SW_CASE(2, 1);
     }
 #undef FP8_SW_CASE
     return hipGetLastError();
