@@ -178,6 +178,10 @@ struct NormBwd {
     int64_t band, longer, bands;
 };
 
+// Rows of one launch of the row kernels: longer calls are cut, so that a grid's
+// threads stay below 2^32 whatever the rows.
+constexpr int64_t kLaunchRows = (int64_t)1 << 20;
+
 // Whether the register kernels take these operands (16-byte chunks everywhere).
 inline bool chunked(const void* p, int64_t ld, unsigned align) {
     return !p || ((reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0 && ld % 8 == 0);

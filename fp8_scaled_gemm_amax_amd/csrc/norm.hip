@@ -198,48 +198,47 @@ __global__ __launch_bounds__(kBlock) void k_norm_quant_row_any(NormFwd p) {
     __shared__ float red[kWaves];
     __shared__ uint32_t redu[kWaves];
     const int tid = threadIdx.x;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const uint16_t* xr = p.x + row * p.ldx;
-        const float inv_n = 1.0f / (float)p.cols;
-        float mean = 0.0f, s = 0.0f;
-        if (!p.rms) {
-            for (int64_t c = tid; c < p.cols; c += kBlock) s += load_bf16(xr + c);
-            mean = block_sum(s, red) * inv_n;
-        }
-        float ss = 0.0f;
-        for (int64_t c = tid; c < p.cols; c += kBlock) {
-            const float d = load_bf16(xr + c) - mean;
-            ss = fmaf(d, d, ss);
-        }
-        const float rstd = 1.0f / __builtin_sqrtf(block_sum(ss, red) * inv_n + p.eps);
-        if (tid == 0) {
-            if (p.mean) p.mean[row] = mean;
-            if (p.rstd) p.rstd[row] = rstd;
-        }
-        auto value = [&](int64_t c) {
-            float y = (load_bf16(xr + c) - mean) * rstd;
-            if (p.gamma) y *= load_weight(p.gamma, p.w_f32, c);
-            if (p.beta) y += load_weight(p.beta, p.w_f32, c);
-            return y;
-        };
-        uint32_t mx = 0;
-        for (int64_t c = tid; c < p.cols; c += kBlock) {
-            const float y = value(c);
-            if (p.y) p.y[row * p.ldy + c] = (uint16_t)f32_to_bf16(y);
-            const uint32_t b = __float_as_uint(y) & 0x7fffffffu;
-            mx = b > mx ? b : mx;
-        }
-        if (!p.q) continue;
-        mx = wave_max_u32(mx);
-        __syncthreads();
-        if ((tid & 63) == 0) redu[tid >> 6] = mx;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) mx = redu[w] > mx ? redu[w] : mx;
-        const float sc = scale_from_amax<F>(__uint_as_float(mx), p.margin);
-        if (tid == 0) p.scale_inv[row] = 1.0f / sc;
-        for (int64_t c = tid; c < p.cols; c += kBlock) p.q[row * p.ldq + c] = (uint8_t)encode_sw<F>(value(c) * sc);
+    const int64_t row = blockIdx.x;
+    const uint16_t* xr = p.x + row * p.ldx;
+    const float inv_n = 1.0f / (float)p.cols;
+    float mean = 0.0f, s = 0.0f;
+    if (!p.rms) {
+        for (int64_t c = tid; c < p.cols; c += kBlock) s += load_bf16(xr + c);
+        mean = block_sum(s, red) * inv_n;
     }
+    float ss = 0.0f;
+    for (int64_t c = tid; c < p.cols; c += kBlock) {
+        const float d = load_bf16(xr + c) - mean;
+        ss = fmaf(d, d, ss);
+    }
+    const float rstd = 1.0f / __builtin_sqrtf(block_sum(ss, red) * inv_n + p.eps);
+    if (tid == 0) {
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+    auto value = [&](int64_t c) {
+        float y = (load_bf16(xr + c) - mean) * rstd;
+        if (p.gamma) y *= load_weight(p.gamma, p.w_f32, c);
+        if (p.beta) y += load_weight(p.beta, p.w_f32, c);
+        return y;
+    };
+    uint32_t mx = 0;
+    for (int64_t c = tid; c < p.cols; c += kBlock) {
+        const float y = value(c);
+        if (p.y) p.y[row * p.ldy + c] = (uint16_t)f32_to_bf16(y);
+        const uint32_t b = __float_as_uint(y) & 0x7fffffffu;
+        mx = b > mx ? b : mx;
+    }
+    if (!p.q) return;
+    mx = wave_max_u32(mx);
+    __syncthreads();
+    if ((tid & 63) == 0) redu[tid >> 6] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) mx = redu[w] > mx ? redu[w] : mx;
+    const float sc = scale_from_amax<F>(__uint_as_float(mx), p.margin);
+    if (tid == 0) p.scale_inv[row] = 1.0f / sc;
+    for (int64_t c = tid; c < p.cols; c += kBlock) p.q[row * p.ldq + c] = (uint8_t)encode_sw<F>(value(c) * sc);
 }
 
 // --------------------------------------------------------------- backward --
@@ -548,16 +547,16 @@ __global__ __launch_bounds__(kAnyCols * kAnySlices) void k_norm_grad_cols_any(No
     if (out) (p.bands == 1 ? out : p.partial + ((int64_t)blockIdx.y * 2 + sl) * p.cols)[c] = s;
 }
 
-unsigned row_grid(int64_t rows) { return (unsigned)(rows < (1 << 20) ? rows : (1 << 20)); }
+unsigned row_grid(int64_t rows) { return (unsigned)(rows < kLaunchRows ? rows : kLaunchRows); }
 
 }  // namespace
 
 template <int F, bool LOOSE>
 hipError_t norm_quant_reg(const NormFwd& p, hipStream_t st) {
     const int64_t nch = (p.cols + 7) / 8;
-    // four wavefronts a row where the row is long (16384 x 2048: 38.0 us, with one
-    // 32.0; more than 2048 columns do not fit one) or the rows are few (1000 x 2048:
-    // 4.7 and 6.2; 16 x 2048: 3.4 and 5.4)
+    // One wavefront a row where it holds the row (16384 x 2048: 32.0 us, 38.0 with
+    // four) unless the rows are few (1000 x 2048: 6.2 us with one, 4.7 with four;
+    // 16 x 2048: 5.4 and 3.4); eight above 8192 columns.
     const bool wide = nch > 256 || (nch > 64 && p.rows < 1024);
     const dim3 grid((unsigned)(wide ? p.rows : (p.rows + kWaves - 1) / kWaves));
 #define FP8_NORM_CASE(C, W) \
@@ -580,18 +579,34 @@ template <int F>
 hipError_t norm_quant_fmt(const NormFwd& p, hipStream_t st) {
     if (norm_vector_layout(p)) return norm_quant_reg<F, false>(p, st);
     if (p.cols >= 8 && p.cols <= kNormMaxVecCols) return norm_quant_reg<F, true>(p, st);
-    hipLaunchKernelGGL((k_norm_quant_row_any<F>), dim3(row_grid(p.rows)), dim3(kBlock), 0, st, p);
+    hipLaunchKernelGGL((k_norm_quant_row_any<F>), dim3((unsigned)p.rows), dim3(kBlock), 0, st, p);
     return hipGetLastError();
 }
 
-hipError_t launch_norm_quant_row(const NormFwd& p, int fmt, hipStream_t st) {
-    if (p.rows == 0 || p.cols == 0) return hipSuccess;
-    switch (fmt) {
-        case kE4M3: return norm_quant_fmt<kE4M3>(p, st);
-        case kE5M2: return norm_quant_fmt<kE5M2>(p, st);
-        case kE4M3Fnuz: return norm_quant_fmt<kE4M3Fnuz>(p, st);
-        default: return norm_quant_fmt<kE5M2Fnuz>(p, st);
+hipError_t launch_norm_quant_row(const NormFwd& p0, int fmt, hipStream_t st) {
+    for (int64_t r0 = 0; r0 < p0.rows; r0 += kLaunchRows) {
+        NormFwd p = p0;
+        p.rows = p0.rows - r0 < kLaunchRows ? p0.rows - r0 : kLaunchRows;
+        p.x += r0 * p.ldx;
+        if (p.q) p.q += r0 * p.ldq;
+        if (p.scale_inv) p.scale_inv += r0;
+        if (p.y) p.y += r0 * p.ldy;
+        if (p.mean) p.mean += r0;
+        if (p.rstd) p.rstd += r0;
+        if (p.xq) {
+            p.xq += r0 * p.ldxq;
+            p.xs += 4 * r0;
+        }
+        hipError_t e;
+        switch (fmt) {
+            case kE4M3: e = norm_quant_fmt<kE4M3>(p, st); break;
+            case kE5M2: e = norm_quant_fmt<kE5M2>(p, st); break;
+            case kE4M3Fnuz: e = norm_quant_fmt<kE4M3Fnuz>(p, st); break;
+            default: e = norm_quant_fmt<kE5M2Fnuz>(p, st); break;
+        }
+        if (e != hipSuccess) return e;
     }
+    return hipSuccess;
 }
 
 template <int SRC, bool LOOSE>

@@ -104,6 +104,10 @@ __global__ __launch_bounds__(WPR == 1 ? kBlock : WPR * 64) void k_swiglu_quant_r
     }
 }
 
+// Chunks of one launch of the gradient (134 million values, a quarter of a
+// millisecond): longer calls are cut, so that chunk numbers stay 32-bit.
+constexpr int64_t kGradChunks = (int64_t)1 << 24;
+
 // One chunk of 8 columns per thread; no reduction. SRC: 0 = h in bf16, 1 / 2 =
 // the checkpoint in e4m3 / e5m2. Chunk i is chunk i % nch of row i / nch; the
 // quotient is (mulhi(magic, i) + i) >> shift, exact for i < 2^31 (the launcher
@@ -183,14 +187,26 @@ hipError_t swiglu_quant_fmt(const SwigluFwd& p, hipStream_t st) {
     return hipGetLastError();
 }
 
-hipError_t launch_swiglu_quant_row_mx(const SwigluFwd& p, int fmt, hipStream_t st) {
-    if (p.rows == 0 || p.inter == 0) return hipSuccess;
-    switch (fmt) {
-        case kE4M3: return swiglu_quant_fmt<kE4M3>(p, st);
-        case kE5M2: return swiglu_quant_fmt<kE5M2>(p, st);
-        case kE4M3Fnuz: return swiglu_quant_fmt<kE4M3Fnuz>(p, st);
-        default: return swiglu_quant_fmt<kE5M2Fnuz>(p, st);
+hipError_t launch_swiglu_quant_row_mx(const SwigluFwd& p0, int fmt, hipStream_t st) {
+    if (p0.inter == 0) return hipSuccess;
+    for (int64_t r0 = 0; r0 < p0.rows; r0 += kLaunchRows) {
+        SwigluFwd p = p0;
+        p.rows = p0.rows - r0 < kLaunchRows ? p0.rows - r0 : kLaunchRows;
+        p.h += r0 * p.ldh;
+        p.q += r0 * p.ldq;
+        p.scale_inv += r0;
+        p.hq += r0 * p.ldhq;
+        p.hs += 4 * r0;
+        hipError_t e;
+        switch (fmt) {
+            case kE4M3: e = swiglu_quant_fmt<kE4M3>(p, st); break;
+            case kE5M2: e = swiglu_quant_fmt<kE5M2>(p, st); break;
+            case kE4M3Fnuz: e = swiglu_quant_fmt<kE4M3Fnuz>(p, st); break;
+            default: e = swiglu_quant_fmt<kE5M2Fnuz>(p, st); break;
+        }
+        if (e != hipSuccess) return e;
     }
+    return hipSuccess;
 }
 
 hipError_t launch_swiglu_backward(const SwigluBwd& p0, hipStream_t st) {
@@ -199,7 +215,7 @@ hipError_t launch_swiglu_backward(const SwigluBwd& p0, hipStream_t st) {
     int shift = 0;                                          // magic division by nch: 2^shift >= nch
     while (((int64_t)1 << shift) < nch) ++shift;
     const uint32_t magic = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - (uint64_t)nch)) / (uint64_t)nch + 1);
-    const int64_t band = (((int64_t)1 << 31) - kBlock) / nch;
+    const int64_t band = kGradChunks / nch > 0 ? kGradChunks / nch : 1;
     for (int64_t r0 = 0; r0 < p0.rows; r0 += band) {
         SwigluBwd p = p0;
         p.rows = p0.rows - r0 < band ? p0.rows - r0 : band;

@@ -230,3 +230,26 @@ def test_moe_few_in_graphs(fp8, orc):
             run(n, eager, fp8.moe_few_workspace(T, k, inter))
             torch.cuda.synchronize()
             assert torch.equal(o[:n], eager[:n]), (it, n)
+
+
+def test_moe_few_two_streams(fp8, orc):
+    """Two calls at once, each with its own workspace, give the bits of a call alone."""
+    rng = np.random.default_rng(16)
+    d = [make(orc, rng, 12, 2, 6, 512, 256) for _ in range(2)]
+    say("moe few two streams")
+    want = [call(fp8, x) for x in d]
+    args = []
+    for x in d:
+        args.append((dev_bf16(x["x"]), torch.from_numpy(x["idx"]).to(DEV), dev_f32(x["w"]), dev_u8(x["w1"]), 0,
+                     dev_f32(x["sw1"]), dev_u8(x["w2"]), 0, dev_f32(x["sw2"])))
+    outs = [[torch.empty((12, 512), dtype=torch.bfloat16, device=DEV) for _ in range(5)] for _ in d]
+    wss = [fp8.moe_few_workspace(12, 2, 256) for _ in d]
+    streams = [torch.cuda.Stream() for _ in d]
+    torch.cuda.synchronize()
+    for i in range(5):
+        for a, o, w, s in zip(args, outs, wss, streams):
+            with torch.cuda.stream(s):
+                fp8.fp8_moe_few_tokens(*a, o[i], w)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(x, w) for x in o)

@@ -324,3 +324,51 @@ def test_norm_gradient_against_differences(fp8):
     # |y's third| <= 3.5 s3 + 3 s'' < 12; times h^2 / 6.
     tol = np.abs(yv).max() * BF / h + np.abs(diff) * BF + 12 * h * h / 6
     assert np.all(np.abs(dx.double().cpu().numpy()[0] - diff) <= tol)
+
+
+def test_norm_many_rows(fp8):
+    """More rows than one launch takes (2^20): the rows on either side of the cut and
+    the last ones are those of a call on them alone."""
+    rows, cols = (1 << 20) + 37, 64
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    x = torch.randn((rows, cols), device=DEV, generator=g, dtype=torch.bfloat16)
+    say("norm many rows")
+
+    def call(x):
+        n = x.shape[0]
+        q, si, rstd = torch.empty((n, cols), dtype=torch.uint8, device=DEV), torch.empty(n, device=DEV), torch.empty(
+            n, device=DEV)
+        y, xq, xs = torch.empty_like(x), torch.empty_like(q), fp8.mx_scale_records(n, cols)
+        fp8.fp8_norm_quantize_row(x, None, None, 1e-5, fp8.NORM_LAYER, 0, 0, q, si, y=y, rstd_out=rstd, xhat_q=xq,
+                                  xhat_scale=xs)
+        return q, si, rstd, y, xq, xs[0]
+
+    whole = call(x)
+    for lo, hi in ((0, 40), ((1 << 20) - 8, (1 << 20) + 8), (rows - 9, rows)):
+        part = call(x[lo:hi])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[lo:hi], b) for a, b in zip(whole, part)), (lo, hi)
+    dx, dg, db = torch.empty_like(x), torch.empty(cols, device=DEV), torch.empty(cols, device=DEV)
+    mean = torch.zeros(rows, device=DEV)
+    fp8.fp8_norm_backward(x, x, None, mean, whole[2], fp8.NORM_LAYER, dx, dgamma=dg, dbeta=db,
+                          workspace=fp8.norm_workspace(rows, cols))
+    part = torch.empty((9, cols), dtype=torch.bfloat16, device=DEV)
+    fp8.fp8_norm_backward(x[-9:], x[-9:], None, mean[-9:], whole[2][-9:], fp8.NORM_LAYER, part)
+    torch.cuda.synchronize()
+    assert torch.equal(dx[-9:], part)
+    xd = x.double()
+    want, mag = xd.sum(0), xd.abs().sum(0)
+    # a band of 2049 rows is added by 8 teams, 257 rows each in turn, then 512 bands in 16 slices
+    assert torch.all((db.double() - want).abs() <= (257 + 8 + 32 + 16) * layer.U * mag)
+
+
+def test_norm_tensors_of_two_devices_are_refused(fp8):
+    x = torch.zeros((4, 64), dtype=torch.bfloat16, device=DEV)
+    z = torch.zeros(4, device=DEV)
+    with pytest.raises(ValueError, match="on one GPU"):
+        fp8.fp8_norm_backward(x, x, None, z, z, fp8.NORM_LAYER, torch.empty_like(x), dgamma=torch.zeros(64, device=DEV),
+                              workspace=torch.zeros(1024))
+    with pytest.raises(fp8.Fp8Error, match="workspace of 2048 bytes"):
+        fp8.fp8_norm_backward(x, x, None, z, z, fp8.NORM_LAYER, torch.empty_like(x), dgamma=torch.zeros(64, device=DEV),
+                              workspace=torch.zeros(511, device=DEV))

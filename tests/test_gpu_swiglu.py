@@ -202,3 +202,55 @@ def test_swiglu_no_rows(fp8):
     fp8.fp8_swiglu_quantize_row_mx(h, 0, 0, q, torch.empty(0, device=DEV), hq, 0, fp8.mx_scale_records(0, 128))
     fp8.fp8_swiglu_backward(torch.empty((0, 64), dtype=torch.bfloat16, device=DEV), h, torch.empty_like(h))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_swiglu_checkpoint_of_every_value(fp8, fmt):
+    """Every bf16 pattern, 32 neighbours a block (subnormal, Inf and NaN blocks among
+    them), and blocks of one loud value among tiny ones: the checkpoint is
+    fp8_mx_quantize_row's, bit for bit."""
+    bits = np.arange(1 << 16, dtype=np.uint32).astype(np.uint16).reshape(1024, 64)
+    mixed = bits.copy()
+    mixed[:, ::32] = np.random.default_rng(1).permutation(bits.reshape(-1))[:2048].reshape(1024, 2)
+    h = dev_bf16(np.concatenate([bits, mixed]))
+    say("swiglu checkpoint of every value", fmt)
+    q, si = torch.empty((2048, 32), dtype=torch.uint8, device=DEV), torch.empty(2048, device=DEV)
+    hq, rec = torch.empty((2048, 64), dtype=torch.uint8, device=DEV), fp8.mx_scale_records(2048, 64)
+    hq0, rec0 = torch.empty_like(hq), torch.empty_like(rec)
+    fp8.fp8_swiglu_quantize_row_mx(h, 0, 0, q, si, hq, fmt, rec)
+    fp8.fp8_mx_quantize_row(h, fmt, hq0, rec0)
+    torch.cuda.synchronize()
+    assert torch.equal(rec, rec0) and torch.equal(hq, hq0)
+
+
+def test_swiglu_many_rows(fp8):
+    """More rows than one launch takes, forward (2^20 rows) and backward (2^24 chunks
+    of 8): the rows at the cut and the last ones are those of a call on them alone."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    say("swiglu many rows")
+    rows = (1 << 20) + 21
+    h = torch.randn((rows, 64), device=DEV, generator=g, dtype=torch.bfloat16)
+
+    def save(h):
+        n = h.shape[0]
+        q, si = torch.empty((n, 32), dtype=torch.uint8, device=DEV), torch.empty(n, device=DEV)
+        hq, rec = torch.empty((n, 64), dtype=torch.uint8, device=DEV), fp8.mx_scale_records(n, 64)
+        fp8.fp8_swiglu_quantize_row_mx(h, 0, 0, q, si, hq, 0, rec)
+        return q, si, hq, rec[0]
+
+    whole = save(h)
+    for lo, hi in (((1 << 20) - 8, (1 << 20) + 8), (rows - 9, rows)):
+        part = save(h[lo:hi])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[lo:hi], b) for a, b in zip(whole, part)), (lo, hi)
+    rows = (1 << 24) + 300
+    h = torch.randn((rows, 16), device=DEV, generator=g, dtype=torch.bfloat16)
+    dh, a = torch.empty_like(h), torch.empty((rows, 8), dtype=torch.bfloat16, device=DEV)
+    fp8.fp8_swiglu_backward(h[:, :8], h, dh, a=a)
+    for lo, hi in ((0, 8), ((1 << 24) - 8, (1 << 24) + 8), (rows - 9, rows)):
+        pd, pa = torch.empty((hi - lo, 16), dtype=torch.bfloat16, device=DEV), torch.empty(
+            (hi - lo, 8), dtype=torch.bfloat16, device=DEV)
+        fp8.fp8_swiglu_backward(h[lo:hi, :8], h[lo:hi], pd, a=pa)
+        torch.cuda.synchronize()
+        assert torch.equal(dh[lo:hi], pd) and torch.equal(a[lo:hi], pa), (lo, hi)
