@@ -8,6 +8,9 @@ library is missing or fails to load, importing this package raises.
 
 bf16 inputs are torch.bfloat16 tensors; FP8 codes are any 1-byte tensors
 (torch.uint8 or a torch.float8_* dtype); scales and amax are float32.
+
+The functions from fp8_norm_quantize_row on also check that every tensor has
+its shape and is on one GPU, which they make the current device for the call.
 """
 import ctypes
 import os
@@ -586,7 +589,8 @@ def fp8_norm_quantize_row(x, gamma, beta, eps, kind, fmt, margin, q, scale_inv_o
     [rows] (both None to skip), y bf16 (or None). gamma, beta [cols]: bf16 or
     fp32, None for 1 and 0. mean_out, rstd_out fp32 [rows] (or None); xhat_q
     codes and xhat_scale records (mx_scale_records) save the normalised rows in
-    8 bits for fp8_mx_norm_backward (cols % 32 == 0)."""
+    8 bits for fp8_mx_norm_backward (cols % 32 == 0). No output may overlap
+    another or an input."""
     rows, cols, ldx = _rows(x, "x")
     w_type = _norm_weights(gamma, beta, cols)
     ldq = _like(q, "q", rows, cols, 1) if q is not None else cols
@@ -621,7 +625,8 @@ def fp8_norm_backward(dy, x, gamma, mean, rstd, kind, dx, dgamma=None, dbeta=Non
     """Gradients of fp8_norm_quantize_row's y: dx bf16 [rows x cols] and, if given,
     dgamma, dbeta fp32 [cols] (overwritten), from dy and x bf16 [rows x cols] and
     the forward pass's mean and rstd (mean None for NORM_RMS). workspace
-    (norm_workspace) is needed with dgamma or dbeta."""
+    (norm_workspace) is needed with dgamma or dbeta; calls that may run at the
+    same time need one each. No output may overlap another or an input."""
     rows, cols, lddy = _rows(dy, "dy")
     ldx, lddx = _like(x, "x", rows, cols), _like(dx, "dx", rows, cols)
     w_type = _norm_weights(gamma, None, cols)
@@ -699,7 +704,8 @@ def fp8_moe_few_tokens(x, expert_idx, weights, w1, f1, w1_scale_inv, w2, f2, w2_
     """The MoE layer for at most MOE_FEW_TOKENS tokens: x, out bf16 [T x H];
     expert_idx int32, weights fp32 [T x k]; w1 codes [E x 2I x H] (gate rows, then
     up rows) with w1_scale_inv fp32 [E x 2I]; w2 codes [E x H x I] with
-    w2_scale_inv fp32 [E x H]; workspace: moe_few_workspace(T, k, I)."""
+    w2_scale_inv fp32 [E x H]; workspace: moe_few_workspace(T, k, I), one for each
+    call that may run at the same time."""
     T, H, ldx = _rows(x, "x")
     k = _i32_2d(expert_idx, "expert_idx")[1]
     if expert_idx.shape[0] != T:

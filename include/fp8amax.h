@@ -521,12 +521,14 @@ typedef enum { FP8_NORM_LAYER = 0, FP8_NORM_RMS = 1 } fp8_norm_t;
  *    is then ignored). Saving xhat instead of x keeps the checkpoint's error
  *    relative to the normalised value whatever the row's mean and scale.
  * cols >= 1; rows < 2^30 (else FP8_ERR_UNSUPPORTED); eps >= 0 and finite;
- * margin 0..32; x, y 2-byte aligned, gamma / beta to their type. Vector path
- * when x, y, gamma, beta are 16-byte and q 8-byte aligned, ldx, ldy, ldq, cols
- * multiples of 8 and cols <= 16384; any other layout takes a scalar path. The
- * checkpoint needs the vector path (else FP8_ERR_ALIGNMENT, or
- * FP8_ERR_UNSUPPORTED for cols > 16384), cols % 32 == 0 (else
- * FP8_ERR_INVALID_ARG), xhat_q 8-byte aligned, ldxq % 8 == 0 and xhat_scale
+ * margin 0..32; x, y 2-byte aligned, gamma / beta to their type. Rows of up to
+ * 16384 columns are read once, in 16-byte accesses when x, y, gamma, beta are
+ * 16-byte and q 8-byte aligned and ldx, ldy, ldq, cols multiples of 8, else in
+ * unaligned ones (about half the speed); longer rows, and rows of fewer than 8
+ * columns, are read again for each pass. The checkpoint needs the aligned
+ * layout (else FP8_ERR_ALIGNMENT, or FP8_ERR_UNSUPPORTED for cols > 16384),
+ * cols % 32 == 0 (else FP8_ERR_INVALID_ARG), xhat_q 8-byte aligned, ldxq % 8
+ * == 0 and xhat_scale
  * 4-byte aligned. Outputs do not overlap each other or the inputs. */
 fp8_status_t fp8_norm_quantize_row(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, const void* gamma,
                                    const void* beta, fp8_out_t w_type, float eps, fp8_norm_t kind, fp8_format_t fmt,
@@ -551,8 +553,8 @@ int64_t fp8_norm_backward_workspace(int64_t rows, int64_t cols);
  * may be NULL when dgamma and dbeta are. It is free for other use once the
  * call's work is done; calls that may run at the same time need one each.
  * Results do not depend on timing (no atomics). Sizes and layouts as the
- * forward pass (vector and scalar path). Outputs do not overlap each other or
- * the inputs. */
+ * forward pass. Outputs do not overlap each other or the inputs (dx may not
+ * take dy's place). */
 fp8_status_t fp8_norm_backward(const uint16_t* dy, int64_t rows, int64_t cols, int64_t lddy, const uint16_t* x,
                                int64_t ldx, const void* gamma, fp8_out_t w_type, const float* mean, const float* rstd,
                                fp8_norm_t kind, uint16_t* dx, int64_t lddx, float* dgamma, float* dbeta,
