@@ -2,6 +2,7 @@
 // norm and its gradient, SwiGLU with checkpoints and its gradient, the MoE
 // layer for a few tokens. Argument validation before any launch, then dispatch.
 #include "checks.hpp"
+#include "layer.hpp"
 
 #include <cmath>
 

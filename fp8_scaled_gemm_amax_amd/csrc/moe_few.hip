@@ -18,7 +18,7 @@
 // K runs in lane order, not memory order: lane l of a 64-byte step of a row
 // holds its bytes 16 (l / 16) .. + 15, and the token's values are read in the
 // same order, so that a lane's 16 bytes are one load.
-#include "kernels.hpp"
+#include "layer.hpp"
 #include "layer_device.hpp"
 
 namespace fp8amax {

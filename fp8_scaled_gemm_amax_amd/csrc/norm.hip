@@ -10,7 +10,7 @@
 //
 // Everything here is bound by HBM: the rows are held in registers from their
 // one read to their last use, and all statistics and sums are fp32.
-#include "kernels.hpp"
+#include "layer.hpp"
 #include "layer_device.hpp"
 
 namespace fp8amax {

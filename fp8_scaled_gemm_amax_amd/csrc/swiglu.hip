@@ -6,7 +6,7 @@
 //   backward: du = da silu(g), dg = da u sigma(g) (1 + g (1 - sigma(g)))
 //
 // Bound by HBM: one read of the inputs, one write of the outputs.
-#include "kernels.hpp"
+#include "layer.hpp"
 #include "layer_device.hpp"
 
 namespace fp8amax {

@@ -10,6 +10,7 @@
 #include <cstring>
 
 #include "../fp8_scaled_gemm_amax_amd/csrc/checks.hpp"
+#include "../fp8_scaled_gemm_amax_amd/csrc/layer.hpp"
 
 static int g_fail = 0, g_launched = 0;
 #define CHECK(cond)                                                         \
