@@ -17,7 +17,7 @@
 //
 // K runs in lane order, not memory order: lane l of a 64-byte step of a row
 // holds its bytes 16 (l / 16) .. + 15, and the token's values are read in the
-// same order, so that a lane's 16 bytes are one load.
+// same order, so that a lane's 16 bytes are one access.
 #include "layer.hpp"
 #include "layer_device.hpp"
 
@@ -76,6 +76,43 @@ __device__ __forceinline__ v8bf load_acts_if(bool in, const uint16_t* p) {
     if (in) v = *reinterpret_cast<const v4u*>(p);
     return __builtin_bit_cast(v8bf, v);
 }
+
+// A tile of 16 weight rows by a block of kStep * U bytes of each, on its way from
+// memory to the matrix cores. Loads take a row's bytes in order (16 U lanes a
+// row); the cores want lane l to hold bytes 16 (l / 16) .. + 15 of a 64-byte step of
+// row l % 16. The wavefront turns the one into the other through LDS of its own
+// (no barrier: a wavefront's LDS accesses happen in order), the chunks of a row
+// exchanged such that neither side meets a bank twice. Loading them as the cores
+// want them (16 rows a load, 64 bytes of each) took one token 69.5 us instead of
+// TIME1, 32 tokens 286 instead of TIME2.
+template <int U>
+struct RowTile {
+    static constexpr int kChunks = 4 * U, kRowsPerLoad = 16 / U, kWords = 64 * U;     // kWords: 16-byte words of LDS
+    static __device__ __forceinline__ int place(int row, int chunk) {
+        return row * kChunks + (chunk ^ ((row * U) >> 2));
+    }
+    // this lane's first address in the tile whose first row is at `rows`
+    static __device__ __forceinline__ const uint8_t* lane(const uint8_t* rows, int64_t ld) {
+        const int l = threadIdx.x & 63;
+        return rows + (l / kChunks) * ld + (l % kChunks) * 16;
+    }
+    static __device__ __forceinline__ void load(const uint8_t* lane, int64_t ld, int k, uint4* w) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) w[i] = load_weights(lane + i * kRowsPerLoad * ld + k);
+    }
+    static __device__ __forceinline__ void put(uint4* lds, const uint4* w) {
+        const int l = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < U; ++i) lds[place(i * kRowsPerLoad + l / kChunks, l % kChunks)] = w[i];
+    }
+    static __device__ __forceinline__ uint4 get(const uint4* lds, int s) {
+        const int l = threadIdx.x & 63;
+        return lds[place(l & 15, s * 4 + (l >> 4))];
+    }
+};
+// Orders this wavefront's LDS accesses on either side for the compiler (the
+// hardware keeps their order).
+__device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // Copies the entries' experts to LDS (-1 for one out of range) and sets the bits
 // of those named (all threads; ends with a barrier).
@@ -174,21 +211,22 @@ constexpr int kUpWaves = 4;
 
 // Sums of 2 RT tiles of weight rows (gate and up) against the tokens of tiles
 // 0 .. NT-1 (NT * 16 entries) over this wavefront's share of K.
+// wp: first row of each tile; stage: this wavefront's LDS, 2 RT tiles.
 template <int F, int RT, int NT, int U>
-__device__ __forceinline__ void up_sums(const uint8_t* const* wp, const uint16_t* const* xp, int K, int wave,
-                                        v4f (*acc)[NT]) {
+__device__ __forceinline__ void up_sums(const uint8_t* const* wp, int64_t ld, const uint16_t* const* xp, int K, int wave,
+                                        uint4* stage, v4f (*acc)[NT]) {
+    using Tile = RowTile<U>;
     const int j16 = ((threadIdx.x & 63) >> 4) * 16;
     const int whole = K / (kStep * U);
+    const uint8_t* lp[2 * RT];
     uint4 w[2 * RT][U];
-    if (wave < whole) {
 #pragma unroll
-        for (int s = 0; s < U; ++s)
-#pragma unroll
-            for (int r = 0; r < 2 * RT; ++r) w[r][s] = load_weights(wp[r] + wave * (kStep * U) + j16 + s * kStep);
+    for (int r = 0; r < 2 * RT; ++r) {
+        lp[r] = Tile::lane(wp[r], ld);
+        if (wave < whole) Tile::load(lp[r], ld, wave * (kStep * U), w[r]);
     }
     for (int b = wave; b < whole; b += kUpWaves) {
         const int k0 = b * (kStep * U) + j16;
-        const int kn = k0 + kUpWaves * (kStep * U);
         v8bf x[NT][U][2];
         uint4 wn[2 * RT][U];
 #pragma unroll
@@ -201,24 +239,31 @@ __device__ __forceinline__ void up_sums(const uint8_t* const* wp, const uint16_t
         __builtin_amdgcn_sched_barrier(0);
         if (b + kUpWaves < whole) {
 #pragma unroll
-            for (int s = 0; s < U; ++s)
-#pragma unroll
-                for (int r = 0; r < 2 * RT; ++r) wn[r][s] = load_weights(wp[r] + kn + s * kStep);
+            for (int r = 0; r < 2 * RT; ++r) Tile::load(lp[r], ld, (b + kUpWaves) * (kStep * U), wn[r]);
         }
         __builtin_amdgcn_sched_barrier(0);
+        wave_lds_fence();
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r) Tile::put(stage + r * Tile::kWords, w[r]);
+        wave_lds_fence();
 #pragma unroll
         for (int s = 0; s < U; ++s)
 #pragma unroll
             for (int r = 0; r < 2 * RT; ++r) {
-                const v8bf w0 = decode_bf16<F>(w[r][s].x, w[r][s].y), w1 = decode_bf16<F>(w[r][s].z, w[r][s].w);
+                const uint4 v = Tile::get(stage + r * Tile::kWords, s);
+                const v8bf w0 = decode_bf16<F>(v.x, v.y), w1 = decode_bf16<F>(v.z, v.w);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     acc[r][n] = mfma(w0, x[n][s][0], acc[r][n]);
                     acc[r][n] = mfma(w1, x[n][s][1], acc[r][n]);
                 }
-                w[r][s] = wn[r][s];
             }
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r)
+#pragma unroll
+            for (int i = 0; i < U; ++i) w[r][i] = wn[r][i];
     }
+    wave_lds_fence();
     // what is left of K, 64 bytes a step, the last step's lanes past K zero on both sides
     const int left0 = whole * U, steps = (K + kStep - 1) / kStep;
     for (int st = left0 + (wave + kUpWaves - whole % kUpWaves) % kUpWaves; st < steps; st += kUpWaves) {
@@ -226,7 +271,7 @@ __device__ __forceinline__ void up_sums(const uint8_t* const* wp, const uint16_t
         const bool in = k < K;
 #pragma unroll
         for (int r = 0; r < 2 * RT; ++r) {
-            const uint4 wl = load_weights_if(in, wp[r] + k);
+            const uint4 wl = load_weights_if(in, wp[r] + (threadIdx.x & 15) * ld + k);
             const v8bf w0 = decode_bf16<F>(wl.x, wl.y), w1 = decode_bf16<F>(wl.z, wl.w);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -235,6 +280,12 @@ __device__ __forceinline__ void up_sums(const uint8_t* const* wp, const uint16_t
             }
         }
     }
+}
+
+// Floats of LDS of a wavefront: 2 RT tiles of U KB of weights, or of NT KB of sums.
+template <int RT, int NT, int U>
+constexpr int up_part() {
+    return 2 * RT * 256 * (NT > U ? NT : U);
 }
 
 // One workgroup's columns for NT tiles of entries.
@@ -246,7 +297,7 @@ __device__ __forceinline__ void up_tile(const MoeFew& p, const int16_t* idx, int
     const uint8_t* wp[2 * RT];                              // gate tile, up tile, gate tile, ..
 #pragma unroll
     for (int r = 0; r < 2 * RT; ++r)
-        wp[r] = we + (int64_t)((r & 1) * p.inter + c0 + (r >> 1) * 16 + (lane & 15)) * p.ld1;
+        wp[r] = we + (int64_t)((r & 1) * p.inter + c0 + (r >> 1) * 16) * p.ld1;
     const uint16_t* xp[NT];
     v4f acc[2 * RT][NT];
 #pragma unroll
@@ -272,14 +323,16 @@ __device__ __forceinline__ void up_tile(const MoeFew& p, const int16_t* idx, int
         for (int j = slot + 1; j < p.topk; ++j)
             if (idx[token * p.topk + j] == e) share[n] += p.weights[token * p.topk + j];
     }
-    up_sums<F, RT, NT, U>(wp, xp, p.hidden, wave, acc);
-    // red[wave][tile of entries][row tile][column * 16 + row], row = 4 (lane / 16) + i
+    // A wavefront's part of red holds its tiles of weights, then its sums: [tile of
+    // entries][row tile][column * 16 + row], row = 4 (lane / 16) + i.
+    constexpr int kPart = up_part<RT, NT, U>();
+    float* mine = red + wave * kPart;
+    up_sums<F, RT, NT, U>(wp, p.ld1, xp, p.hidden, wave, reinterpret_cast<uint4*>(mine), acc);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 2 * RT; ++r)
-            *reinterpret_cast<v4f*>(red + ((wave * NT + n) * 2 * RT + r) * 256 + (lane & 15) * 16 + (lane >> 4) * 4) =
-                acc[r][n];
+            *reinterpret_cast<v4f*>(mine + (n * 2 * RT + r) * 256 + (lane & 15) * 16 + (lane >> 4) * 4) = acc[r][n];
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -293,8 +346,8 @@ __device__ __forceinline__ void up_tile(const MoeFew& p, const int16_t* idx, int
             float g = 0.0f, u = 0.0f;
 #pragma unroll
             for (int w = 0; w < kUpWaves; ++w) {
-                g += red[((w * NT + n) * 2 * RT + 2 * r) * 256 + threadIdx.x];
-                u += red[((w * NT + n) * 2 * RT + 2 * r + 1) * 256 + threadIdx.x];
+                g += red[w * kPart + (n * 2 * RT + 2 * r) * 256 + threadIdx.x];
+                u += red[w * kPart + (n * 2 * RT + 2 * r + 1) * 256 + threadIdx.x];
             }
             const float a = silu_fast(g * factor[2 * r]) * (u * factor[2 * r + 1]) * share[n];
             const uint32_t hi = f32_to_bf16(a);
@@ -312,7 +365,8 @@ template <int F, int RT, int NTMAX>
 __global__ __launch_bounds__(kUpWaves * 64) void k_moe_few_up(MoeFew p) {
     __shared__ uint32_t bits[kMaxWords];
     __shared__ int16_t idx[NTMAX * 16 * kMoeMaxTopk];
-    __shared__ __attribute__((aligned(16))) float red[kUpWaves * NTMAX * 2 * RT * 256];
+    constexpr int U1 = RT == 1 ? 4 : 2, kPart = NTMAX >= 4 ? up_part<RT, 4, U1>() : up_part<RT, NTMAX, U1>();
+    __shared__ __attribute__((aligned(16))) float red[kUpWaves * kPart];
     const int lane = threadIdx.x & 63;
     read_entries(p, idx, bits);
     const uint32_t word = lane < kMaxWords ? bits[lane] : 0u;
@@ -339,7 +393,7 @@ __global__ __launch_bounds__(kUpWaves * 64) void k_moe_few_up(MoeFew p) {
             return;
         }
     }
-    up_tile<F, RT, 1, RT == 1 ? 4 : 2>(p, idx, e, c0, ent, red);
+    up_tile<F, RT, 1, U1>(p, idx, e, c0, ent, red);
 }
 
 // -------------------------------------------------------------------- down --
@@ -353,52 +407,69 @@ constexpr int kDownWaves = 8;
 
 // Products of RT * 16 weight rows with the entries of tiles 0 .. NT-1 over the
 // blocks b0, b0 + db, .. of K.
+// wp: first row of each tile; stage: this wavefront's LDS, RT tiles.
 template <int F, int RT, int NT, int U>
-__device__ __forceinline__ void down_sums(const uint8_t* const* wp, const ActTile* tile, const int* col, int K, int b0,
-                                          int db, v4f (*acc)[NT]) {
+__device__ __forceinline__ void down_sums(const uint8_t* const* wp, int64_t ld, const ActTile* tile, const int* col, int K,
+                                          int b0, int db, uint4* stage, v4f (*acc)[NT]) {
+    using Tile = RowTile<U>;
     const int j = (threadIdx.x & 63) >> 4, j16 = j * 16;
     const int whole = K / (kStep * U);
+    const uint8_t* lp[RT];
     uint4 w[RT][U];
-    if (b0 < whole) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int s = 0; s < U; ++s) w[r][s] = load_weights(wp[r] + b0 * (kStep * U) + s * kStep + j16);
+    for (int r = 0; r < RT; ++r) {
+        lp[r] = Tile::lane(wp[r], ld);
+        if (b0 < whole) Tile::load(lp[r], ld, b0 * (kStep * U), w[r]);
     }
-    int b = b0;
-    for (; b < whole; b += db) {
-        const int k0 = b * (kStep * U) + j16;
-        const int kn = k0 + db * (kStep * U);
-        v8bf a[NT][U][2];
-        uint4 wn[RT][U];
+    constexpr int G = NT > 4 ? 4 : NT;                      // tiles at a time (eight's activations do not fit)
+    v8bf a[G][U][2];
+    auto load_tiles = [&](int b, int n0) {
 #pragma unroll
         for (int s = 0; s < U; ++s)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < G; ++n)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)                 // (a whole step: 4 groups)
-                    a[n][s][h] = load_acts(tile[n].base + (b * U + s) * 128 * tile[n].w + h * 64 * tile[n].w + col[n]);
+                for (int h = 0; h < 2; ++h) {               // (a whole step: 4 groups)
+                    const ActTile& t = tile[n0 + n];
+                    a[n][s][h] = load_acts(t.base + (b * U + s) * 128 * t.w + h * 64 * t.w + col[n0 + n]);
+                }
+    };
+    int b = b0;
+    for (; b < whole; b += db) {
+        uint4 wn[RT][U];
+        load_tiles(b, 0);
         __builtin_amdgcn_sched_barrier(0);
         if (b + db < whole) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int s = 0; s < U; ++s) wn[r][s] = load_weights(wp[r] + kn + s * kStep);
+            for (int r = 0; r < RT; ++r) Tile::load(lp[r], ld, (b + db) * (kStep * U), wn[r]);
         }
         __builtin_amdgcn_sched_barrier(0);
+        wave_lds_fence();
 #pragma unroll
-        for (int s = 0; s < U; ++s)
+        for (int r = 0; r < RT; ++r) Tile::put(stage + r * Tile::kWords, w[r]);
+        wave_lds_fence();
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const v8bf w0 = decode_bf16<F>(w[r][s].x, w[r][s].y), w1 = decode_bf16<F>(w[r][s].z, w[r][s].w);
+        for (int n0 = 0; n0 < NT; n0 += G) {
+            if (n0 > 0) load_tiles(b, n0);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    acc[r][n] = mfma(w0, a[n][s][0], acc[r][n]);
-                    acc[r][n] = mfma(w1, a[n][s][1], acc[r][n]);
+            for (int s = 0; s < U; ++s)
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const uint4 v = Tile::get(stage + r * Tile::kWords, s);
+                    const v8bf w0 = decode_bf16<F>(v.x, v.y), w1 = decode_bf16<F>(v.z, v.w);
+#pragma unroll
+                    for (int n = 0; n < G; ++n) {
+                        acc[r][n0 + n] = mfma(w0, a[n][s][0], acc[r][n0 + n]);
+                        acc[r][n0 + n] = mfma(w1, a[n][s][1], acc[r][n0 + n]);
+                    }
                 }
-                w[r][s] = wn[r][s];
-            }
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < U; ++i) w[r][i] = wn[r][i];
     }
+    wave_lds_fence();
     if (b * (kStep * U) >= K) return;                       // (the last, partial block is this wavefront's or another's)
     for (int k = b * (kStep * U) + j16; k - j16 < K; k += kStep) {
         const bool in = k < K;
@@ -411,7 +482,7 @@ __device__ __forceinline__ void down_sums(const uint8_t* const* wp, const ActTil
             for (int h = 0; h < 2; ++h) a[h] = load_acts_if(in, tile[n].base + tile[n].offset(k >> 6, h, j, part, c));
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const uint4 wl = load_weights_if(in, wp[r] + k);
+                const uint4 wl = load_weights_if(in, wp[r] + (threadIdx.x & 15) * ld + k);
                 const v8bf w0 = decode_bf16<F>(wl.x, wl.y), w1 = decode_bf16<F>(wl.z, wl.w);
                 acc[r][n] = mfma(w0, a[0], acc[r][n]);
                 acc[r][n] = mfma(w1, a[1], acc[r][n]);
@@ -423,16 +494,21 @@ __device__ __forceinline__ void down_sums(const uint8_t* const* wp, const ActTil
 // One unit for NT tiles of entries; sums: this wavefront's [token][RT * 16].
 template <int F, int RT, int NT, int U>
 __device__ __forceinline__ void down_unit(const MoeFew& p, int e, int row0, const Entries& ent, int b0, int db,
-                                          float* sums) {
+                                          uint4* stage, float* sums) {
     const int lane = threadIdx.x & 63;
     const uint8_t* we = p.w2 + (int64_t)e * p.gs2;
     const uint8_t* wp[RT];
     v4f acc[RT][NT], sc[RT];
+    auto load_factors = [&]() {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[r][i] = p.s2[(int64_t)e * p.hidden + row0 + r * 16 + (lane >> 4) * 4 + i];
+    };
+    if (NT <= 4) load_factors();                            // (eight tiles leave no registers for them)
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        wp[r] = we + (int64_t)(row0 + r * 16 + (lane & 15)) * p.ld2;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[r][i] = p.s2[(int64_t)e * p.hidden + row0 + r * 16 + (lane >> 4) * 4 + i];
+        wp[r] = we + (int64_t)(row0 + r * 16) * p.ld2;
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[r][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -445,7 +521,8 @@ __device__ __forceinline__ void down_unit(const MoeFew& p, int e, int row0, cons
         const int c = lane & 7, part = (lane >> 3) & 1;     // (columns past the entries are not used)
         col[n] = (((lane >> 4) * 2 + part) * tile[n].w + (c < tile[n].w ? c : 0)) * 8;
     }
-    down_sums<F, RT, NT, U>(wp, tile, col, p.inter, b0, db, acc);
+    down_sums<F, RT, NT, U>(wp, p.ld2, tile, col, p.inter, b0, db, stage, acc);
+    if (NT > 4) load_factors();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int c = n * kActTile + (lane & 7);
@@ -474,6 +551,7 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_moe_few_down(MoeFew p) {
     __shared__ int16_t idx[TT * kMoeMaxTopk];
     __shared__ uint16_t list[kMoeMaxExperts];
     __shared__ __attribute__((aligned(16))) float red[kDownWaves * W];
+    __shared__ uint4 tiles[kDownWaves * RT * RowTile<4>::kWords];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int i = threadIdx.x; i < kDownWaves * W; i += kDownWaves * 64) red[i] = 0.0f;
     read_entries(p, idx, bits);
@@ -488,14 +566,15 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_moe_few_down(MoeFew p) {
     int pieces = total > 0 ? kDownWaves / total : 1;
     pieces = pieces < 1 ? 1 : (pieces > blocks ? blocks : pieces);
     float* sums = red + wave * W;
+    uint4* stage = tiles + wave * (RT * RowTile<4>::kWords);
     for (int unit = wave; unit < total * pieces; unit += kDownWaves) {
         const int e = __builtin_amdgcn_readfirstlane(list[unit / pieces]);
         const Entries ent = find_entries(p, idx, e);
         const int b0 = unit % pieces;
-        if (TT > 32 && ent.count > 32) down_unit<F, RT, 8, 1>(p, e, row0, ent, b0, pieces, sums);
-        else if (TT > 16 && ent.count > 16) down_unit<F, RT, 4, 2>(p, e, row0, ent, b0, pieces, sums);
-        else if (ent.count > 8) down_unit<F, RT, 2, 4>(p, e, row0, ent, b0, pieces, sums);
-        else down_unit<F, RT, 1, 4>(p, e, row0, ent, b0, pieces, sums);
+        if (TT > 32 && ent.count > 32) down_unit<F, RT, 8, 1>(p, e, row0, ent, b0, pieces, stage, sums);
+        else if (TT > 16 && ent.count > 16) down_unit<F, RT, 4, 2>(p, e, row0, ent, b0, pieces, stage, sums);
+        else if (ent.count > 8) down_unit<F, RT, 2, 4>(p, e, row0, ent, b0, pieces, stage, sums);
+        else down_unit<F, RT, 1, 4>(p, e, row0, ent, b0, pieces, stage, sums);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < p.tokens * (RT * 16); i += kDownWaves * 64) {
