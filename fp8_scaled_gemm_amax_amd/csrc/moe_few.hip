@@ -56,11 +56,12 @@ __device__ __forceinline__ v4f mfma(v8bf a, v8bf b, v4f c) {
 constexpr int kStep = 64;                   // bytes of a weight row per load of a wavefront
 constexpr int kMaxWords = kMoeMaxExperts / 32;
 
-// (Through the caches: a row's 64 bytes of one step and of the next share a
-// line, which a nontemporal load does not keep; 32 tokens, 32 experts of 7168 x
-// 2048: 384 us with nontemporal loads, 334 us without.)
 __device__ __forceinline__ uint4 load_weights(const uint8_t* p) {
     return *reinterpret_cast<const uint4*>(p);
+}
+__device__ __forceinline__ uint4 load_weights_once(const uint8_t* p) {
+    const v4u v = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p));
+    return make_uint4(v.x, v.y, v.z, v.w);
 }
 __device__ __forceinline__ v8bf load_acts(const uint16_t* p) {
     return __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(p));
@@ -83,8 +84,13 @@ __device__ __forceinline__ v8bf load_acts_if(bool in, const uint16_t* p) {
 // row l % 16. The wavefront turns the one into the other through LDS of its own
 // (no barrier: a wavefront's LDS accesses happen in order), the chunks of a row
 // exchanged such that neither side meets a bank twice. Loading them as the cores
-// want them (16 rows a load, 64 bytes of each) took one token 69.5 us instead of
-// TIME1, 32 tokens 286 instead of TIME2.
+// want them (16 rows a load, 64 bytes of each) took, of 32 experts of 7168 x 2048,
+// one token 69.7 us instead of 67.2 and 64 tokens 332 instead of 303.
+// Loads of whole lines (U >= 2) leave no copy in the caches: a layer's weights are
+// used once a call, and the tokens' values stay (one token 67.1 -> 62.0 us, 32
+// tokens 264 -> 247; where all weights of a few small experts could have stayed
+// from the call before, 3 tokens of 8 experts of 2048 x 1408, 17.4 -> 19.0).
+// Half lines go through the caches, since the other half follows.
 template <int U>
 struct RowTile {
     static constexpr int kChunks = 4 * U, kRowsPerLoad = 16 / U, kWords = 64 * U;     // kWords: 16-byte words of LDS
@@ -98,7 +104,10 @@ struct RowTile {
     }
     static __device__ __forceinline__ void load(const uint8_t* lane, int64_t ld, int k, uint4* w) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) w[i] = load_weights(lane + i * kRowsPerLoad * ld + k);
+        for (int i = 0; i < U; ++i) {
+            const uint8_t* p = lane + i * kRowsPerLoad * ld + k;
+            w[i] = U >= 2 ? load_weights_once(p) : load_weights(p);
+        }
     }
     static __device__ __forceinline__ void put(uint4* lds, const uint4* w) {
         const int l = threadIdx.x & 63;
@@ -180,7 +189,8 @@ __device__ __forceinline__ Entries find_entries(const MoeFew& p, const int16_t* 
 // columns 0..7 of the product, the low ones columns 8..15. (Rows of K per token
 // made every load 16 lines: 32 tokens, 32 experts of 7168 x 2048, the down
 // product 150 us, without its loads of activations 86; tiles of 16 tokens with
-// one load for either part 108, these 105; one token 30 and 25.) The last step of K has K / 16 % 4
+// one load for either part 108, these 105; one token 30 and 25; all of them with
+// the weights loaded as the cores want them.) The last step of K has K / 16 % 4
 // groups. The tiles of all experts add up to at most tokens * topk rows of
 // 2 * inter values.
 constexpr int kActTile = 8;
@@ -592,9 +602,9 @@ hipError_t moe_few_up(const MoeFew& p, hipStream_t st) {
     const int entries = p.tokens * p.topk;
     const unsigned experts = (unsigned)(entries < p.experts ? entries : p.experts);
     // Two row tiles where that leaves four workgroups per CU and an expert has
-    // four tokens or more on average (32 experts of 7168 x 2048: 64 tokens 383 us
-    // for both launches with one tile, 338 with two; 4096 x 1536, 8 tokens, 128 and
-    // 131 us).
+    // four tokens or more on average (32 experts of 7168 x 2048: 64 tokens 344 us
+    // for both launches with one tile, 303 with two; 4096 x 1536, 8 tokens, 108 and
+    // 114 us).
     const bool two = p.inter % 32 == 0 && (int64_t)(p.inter / 32) * experts >= 1024 && entries >= 4 * (int)experts;
     const dim3 grid((unsigned)(p.inter / (two ? 32 : 16)), experts), block(kUpWaves * 64);
 #define FP8_UP(R, N) hipLaunchKernelGGL((k_moe_few_up<F, R, N>), grid, block, 0, st, p)
@@ -623,9 +633,9 @@ hipError_t launch_moe_few_tokens(const MoeFew& p, int f1, int f2, hipStream_t st
     const hipError_t e = f1 == kE4M3 ? moe_few_up<kE4M3>(p, st) : moe_few_up<kE5M2>(p, st);
     if (e != hipSuccess) return e;
     // 32 rows a workgroup where that leaves most CUs one: an activation load serves
-    // two of weights (32 tokens, 32 experts of 7168 x 2048: 290 us for both
-    // launches, 322 with 16 rows); below, twice the workgroups count for more (4096 x
-    // 1536, 8 tokens: 142 us with 32 rows, 128 with 16).
+    // two of weights (64 tokens, 32 experts of 7168 x 2048: 303 us for both
+    // launches, 363 with 16 rows); below, twice the workgroups count for more (4096 x
+    // 1536, 8 tokens: 120 us with 32 rows, 108 with 16).
     const bool wide = p.hidden % 32 == 0 && p.hidden >= 32 * 160;
     if (f2 == kE4M3) return wide ? moe_few_down<kE4M3, 2>(p, st) : moe_few_down<kE4M3, 1>(p, st);
     return wide ? moe_few_down<kE5M2, 2>(p, st) : moe_few_down<kE5M2, 1>(p, st);
