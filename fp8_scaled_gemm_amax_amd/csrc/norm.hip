@@ -366,8 +366,9 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
         for (int c = 0; c < MAXC; ++c) {
             const uint32_t ch = tt + c * TPR;
             const bool live = live_row && ch < nch;
-            // Past the row (or the band) dy counts as 0: every term of the sums is then
-            // 0, or NaN where the row's own duplicated values give NaN anyway.
+            // Past the row dy counts as 0: every term of the sums is then 0, or NaN
+            // where the row's own duplicated values give NaN anyway. (A row past the
+            // band is worked on and used nowhere.)
             if (LOOSE && live) {
                 uint4 x = make_uint4(cur.x[c][0], cur.x[c][1], cur.x[c][SRC == 0 ? 2 : 0], cur.x[c][SRC == 0 ? 3 : 0]);
                 place_chunk<LOOSE>(&cur.dy[c], ch, n);
@@ -424,10 +425,12 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = cur.rstd * (fmaf(-c1, xh[i], dy[i] * g[c][i]) - c2);
             if (live) store_chunk<LOOSE>(p.dx + row * p.lddx, ch, n, o);
+            if (live_row) {         // (uniform; the duplicate of a row could add 0 * Inf)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                dg[c][i] = fmaf(dy[i], xh[i], dg[c][i]);
-                db[c][i] += dy[i];
+                for (int i = 0; i < 8; ++i) {
+                    dg[c][i] = fmaf(dy[i], xh[i], dg[c][i]);
+                    db[c][i] += dy[i];
+                }
             }
         }
         cur = nxt;

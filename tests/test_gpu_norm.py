@@ -276,6 +276,34 @@ def test_norm_backward_checkpoint_nan_block(fp8):
     assert np.array_equal(torch.isnan(dg).cpu().numpy(), np.arange(cols) // 32 == 5)
 
 
+def test_norm_backward_inf_in_an_odd_row(fp8):
+    """An Inf in the last columns of a band's last row (RMS: rstd is 0 there and xhat
+    NaN in that column alone): dgamma is NaN in that column alone, also where
+    threads without a row of their own read that row again."""
+    rows, cols, bad = 333, 1111, 1108
+    rng = np.random.default_rng(11)
+    x = make_x(rng, rows, cols)
+    x[rows - 1, bad] = 0x7F80
+    dyb = workloads.bf16_bits(rng.standard_normal((rows, cols)).astype(np.float32))
+    v = layer.values(x)
+    rstd = 1 / np.sqrt(np.mean(np.where(np.isinf(v), 0, v) ** 2, axis=1) + 1e-5)
+    rstd[rows - 1] = 0
+    rstd = rstd.astype(np.float32)
+    dx = torch.empty((rows, cols), dtype=torch.bfloat16, device=DEV)
+    dg, db = (torch.empty(cols, device=DEV) for _ in range(2))
+    fp8.fp8_norm_backward(dev_bf16(dyb), dev_bf16(x), None, None, torch.from_numpy(rstd).to(DEV), fp8.NORM_RMS, dx, dg, db,
+                          fp8.norm_workspace(rows, cols))
+    dg = dg.cpu().numpy()
+    assert np.array_equal(np.nonzero(np.isnan(dg))[0], [bad])
+    terms = layer.values(dyb)[:-1] * (v[:-1] * rstd[:-1, None].astype(np.float64))
+    keep = np.arange(cols) != bad
+    # xhat rounded once, then a sum of rows terms in some order: rows + 1 roundings a term
+    tol = (rows + 4) * 2.0**-24 * np.abs(terms).sum(axis=0)
+    within(dg[keep], terms.sum(axis=0)[keep], tol[keep], "dgamma")
+    assert torch.isnan(dx[rows - 1].float()).all() and torch.isfinite(dx[:rows - 1].float()).all()
+    assert torch.isfinite(db).all()
+
+
 def test_norm_no_rows(fp8):
     """No rows: nothing to cast, and the weights' gradients are 0."""
     say("norm no rows")
