@@ -10,6 +10,7 @@ namespace fp8amax {
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
+constexpr int64_t kMaxCols = (int64_t)1 << 27;      // of a norm's gradient: its grid of 32 threads a column is 32-bit
 
 fp8_status_t check_rows(const char* fn, int64_t rows, int64_t limit) {
     if (rows >= limit) return fail(FP8_ERR_UNSUPPORTED, "%s: %lld rows or more", fn, (long long)limit);
@@ -61,6 +62,7 @@ fp8_status_t check_norm_backward(const char* fn, const uint16_t* dy, int64_t row
     if (!aligned(dy, 2) || !aligned(dx, 2) || !aligned(rstd, 4) || !aligned(dgamma, 4) || !aligned(dbeta, 4))
         return fail(FP8_ERR_ALIGNMENT, "%s: misaligned pointer", fn);
     FP8_TRY(check_rows(fn, rows, kMaxRows));
+    if (cols >= kMaxCols) return fail(FP8_ERR_UNSUPPORTED, "%s: %lld columns or more", fn, (long long)kMaxCols);
     if (dgamma || dbeta) {
         const int64_t need = fp8_norm_backward_workspace(rows, cols);
         if (need > 0 && (!workspace || workspace_bytes < need))
@@ -148,7 +150,7 @@ fp8_status_t fp8_norm_quantize_row(const uint16_t* x, int64_t rows, int64_t cols
 }
 
 int64_t fp8_norm_backward_workspace(int64_t rows, int64_t cols) {
-    if (rows < 1 || cols < 1 || rows >= kMaxRows || cols > ((int64_t)1 << 40)) return 0;
+    if (rows < 1 || cols < 1 || rows >= kMaxRows || cols >= kMaxCols) return 0;
     return (rows < kNormMaxBands ? rows : kNormMaxBands) * 2 * cols * (int64_t)sizeof(float);
 }
 

@@ -110,8 +110,8 @@ hipError_t launch_swiglu_quant_row_mx(const SwigluFwd& p, int fmt, hipStream_t s
 hipError_t launch_swiglu_backward(const SwigluBwd& p, hipStream_t st);
 
 // The MoE layer for a few tokens (kMoeFewTokens at most), two launches. ws
-// holds for every entry 2 * inter bf16 values: the activation's high parts,
-// then its low parts.
+// holds for every entry 2 * inter bf16 values: the activation's high and low
+// parts, in the order of the down product's loads.
 constexpr int kMoeFewTokens = 64;
 
 struct MoeFew {

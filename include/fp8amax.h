@@ -521,7 +521,9 @@ typedef enum { FP8_NORM_LAYER = 0, FP8_NORM_RMS = 1 } fp8_norm_t;
  *    is then ignored). Saving xhat instead of x keeps the checkpoint's error
  *    relative to the normalised value whatever the row's mean and scale.
  * cols >= 1; rows < 2^30 (else FP8_ERR_UNSUPPORTED); eps >= 0 and finite;
- * margin 0..32; x, y 2-byte aligned, gamma / beta to their type. Rows of up to
+ * margin 0..32; x, y 2-byte aligned, gamma / beta to their type. Sums are
+ * fp32: a row whose squares add up to more than 3.4e38 has variance Inf and
+ * rstd 0, one whose values do (FP8_NORM_LAYER) mean Inf. Rows of up to
  * 16384 columns are read once, in 16-byte accesses when x, y, gamma, beta are
  * 16-byte and q 8-byte aligned and ldx, ldy, ldq, cols multiples of 8, else in
  * unaligned ones (about half the speed); longer rows, and rows of fewer than 8
@@ -553,8 +555,8 @@ int64_t fp8_norm_backward_workspace(int64_t rows, int64_t cols);
  * may be NULL when dgamma and dbeta are. It is free for other use once the
  * call's work is done; calls that may run at the same time need one each.
  * Results do not depend on timing (no atomics). Sizes and layouts as the
- * forward pass. Outputs do not overlap each other or the inputs (dx may not
- * take dy's place). */
+ * forward pass, and cols < 2^27 (else FP8_ERR_UNSUPPORTED). Outputs do not
+ * overlap each other or the inputs (dx may not take dy's place). */
 fp8_status_t fp8_norm_backward(const uint16_t* dy, int64_t rows, int64_t cols, int64_t lddy, const uint16_t* x,
                                int64_t ldx, const void* gamma, fp8_out_t w_type, const float* mean, const float* rstd,
                                fp8_norm_t kind, uint16_t* dx, int64_t lddx, float* dgamma, float* dbeta,

@@ -102,7 +102,7 @@ int main() {
     RUN(grad(0, 64, 64, 0), FP8_OK);
     RUN(grad((1 << 30) - 1, 64, 64, 512 * 2 * 64 * 4), FP8_OK);
     RUN(grad(big, 64, 64, big), FP8_ERR_UNSUPPORTED);
-    CHECK(fp8_norm_backward_workspace(big, big) == 0 && fp8_norm_backward_workspace(1000, (int64_t)1 << 40) > 0);
+    CHECK(fp8_norm_backward_workspace(big, big) == 0 && fp8_norm_backward_workspace(1000, ((int64_t)1 << 27) - 1) > 0);
     auto mx = [&](int64_t rows, int64_t cols, int64_t ld) {
         return fp8_mx_norm_backward(U16(1), rows, cols, ld, U8(2), FP8_E5M2, ld, U8(3), rows > 1 ? rows : 1, dev(4),
                                     dev(5), FP8_OUT_F32, F32(6), FP8_NORM_RMS, U16(7), ld, nullptr, nullptr, U16(8), ld,

@@ -58,13 +58,15 @@ def test_norm_backward(fp8):
         ({0: None}, IA), ({4: None}, IA), ({11: None}, IA), ({9: None}, IA), ({8: None}, IA), ({2: 0}, IA),
         ({3: 60}, IA), ({5: 60}, IA), ({12: 60}, IA), ({7: 3}, IA), ({10: -1}, IA), ({15: None}, IA), ({16: 2047}, IA),
         ({0: off(1)}, AL), ({4: off(1)}, AL), ({11: off(1)}, AL), ({8: off(2)}, AL), ({9: off(1)}, AL),
-        ({13: off(2)}, AL), ({14: off(2)}, AL), ({15: off(8)}, AL), ({6: off(1)}, AL), ({1: 1 << 30}, UN)])
+        ({13: off(2)}, AL), ({14: off(2)}, AL), ({15: off(8)}, AL), ({6: off(1)}, AL), ({1: 1 << 30}, UN),
+        ({2: 1 << 27, 3: 1 << 27, 5: 1 << 27, 12: 1 << 27, 16: 1 << 40}, UN)])
 
 
 def test_norm_workspace_sizes(fp8):
     w = fp8.lib.fp8_norm_backward_workspace
     assert w(1, 1) == 8 and w(100000, 8) == 512 * 2 * 8 * 4
-    assert w(0, 8) == w(8, 0) == w(-1, 8) == w(1 << 30, 8) == 0
+    assert w(0, 8) == w(8, 0) == w(-1, 8) == w(1 << 30, 8) == w(8, 1 << 27) == 0
+    assert w(1, (1 << 27) - 1) == 8 * ((1 << 27) - 1)
 
 
 def test_mx_norm_backward(fp8):
