@@ -559,15 +559,21 @@ hipError_t norm_quant_reg(const NormFwd& p, hipStream_t st) {
     const int64_t nch = (p.cols + 7) / 8;
     // One wavefront a row where it holds the row (16384 x 2048: 32.0 us, 38.0 with
     // four) unless the rows are few (1000 x 2048: 6.2 us with one, 4.7 with four;
-    // 16 x 2048: 5.4 and 3.4); eight above 8192 columns.
+    // 16 x 2048: 5.4 and 3.4); longer rows as many wavefronts as they fill (8192 x
+    // 5120: 41.0 us with four, 37.6 with three; x 10240 76 with eight, 67.5 with
+    // five; two chunks a lane for these sizes 38.9 and 85).
     const bool wide = nch > 256 || (nch > 64 && p.rows < 1024);
     const dim3 grid((unsigned)(wide ? p.rows : (p.rows + kWaves - 1) / kWaves));
 #define FP8_NORM_CASE(C, W) \
     hipLaunchKernelGGL((k_norm_quant_row<F, C, W, LOOSE>), grid, dim3(W == 1 ? kBlock : W * 64), 0, st, p)
     if (wide) {
         if (nch <= 256) FP8_NORM_CASE(1, 4);
+        else if (nch <= 384) FP8_NORM_CASE(2, 3);
         else if (nch <= 512) FP8_NORM_CASE(2, 4);
+        else if (nch <= 768) FP8_NORM_CASE(4, 3);
         else if (nch <= 1024) FP8_NORM_CASE(4, 4);
+        else if (nch <= 1280) FP8_NORM_CASE(4, 5);
+        else if (nch <= 1536) FP8_NORM_CASE(4, 6);
         else FP8_NORM_CASE(4, 8);
     } else {
         if (nch <= 64) FP8_NORM_CASE(1, 1);

@@ -169,16 +169,24 @@ hipError_t swiglu_quant_fmt(const SwigluFwd& p, hipStream_t st) {
     const int64_t nch = p.inter / 8;
     // four wavefronts a row where the row is long (16384 x 2048: 40.9 us, with one
     // 46.5; 16384 x 1024: 37.3 and 24.9) or the rows are few (1000 x 2048: 5.4 and
-    // 6.5), eight above 8192 columns, whose row in four took 160 VGPRs
+    // 6.5). Longer rows take more wavefronts, two chunks a lane (with four, 92 VGPRs
+    // leave 20 wavefronts a CU: 8192 x 7168 78 us, with two 75; 8192 x 14336 168 and
+    // 163), as many as the row fills (8192 x 10240: 145 us with a third of the lanes
+    // idle, 118 with ten wavefronts; x 5120 71 and 62), except fourteen, which are 175
+    // at 14336
     const bool wide = nch > 128 || (nch > 64 && p.rows < 1024);
     const dim3 grid((unsigned)(wide ? p.rows : (p.rows + kWaves - 1) / kWaves));
 #define FP8_SW_CASE(C, W) \
     hipLaunchKernelGGL((k_swiglu_quant_row_mx<F, C, W>), grid, dim3(W == 1 ? kBlock : W * 64), 0, st, p)
     if (wide) {
         if (nch <= 256) FP8_SW_CASE(1, 4);
+        else if (nch <= 384) FP8_SW_CASE(2, 3);
         else if (nch <= 512) FP8_SW_CASE(2, 4);
-        else if (nch <= 1024) FP8_SW_CASE(4, 4);
-        else FP8_SW_CASE(4, 8);
+        else if (nch <= 768) FP8_SW_CASE(2, 6);
+        else if (nch <= 1024) FP8_SW_CASE(2, 8);
+        else if (nch <= 1280) FP8_SW_CASE(2, 10);
+        else if (nch <= 1536) FP8_SW_CASE(2, 12);
+        else FP8_SW_CASE(2, 16);
     } else {
         if (nch <= 64) FP8_SW_CASE(1, 1);
         else FP8_SW_CASE(2, 1);

@@ -57,6 +57,10 @@ FORWARD = [  # rows, cols, rms, gamma, beta, fmt
     (9, 2056, True, "none", "f32", 0), (33, 7168, True, "bf16", "none", 0), (3, 16384, False, "bf16", "bf16", 1),
     (4, 1, False, "bf16", "bf16", 0), (7, 1111, False, "bf16", "bf16", 0), (3, 20000, True, "f32", "none", 1),
     (2, 17, True, "none", "none", 3), (1030, 1021, False, "f32", "bf16", 0), (2, 16383, True, "bf16", "none", 0),
+    (6, 2880, False, "bf16", "bf16", 0), (5, 4104, False, "bf16", "bf16", 0), (4, 6144, True, "f32", "none", 1),
+    (3, 8224, False, "none", "bf16", 0), (2, 10240, True, "bf16", "none", 2), (2, 12256, False, "bf16", "bf16", 0),
+    (2, 12320, True, "bf16", "none", 0), (3, 2999, False, "bf16", "bf16", 0), (2, 9001, True, "none", "none", 0),
+    (2, 11003, False, "f32", "f32", 1),
 ]
 
 

@@ -30,7 +30,8 @@ def make_h(rng, rows, inter):
 
 
 SAVE = [(1, 32, 0, 0), (37, 256, 1, 1), (1030, 512, 0, 0), (1025, 1024, 2, 0), (1024, 2048, 0, 1), (3, 2080, 3, 0),
-        (300, 4096, 0, 0), (65, 4128, 1, 0), (20, 14336, 0, 0), (5, 16384, 0, 1), (6, 96, 0, 0)]
+        (300, 4096, 0, 0), (65, 4128, 1, 0), (20, 14336, 0, 0), (5, 16384, 0, 1), (6, 96, 0, 0),
+        (4, 3008, 0, 0), (3, 6112, 1, 1), (2, 8192, 0, 0), (3, 10240, 0, 0), (2, 11008, 2, 1), (3, 12320, 0, 0)]
 
 
 @pytest.mark.parametrize("rows,inter,fmt,ck", SAVE)
