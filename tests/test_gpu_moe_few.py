@@ -62,6 +62,7 @@ CASES = [  # T, k, E, H, inter, f1, f2
     (16, 4, 8, 512, 272, 1, 0), (17, 2, 4, 304, 144, 0, 0), (32, 8, 32, 256, 256, 0, 0), (33, 3, 4, 528, 64, 0, 0),
     (64, 2, 3, 1040, 112, 0, 1), (64, 64, 64, 64, 32, 0, 0), (2, 64, 1024, 32, 16, 0, 0), (7, 3, 2, 96, 48, 0, 0),
     (1, 2, 2, 7168, 2048, 0, 0), (4, 1, 8, 2064, 1040, 0, 0),
+    (64, 2, 3, 5152, 80, 0, 1), (20, 3, 4, 5120, 336, 1, 0), (9, 8, 8, 5152, 272, 0, 0), (40, 1, 2, 5184, 592, 0, 0),
 ]
 
 
@@ -80,6 +81,21 @@ def test_moe_few_parity(fp8, orc, T, k, E, H, inter, f1, f2):
     # the same bits whatever the workspace held before
     again = call(fp8, d, f1, f2, ws=torch.full((n,), float("nan"), device=DEV))
     assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("T,k,f1", [(16, 16, 0), (31, 9, 1), (64, 4, 0)])
+def test_moe_few_many_experts(fp8, orc, T, k, f1):
+    """64 experts with four tokens or more on average, where the gate and up product
+    takes two row tiles a workgroup; one expert has every token, another half of
+    them (both also by chance in other slots)."""
+    rng = np.random.default_rng(T)
+    d = make(orc, rng, T, k, 64, 176, 544, f1, 0)
+    d["idx"][:, 0] = 5
+    d["idx"][:T // 2 + 1, 1] = 6
+    say("moe few, many experts", T, k, f1)
+    out = call(fp8, d, f1, 0)
+    check(d, out, "out")
+    assert torch.equal(call(fp8, d, f1, 0, ws=torch.full((T * k * 544,), float("nan"), device=DEV)), out)
 
 
 def test_moe_few_every_code(fp8, orc):
