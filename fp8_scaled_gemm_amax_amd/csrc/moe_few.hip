@@ -20,6 +20,7 @@
 // same order, so that a lane's 16 bytes are one access.
 #include "layer.hpp"
 #include "layer_device.hpp"
+#include "moe_few_layout.hpp"
 
 namespace fp8amax {
 namespace {
@@ -180,33 +181,12 @@ __device__ __forceinline__ Entries find_entries(const MoeFew& p, const int16_t* 
     return en;
 }
 
-// The workspace between the two launches: an expert's activations as the down
-// product loads them. Tile n of an expert (8 of its tokens, w of them there)
-// has 2 * inter * w values from (base + 8 n) * 2 * inter on; its step kb of 64
-// values of K has w * 128 of them, as [half h][group j][high | low][token][8]
-// for K = 64 kb + 16 j + 8 h + 0..7. A load of a wavefront (lane: token, part and
-// group) is 128 w consecutive bytes and holds both parts: the high ones are
-// columns 0..7 of the product, the low ones columns 8..15. (Rows of K per token
-// made every load 16 lines: 32 tokens, 32 experts of 7168 x 2048, the down
-// product 150 us, without its loads of activations 86; tiles of 16 tokens with
-// one load for either part 108, these 105; one token 30 and 25; all of them with
-// the weights loaded as the cores want them.) The last step of K has K / 16 % 4
-// groups. The tiles of all experts add up to at most tokens * topk rows of
-// 2 * inter values.
-constexpr int kActTile = 8;
-struct ActTile {
+// A tile of activations (its layout: moe_few_layout.hpp) in the workspace.
+struct ActRows : ActTile {
     uint16_t* base;
-    int w, inter;
     __device__ __forceinline__ void set(const MoeFew& p, const Entries& en, int n) {
-        w = en.count - n * kActTile < kActTile ? en.count - n * kActTile : kActTile;
-        w = w < 1 ? 1 : w;                                  // (no tokens: not used)
-        inter = p.inter;
-        base = p.ws + (int64_t)(en.base + n * kActTile) * 2 * p.inter;
-    }
-    // values from the start to step kb, half h, group j, part (0 high, 1 low), token c
-    __device__ __forceinline__ int offset(int kb, int h, int j, int part, int c) const {
-        const int left = inter / 16 - kb * 4, groups = left < 4 ? left : 4;
-        return kb * 128 * w + (((h * groups + j) * 2 + part) * w + c) * 8;
+        ActTile::set(en.base, en.count, p.inter, n);
+        base = p.ws + first;
     }
 };
 
@@ -349,7 +329,7 @@ __device__ __forceinline__ void up_tile(const MoeFew& p, const int16_t* idx, int
         const int col = threadIdx.x >> 4;
         if (n * 16 + col >= ent.count) continue;
         const int c = n * 16 + col;
-        ActTile tile;
+        ActRows tile;
         tile.set(p, ent, c / kActTile);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -423,10 +403,10 @@ constexpr int kDownWaves = 8;
 // blocks b0, b0 + db, .. of K.
 // wp: first row of each tile; stage: this wavefront's LDS, RT tiles.
 template <int F, int RT, int NT, int U>
-__device__ __forceinline__ void down_sums(const uint8_t* const* wp, int64_t ld, const ActTile* tile, const int* col, int K,
+__device__ __forceinline__ void down_sums(const uint8_t* const* wp, int64_t ld, const ActRows* tile, const int* col, int K,
                                           int b0, int db, uint4* stage, v4f (*acc)[NT]) {
     using Tile = RowTile<U>;
-    const int j = (threadIdx.x & 63) >> 4, j16 = j * 16;
+    const int lane = threadIdx.x & 63, j16 = (lane >> 4) * 16;
     const int whole = K / (kStep * U);
     const uint8_t* lp[RT];
     uint4 w[RT][U];
@@ -444,8 +424,8 @@ __device__ __forceinline__ void down_sums(const uint8_t* const* wp, int64_t ld, 
             for (int n = 0; n < G; ++n)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {               // (a whole step: 4 groups)
-                    const ActTile& t = tile[n0 + n];
-                    a[n][s][h] = load_acts(t.base + (b * U + s) * 128 * t.w + h * 64 * t.w + col[n0 + n]);
+                    const ActRows& t = tile[n0 + n];
+                    a[n][s][h] = load_acts(t.base + t.whole(b * U + s, h, col[n0 + n]));
                 }
     };
     int b = b0;
@@ -489,11 +469,9 @@ __device__ __forceinline__ void down_sums(const uint8_t* const* wp, int64_t ld, 
         const bool in = k < K;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int part = ((threadIdx.x & 63) >> 3) & 1;
-            const int c = col[n] / 8 - (j * 2 + part) * tile[n].w;      // (the token)
             v8bf a[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) a[h] = load_acts_if(in, tile[n].base + tile[n].offset(k >> 6, h, j, part, c));
+            for (int h = 0; h < 2; ++h) a[h] = load_acts_if(in, tile[n].base + tile[n].last(k, h, lane));
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 const uint4 wl = load_weights_if(in, wp[r] + (threadIdx.x & 15) * ld + k);
@@ -526,14 +504,12 @@ __device__ __forceinline__ void down_unit(const MoeFew& p, int e, int row0, cons
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[r][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    ActTile tile[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) tile[n].set(p, ent, n);
-    int col[NT];                                            // this lane's place in a part of a whole step
+    ActRows tile[NT];
+    int col[NT];                                            // this lane's place in a whole step
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int c = lane & 7, part = (lane >> 3) & 1;     // (columns past the entries are not used)
-        col[n] = (((lane >> 4) * 2 + part) * tile[n].w + (c < tile[n].w ? c : 0)) * 8;
+        tile[n].set(p, ent, n);
+        col[n] = tile[n].lane(lane);
     }
     down_sums<F, RT, NT, U>(wp, p.ld2, tile, col, p.inter, b0, db, stage, acc);
     if (NT > 4) load_factors();
@@ -585,10 +561,13 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_moe_few_down(MoeFew p) {
         const int e = __builtin_amdgcn_readfirstlane(list[unit / pieces]);
         const Entries ent = find_entries(p, idx, e);
         const int b0 = unit % pieces;
-        if (TT > 32 && ent.count > 32) down_unit<F, RT, 8, 1>(p, e, row0, ent, b0, pieces, stage, sums);
-        else if (TT > 16 && ent.count > 16) down_unit<F, RT, 4, 2>(p, e, row0, ent, b0, pieces, stage, sums);
-        else if (ent.count > 8) down_unit<F, RT, 2, 4>(p, e, row0, ent, b0, pieces, stage, sums);
-        else down_unit<F, RT, 1, 4>(p, e, row0, ent, b0, pieces, stage, sums);
+        const int tiles = down_shape(ent.count).tiles;
+#define FP8_DOWN(N) down_unit<F, RT, N, down_shape(N * kActTile).steps>(p, e, row0, ent, b0, pieces, stage, sums)
+        if (TT > 32 && tiles == 8) FP8_DOWN(8);
+        else if (TT > 16 && tiles == 4) FP8_DOWN(4);
+        else if (tiles == 2) FP8_DOWN(2);
+        else FP8_DOWN(1);
+#undef FP8_DOWN
     }
     __syncthreads();
     for (int i = threadIdx.x; i < p.tokens * (RT * 16); i += kDownWaves * 64) {

@@ -98,6 +98,20 @@ def test_moe_few_many_experts(fp8, orc, T, k, f1):
     assert torch.equal(call(fp8, d, f1, 0, ws=torch.full((T * k * 544,), float("nan"), device=DEV)), out)
 
 
+@pytest.mark.parametrize("T", [17, 24, 25, 33, 40, 41, 56, 57])
+def test_moe_few_tiles_without_tokens(fp8, orc, T):
+    """Every token at the last expert, one slot each: the down product's instance has
+    tiles without tokens (17..24 and 33..56 tokens), the workspace no spare row
+    (tests/test_moe_few_layout.py has the addresses)."""
+    rng = np.random.default_rng(T + 100)
+    d = make(orc, rng, T, 1, 2, 96, 336)
+    d["idx"][:] = 1
+    say("moe few, tiles without tokens", T)
+    out = call(fp8, d)
+    check(d, out, "out")
+    assert torch.equal(call(fp8, d, ws=torch.full((T, 336), float("nan"), device=DEV)), out)
+
+
 def test_moe_few_every_code(fp8, orc):
     """Every finite code of both formats decodes exactly: one-hot tokens read the
     columns of W1 = all codes back through a large gate (silu = identity)."""
