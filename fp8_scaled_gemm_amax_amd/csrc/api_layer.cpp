@@ -10,7 +10,7 @@ namespace fp8amax {
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
-constexpr int64_t kMaxCols = (int64_t)1 << 27;      // of a norm's gradient: its grid of 32 threads a column is 32-bit
+constexpr int64_t kMaxCols = (int64_t)1 << 27;      // of a norm's gradient: 16 threads a column add the bands, in one grid
 
 fp8_status_t check_rows(const char* fn, int64_t rows, int64_t limit) {
     if (rows >= limit) return fail(FP8_ERR_UNSUPPORTED, "%s: %lld rows or more", fn, (long long)limit);

@@ -70,6 +70,18 @@ inline bool norm_vector_layout(const NormBwd& p) {
     return p.cols % 8 == 0 && p.cols <= kNormMaxVecCols && chunked(p.dy, p.lddy, 16) && chunked(p.dx, p.lddx, 16) &&
            chunked(p.gamma, 0, 16) && chunked(p.beta, 0, 16) && chunked(p.x, p.ldx, 16) && chunked(p.y, p.ldy, 16);
 }
+// Columns and slices of the rows of a workgroup of the weights' gradients in any
+// layout, and its grid over the columns: at most 2^21 workgroups side by side,
+// since a grid's threads (32 a column here) stay below 2^32 in each direction.
+constexpr int kAnyCols = 32, kAnySlices = 32;
+struct ColsGrid {
+    unsigned x, z;
+};
+inline ColsGrid any_cols_grid(int64_t cols) {
+    const int64_t blocks = (cols + kAnyCols - 1) / kAnyCols, most = (int64_t)1 << 21;
+    const int64_t x = blocks < most ? blocks : most;
+    return {(unsigned)x, (unsigned)((blocks + x - 1) / x)};
+}
 hipError_t launch_norm_quant_row(const NormFwd& p, int fmt, hipStream_t st);
 hipError_t launch_norm_backward(const NormBwd& p, hipStream_t st);
 

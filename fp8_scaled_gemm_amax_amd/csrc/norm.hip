@@ -524,11 +524,10 @@ __global__ __launch_bounds__(kBlock) void k_norm_grad_row_any(NormBwd p) {
 // 32 columns x 32 slices of the band's rows per workgroup, the slices added in
 // order. (One thread per column over bands of 32 rows: a third launch for every
 // size, 333 x 1111: 4.6 + 2.6 us.)
-constexpr int kAnyCols = 32, kAnySlices = 32;
 __global__ __launch_bounds__(kAnyCols * kAnySlices) void k_norm_grad_cols_any(NormBwd p) {
     __shared__ float red[2][kAnySlices][kAnyCols];
     const int cl = threadIdx.x % kAnyCols, sl = threadIdx.x / kAnyCols;
-    const int64_t c = (int64_t)blockIdx.x * kAnyCols + cl, cc = c < p.cols ? c : p.cols - 1;
+    const int64_t c = ((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * kAnyCols + cl, cc = c < p.cols ? c : p.cols - 1;
     const int64_t r0 = (int64_t)blockIdx.y * p.band;
     const int64_t r1 = r0 + p.band < p.rows ? r0 + p.band : p.rows;
     float dg = 0.0f, db = 0.0f;
@@ -675,8 +674,9 @@ hipError_t launch_norm_backward(const NormBwd& p0, hipStream_t st) {
     p.band = (p.rows + kNormMaxBands - 1) / kNormMaxBands;
     if (p.band < kAnySlices * 32) p.band = kAnySlices * 32;
     p.bands = (p.rows + p.band - 1) / p.band;
-    hipLaunchKernelGGL(k_norm_grad_cols_any, dim3((unsigned)((p.cols + kAnyCols - 1) / kAnyCols), (unsigned)p.bands),
-                       dim3(kAnyCols * kAnySlices), 0, st, p);
+    const ColsGrid grid = any_cols_grid(p.cols);
+    hipLaunchKernelGGL(k_norm_grad_cols_any, dim3(grid.x, (unsigned)p.bands, grid.z), dim3(kAnyCols * kAnySlices), 0, st,
+                       p);
     e = hipGetLastError();
     if (e == hipSuccess && p.bands > 1) {
         hipLaunchKernelGGL(k_norm_weight_grad, dim3((unsigned)((p.cols + kSliceCols - 1) / kSliceCols), 2),

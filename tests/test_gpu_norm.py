@@ -404,3 +404,28 @@ def test_norm_tensors_of_two_devices_are_refused(fp8):
     with pytest.raises(fp8.Fp8Error, match="workspace of 2048 bytes"):
         fp8.fp8_norm_backward(x, x, None, z, z, fp8.NORM_LAYER, torch.empty_like(x), dgamma=torch.zeros(64, device=DEV),
                               workspace=torch.zeros(511, device=DEV))
+
+
+def test_norm_backward_of_the_most_columns(fp8):
+    """One row of 2^27 - 1 columns, the most that is accepted: the grid of the weights'
+    gradients is in two layers. dbeta is dy and dgamma the rounded product, bit for bit;
+    dx within the rounding of its sums (256 threads add 2^19 terms each, in order)."""
+    n = (1 << 27) - 1
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(3)
+    x, dy = (torch.randn((1, n), device=DEV, generator=gen, dtype=torch.bfloat16) for _ in range(2))
+    rstd = torch.full((1,), 1.25, device=DEV)
+    dx = torch.zeros_like(x)
+    dgamma, dbeta = (torch.full((n,), float("nan"), device=DEV) for _ in range(2))
+    say("norm gradient", 1, n)
+    fp8.fp8_norm_backward(dy, x, None, None, rstd, fp8.NORM_RMS, dx, dgamma, dbeta, fp8.norm_workspace(1, n))
+    torch.cuda.synchronize()
+    assert torch.equal(dbeta, dy[0].float())
+    xh = x[0].float() * rstd
+    assert torch.equal(dgamma, xh * dy[0].float())
+    d64, x64 = dy[0].double(), xh.double()
+    c1 = (d64 * x64).sum() / n
+    c1_tol = (2.0 ** 19 + 16) * layer.U * (d64 * x64).abs().sum() / n
+    want = 1.25 * (d64 - x64 * c1)
+    tol = 1.25 * (x64.abs() * c1_tol + 6 * layer.U * (d64.abs() + (x64 * c1).abs()))
+    assert ((dx[0].double() - want).abs() <= tol * (1 + BF) + BF * want.abs()).all()
