@@ -366,9 +366,7 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
         for (int c = 0; c < MAXC; ++c) {
             const uint32_t ch = tt + c * TPR;
             const bool live = live_row && ch < nch;
-            // Past the row dy counts as 0: every term of the sums is then 0, or NaN
-            // where the row's own duplicated values give NaN anyway. (A row past the
-            // band is worked on and used nowhere.)
+            // (A row past the band is worked on and used nowhere.)
             if (LOOSE && live) {
                 uint4 x = make_uint4(cur.x[c][0], cur.x[c][1], cur.x[c][SRC == 0 ? 2 : 0], cur.x[c][SRC == 0 ? 3 : 0]);
                 place_chunk<LOOSE>(&cur.dy[c], ch, n);
@@ -378,15 +376,20 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
                 cur.x[c][SRC == 0 ? 2 : 0] = x.z;
                 cur.x[c][SRC == 0 ? 3 : 0] = x.w;
             }
-            if (!live) cur.dy[c] = make_uint4(0u, 0u, 0u, 0u);
             float xh[8], dy[8];
             row_values<SRC>(cur, c, xh, dy);
+            // What stands past the row is selected out of the sums: as a term of 0
+            // it would be 0 * Inf where a weight, xhat or rstd is infinite.
+            float t1 = s1, t2 = s2;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float w = dy[i] * g[c][i];
-                s1 = fmaf(w, xh[i], s1);
-                s2 += w;
+                const float w = dy[i] * g[c][i], f1 = fmaf(w, xh[i], t1), f2 = t2 + w;
+                const bool in = !LOOSE || ch * 8 + i < n;
+                t1 = in ? f1 : t1;
+                t2 = in ? f2 : t2;
             }
+            s1 = ch < nch ? t1 : s1;
+            s2 = ch < nch ? t2 : s2;
             if (SRC > 0 && p.y && live) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {

@@ -429,3 +429,81 @@ def test_norm_backward_of_the_most_columns(fp8):
     want = 1.25 * (d64 - x64 * c1)
     tol = 1.25 * (x64.abs() * c1_tol + 6 * layer.U * (d64.abs() + (x64 * c1).abs()))
     assert ((dx[0].double() - want).abs() <= tol * (1 + BF) + BF * want.abs()).all()
+
+
+def special_gradient(dy, xh, g, rstd, rms):
+    """dx of one row in the arithmetic of the definition (fp64, Inf and NaN included)."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        w = dy * g
+        c1, c2 = (w * xh).sum() / len(dy), 0.0 if rms else w.sum() / len(dy)
+        return rstd * (w - xh * c1 - c2)
+
+
+def same_specials(got, want, what):
+    assert np.array_equal(np.isnan(got), np.isnan(want)), what
+    assert np.array_equal(np.isposinf(got), np.isposinf(want)) and np.array_equal(np.isneginf(got), np.isneginf(want)), what
+
+
+@pytest.mark.parametrize("cols", [520, 512, 1030, 1111, 2560, 2999, 4104, 8224])
+@pytest.mark.parametrize("rms", [True, False])
+def test_norm_backward_infinite_weight(fp8, cols, rms):
+    """An infinite gamma among the row's last columns makes the row's means infinite, not
+    NaN, whether or not the width fills the lanes of its team: dx is the definition's."""
+    rng = np.random.default_rng(cols)
+    rows, at = 3, cols - 2
+    x = workloads.bf16_bits(rng.uniform(0.5, 2.0, (rows, cols)).astype(np.float32))
+    dy = workloads.bf16_bits(rng.uniform(0.5, 2.0, (rows, cols)).astype(np.float32))
+    gamma = np.ones(cols, np.float32)
+    gamma[at] = np.inf
+    mean, rstd = np.array([0.25, -1.0, 0.0], np.float32), np.array([1.0, 0.5, 2.0], np.float32)
+    dx = torch.zeros((rows, cols), dtype=torch.bfloat16, device=DEV)
+    say("norm gradient, infinite gamma", cols, rms)
+    fp8.fp8_norm_backward(dev_bf16(dy), dev_bf16(x), torch.from_numpy(gamma).to(DEV), torch.from_numpy(mean).to(DEV),
+                          torch.from_numpy(rstd).to(DEV), fp8.NORM_RMS if rms else fp8.NORM_LAYER, dx)
+    got = dx.float().cpu().numpy()
+    for r in range(rows):
+        xh = (layer.values(x)[r] - (0.0 if rms else mean[r])) * rstd[r]
+        same_specials(got[r], special_gradient(layer.values(dy)[r], xh, gamma.astype(np.float64), rstd[r], rms), (r, cols))
+
+
+@pytest.mark.parametrize("cols", [1032, 1111, 2047, 4099])
+def test_norm_backward_infinite_rstd(fp8, cols):
+    """rstd = Inf (eps = 0 and squares that underflow): xhat is infinite and so is dx; the
+    zeros behind a row that ends inside a chunk of 8 add nothing (0 * Inf)."""
+    rng = np.random.default_rng(cols)
+    x = workloads.bf16_bits(rng.uniform(0.5, 2.0, (2, cols)).astype(np.float32))
+    dy = workloads.bf16_bits(rng.uniform(0.5, 2.0, (2, cols)).astype(np.float32))
+    dx = torch.zeros((2, cols), dtype=torch.bfloat16, device=DEV)
+    say("norm gradient, infinite rstd", cols)
+    fp8.fp8_norm_backward(dev_bf16(dy), dev_bf16(x), None, None, torch.full((2,), float("inf"), device=DEV),
+                          fp8.NORM_RMS, dx)
+    got = dx.float().cpu().numpy()
+    for r in range(2):
+        same_specials(got[r], special_gradient(layer.values(dy)[r], layer.values(x)[r] * np.inf, 1.0, np.inf, True), r)
+    assert np.isneginf(got).all()
+
+
+@pytest.mark.parametrize("cols", [544, 512, 1056, 2592, 8224])
+@pytest.mark.parametrize("with_y", [False, True])
+def test_norm_backward_infinite_checkpoint(fp8, cols, with_y):
+    """An Inf code (e5m2) of a checkpoint in the row's last columns, its block's byte an
+    ordinary one: the mean is infinite and dx the definition's at every width."""
+    rng = np.random.default_rng(cols)
+    rows, at = 2, cols - 3
+    dy = workloads.bf16_bits(rng.uniform(0.5, 2.0, (rows, cols)).astype(np.float32))
+    q = np.full((rows, cols), 0x3C, np.uint8)                       # 1.0
+    q[:, at] = 0x7C                                                 # Inf
+    xs = fp8.mx_scale_records(rows, cols)
+    xs.fill_(127)
+    dx = torch.zeros((rows, cols), dtype=torch.bfloat16, device=DEV)
+    y = torch.zeros_like(dx) if with_y else None
+    say("norm gradient, infinite checkpoint", cols, with_y)
+    fp8.fp8_mx_norm_backward(dev_bf16(dy), torch.from_numpy(q).to(DEV), 1, xs, None, None,
+                             torch.ones(rows, device=DEV), fp8.NORM_RMS, dx, y=y)
+    got = dx.float().cpu().numpy()
+    xh = np.ones(cols)
+    xh[at] = np.inf
+    for r in range(rows):
+        same_specials(got[r], special_gradient(layer.values(dy)[r], xh, 1.0, 1.0, True), (r, cols))
+    if with_y:
+        assert np.array_equal(bf16_of(y), np.tile(xh, (rows, 1)))
