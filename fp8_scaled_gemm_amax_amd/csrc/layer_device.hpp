@@ -241,14 +241,31 @@ __device__ __forceinline__ void store_checkpoint(uint8_t* p, uint2 v) {
 // the row's last 8 values and shifted into place when it is used, zeros behind
 // it: no load waits in a branch (by elements in a branch, the gradient of 333 x
 // 1111 took 17 us instead of 10).
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+// A value whose address is a multiple of A bytes only. V is a scalar or one of the
+// compiler's own vectors: a class (HIP's uint4, float4) would keep its alignment
+// of 16 in here, and the access would promise it.
 template <typename V, int A>
 struct __attribute__((packed, aligned(A))) Loose {
     V v;
 };
+template <typename V, int A>
+__device__ __forceinline__ V load_loose(const void* base, uint32_t bytes) {
+    static_assert(alignof(Loose<V, A>) == A && sizeof(Loose<V, A>) == sizeof(V), "no more alignment than the layout has");
+    return at<Loose<V, A>>(base, bytes)->v;
+}
+template <typename V, int A>
+__device__ __forceinline__ void store_loose(void* base, uint32_t bytes, V v) {
+    static_assert(alignof(Loose<V, A>) == A && sizeof(Loose<V, A>) == sizeof(V), "no more alignment than the layout has");
+    at<Loose<V, A>>(base, bytes)->v = v;
+}
 template <bool LOOSE>
 __device__ __forceinline__ uint4 load_chunk(const uint16_t* row, uint32_t ch, uint32_t n) {
     if constexpr (!LOOSE) return load_stream(at<uint4>(row, ch * 16));
-    return at<Loose<uint4, 2>>(row, (ch * 8 + 8 <= n ? ch * 8 : n - 8) * 2)->v;
+    const u32x4 v = load_loose<u32x4, 2>(row, (ch * 8 + 8 <= n ? ch * 8 : n - 8) * 2);
+    return make_uint4(v.x, v.y, v.z, v.w);
 }
 // What load_chunk gave for chunk ch, its values in place.
 template <bool LOOSE>
@@ -256,11 +273,21 @@ __device__ __forceinline__ void place_chunk(uint4* v, uint32_t ch, uint32_t n) {
     if constexpr (LOOSE) {
         if (ch * 8 + 8 > n) {
             const uint32_t s = ch * 8 + 8 - n;              // values to drop: 1 .. 7
-            if (s & 4) *v = make_uint4(v->z, v->w, 0u, 0u);
-            if (s & 2) *v = make_uint4(v->y, v->z, v->w, 0u);
-            if (s & 1)
-                *v = make_uint4((v->x >> 16) | (v->y << 16), (v->y >> 16) | (v->z << 16), (v->z >> 16) | (v->w << 16),
-                                v->w >> 16);
+            uint32_t x = v->x, y = v->y, z = v->z, w = v->w;
+            x = s & 4 ? z : x;
+            y = s & 4 ? w : y;
+            z = s & 4 ? 0u : z;
+            w = s & 4 ? 0u : w;
+            x = s & 2 ? y : x;
+            y = s & 2 ? z : y;
+            z = s & 2 ? w : z;
+            w = s & 2 ? 0u : w;
+            const uint32_t odd = (s & 1) * 16;
+            x = __builtin_amdgcn_alignbit(y, x, odd);
+            y = __builtin_amdgcn_alignbit(z, y, odd);
+            z = __builtin_amdgcn_alignbit(w, z, odd);
+            w >>= odd;
+            *v = make_uint4(x, y, z, w);
         }
     }
 }
@@ -272,19 +299,19 @@ __device__ __forceinline__ void store_chunk(uint16_t* row, uint32_t ch, uint32_t
         return;
     }
     if (ch * 8 + 8 <= n) {
-        at<Loose<uint4, 2>>(row, ch * 16)->v = v;
+        store_loose<u32x4, 2>(row, ch * 16, u32x4{v.x, v.y, v.z, v.w});
         return;
     }
     const uint32_t m = n - ch * 8;                          // 4 + 2 + 1 of the 1 .. 7 values there
     uint32_t o = ch * 16;
     if (m & 4) {
-        at<Loose<uint2, 2>>(row, o)->v = make_uint2(v.x, v.y);
+        store_loose<u32x2, 2>(row, o, u32x2{v.x, v.y});
         v.x = v.z;
         v.y = v.w;
         o += 8;
     }
     if (m & 2) {
-        at<Loose<uint32_t, 2>>(row, o)->v = v.x;
+        store_loose<uint32_t, 2>(row, o, v.x);
         v.x = v.y;
         o += 4;
     }
@@ -297,18 +324,18 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint32_t ch, uint32_t 
         return;
     }
     if (ch * 8 + 8 <= n) {
-        at<Loose<uint2, 1>>(row, ch * 8)->v = v;
+        store_loose<u32x2, 1>(row, ch * 8, u32x2{v.x, v.y});
         return;
     }
     const uint32_t m = n - ch * 8;
     uint32_t o = ch * 8;
     if (m & 4) {
-        at<Loose<uint32_t, 1>>(row, o)->v = v.x;
+        store_loose<uint32_t, 1>(row, o, v.x);
         v.x = v.y;
         o += 4;
     }
     if (m & 2) {
-        at<Loose<uint16_t, 1>>(row, o)->v = (uint16_t)v.x;
+        store_loose<uint16_t, 1>(row, o, (uint16_t)v.x);
         v.x >>= 16;
         o += 2;
     }

@@ -24,8 +24,8 @@ template <bool LOOSE>
 __device__ __forceinline__ void load_weights8(const void* w, int w_f32, uint32_t ch, uint32_t n, float* o) {
     const uint32_t first = !LOOSE || ch * 8 + 8 <= n ? ch * 8 : n - 8;
     if (w_f32) {
-        const float4 a = LOOSE ? at<Loose<float4, 4>>(w, first * 4)->v : *at<float4>(w, first * 4);
-        const float4 b = LOOSE ? at<Loose<float4, 4>>(w, first * 4 + 16)->v : *at<float4>(w, first * 4 + 16);
+        constexpr int A = LOOSE ? 4 : 16;
+        const f32x4 a = load_loose<f32x4, A>(w, first * 4), b = load_loose<f32x4, A>(w, first * 4 + 16);
         o[0] = a.x;
         o[1] = a.y;
         o[2] = a.z;
@@ -39,14 +39,13 @@ __device__ __forceinline__ void load_weights8(const void* w, int w_f32, uint32_t
             if (s > 0) {
 #pragma unroll
                 for (int k = 4; k >= 1; k >>= 1)
-                    if (s & k) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = i + k < 8 ? o[i + k] : 0.0f;
-                    }
+                    for (int i = 0; i < 8; ++i) o[i] = s & k ? (i + k < 8 ? o[i + k] : 0.0f) : o[i];
             }
         }
     } else {
-        uint4 v = LOOSE ? at<Loose<uint4, 2>>(w, first * 2)->v : *at<uint4>(w, first * 2);
+        const u32x4 r = load_loose<u32x4, LOOSE ? 2 : 16>(w, first * 2);
+        uint4 v = make_uint4(r.x, r.y, r.z, r.w);
         place_chunk<LOOSE>(&v, ch, n);
         unpack8(v, o);
     }
@@ -289,8 +288,8 @@ __device__ __forceinline__ void load_row(const NormBwd& p, int row, uint32_t tt,
 template <bool LOOSE>
 __device__ __forceinline__ void store_sums(float* p, uint32_t ch, uint32_t n, const float* v) {
     if (!LOOSE || ch * 8 + 8 <= n) {
-        at<Loose<float4, 4>>(p, ch * 32)->v = make_float4(v[0], v[1], v[2], v[3]);
-        at<Loose<float4, 4>>(p, ch * 32 + 16)->v = make_float4(v[4], v[5], v[6], v[7]);
+        store_loose<f32x4, 4>(p, ch * 32, f32x4{v[0], v[1], v[2], v[3]});
+        store_loose<f32x4, 4>(p, ch * 32 + 16, f32x4{v[4], v[5], v[6], v[7]});
         return;
     }
 #pragma unroll
