@@ -520,7 +520,11 @@ __device__ __forceinline__ void down_unit(const MoeFew& p, int e, int row0, cons
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[r][n][i] += __shfl_xor(acc[r][n][i], 8, 64);   // high and low columns
+            for (int i = 0; i < 4; ++i) {                   // the high column's sum and the low one's
+                const float hi = acc[r][n][i], lo = __shfl_xor(hi, 8, 64);
+                // (an infinite weight: the low parts, of either sign or 0, would make NaN of Inf)
+                acc[r][n][i] = __builtin_isfinite(hi) ? hi + lo : hi;
+            }
         if (c >= ent.count || (lane & 8)) continue;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {

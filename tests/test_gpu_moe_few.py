@@ -283,3 +283,36 @@ def test_moe_few_two_streams(fp8, orc):
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert all(torch.equal(x, w) for x in o)
+
+
+@pytest.mark.parametrize("T,inter", [(1, 336), (12, 336), (20, 272), (40, 80), (64, 16)])
+def test_moe_few_infinite_codes(fp8, orc, T, inter):
+    """Infinite codes (e5m2) of W1 and W2 give what the definition's arithmetic gives: an
+    infinite output of the activation's sign from W2, whichever sign the activation's low
+    part has, NaN where two of them meet with opposite signs; infinite gates and ups from
+    W1 (a gate of -Inf is NaN). Every other output stays within its bound."""
+    rng = np.random.default_rng(T + inter)
+    k, E, H = 2, 4, 64
+    d = make(orc, rng, T, k, E, H, inter, 1, 1)
+    d["x"] = np.where((d["x"] & 0x7FFF) == 0, 0x3F80, d["x"]).astype(np.uint16)
+
+    def put(name, e, row, col, code):
+        d[name][e, row, col] = code
+        d["v" + name][e, row, col] = np.inf if code == 0x7C else -np.inf
+
+    for row in range(0, 40):                                        # every place of K in turn
+        put("w2", 0, row, (row * 37) % inter, 0x7C if row % 3 else 0xFC)
+    put("w2", 1, 50, 3, 0x7C)
+    put("w2", 1, 50, 7, 0xFC)                                       # Inf or NaN, as the activations' signs meet
+    put("w1", 3, 5, 9, 0x7C)                                        # a gate
+    put("w1", 2, inter + 2, 17, 0xFC)                               # an up
+    say("moe few, infinite codes", T, inter)
+    got = layer.values(host_bits(call(fp8, d, 1, 1)))
+    with np.errstate(invalid="ignore", over="ignore"):
+        want, tol = layer.moe_few(layer.values(d["x"]), d["idx"], d["w"], d["vw1"], d["vw2"])
+    assert np.isinf(want).any()
+    for same in (np.isnan, np.isposinf, np.isneginf):
+        assert np.array_equal(same(got), same(want)), (same.__name__, np.argwhere(same(got) != same(want))[:3])
+    fin = np.isfinite(want)
+    if fin.any():
+        within(got[fin], want[fin], tol[fin] * (1 + BF), "finite outputs", rel=BF)
