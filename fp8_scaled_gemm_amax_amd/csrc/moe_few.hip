@@ -340,10 +340,12 @@ __device__ __forceinline__ void up_tile(const MoeFew& p, const int16_t* idx, int
                 u += red[w * kPart + (n * 2 * RT + 2 * r + 1) * 256 + threadIdx.x];
             }
             const float a = silu_fast(g * factor[2 * r]) * (u * factor[2 * r + 1]) * share[n];
-            const uint32_t hi = f32_to_bf16(a);
-            const float rest = a - __uint_as_float(hi << 16);
-            // (an Inf or NaN is carried by the high part alone)
-            const uint32_t lo = __builtin_isfinite(a) && __builtin_isfinite(rest) ? f32_to_bf16(rest) : 0u;
+            // (an Inf or NaN is carried by the high part alone; a finite value that
+            // bf16 would round to Inf is bf16's largest and the rest)
+            const bool finite = __builtin_isfinite(a);
+            uint32_t hi = f32_to_bf16(a);
+            hi -= finite && (hi & 0x7fffu) == 0x7f80u ? 1u : 0u;
+            const uint32_t lo = finite ? f32_to_bf16(a - __uint_as_float(hi << 16)) : 0u;
             const int k = c0 + r * 16, kb = k >> 6, j = (k >> 4) & 3, half = row >> 3;
             tile.base[tile.offset(kb, half, j, 0, c % kActTile) + (row & 7)] = (uint16_t)hi;
             tile.base[tile.offset(kb, half, j, 1, c % kActTile) + (row & 7)] = (uint16_t)lo;

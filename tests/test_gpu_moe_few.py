@@ -316,3 +316,26 @@ def test_moe_few_infinite_codes(fp8, orc, T, inter):
     fin = np.isfinite(want)
     if fin.any():
         within(got[fin], want[fin], tol[fin] * (1 + BF), "finite outputs", rel=BF)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_moe_few_largest_activations(fp8, orc, sign):
+    """An activation between bf16's largest value and fp32's is finite: its parts are bf16's
+    largest value and the rest, and the output follows the definition."""
+    H = inter = 16
+    one = orc.encode(1, np.array([1.0], np.float32))[0]
+    d = {"x": np.zeros((1, H), np.uint16), "idx": np.zeros((1, 1), np.int32), "w": np.ones((1, 1), np.float32),
+         "w1": np.zeros((1, 2 * inter, H), np.uint8), "w2": np.zeros((1, H, inter), np.uint8),
+         "sw1": np.ones((1, 2 * inter), np.float32), "sw2": np.full((1, H), 2.0 ** -100, np.float32)}
+    d["x"][0, 0] = 0x3F80
+    d["w1"][0, 0, 0] = d["w1"][0, inter, 0] = d["w2"][0, 5, 0] = one
+    gate, up = np.float32(1.8432e19), np.float32(sign * 3.4e38 / 1.8432e19)
+    d["sw1"][0, 0], d["sw1"][0, inter] = gate, up
+    want = float(gate) * float(up)
+    assert 3.3962e38 < abs(want) < 3.4028e38
+    say("moe few, largest activations", sign)
+    got = layer.values(host_bits(call(fp8, d, 1, 1)))[0]
+    want *= 2.0 ** -100
+    # two roundings of the activation, its two parts to 2^-16, the output's half step
+    assert abs(got[5] - want) <= (BF + 2.0 ** -16 + 4 * layer.U) * abs(want) * (1 + BF)
+    assert not got[:5].any() and not got[6:].any()
