@@ -705,7 +705,8 @@ def fp8_moe_few_tokens(x, expert_idx, weights, w1, f1, w1_scale_inv, w2, f2, w2_
     expert_idx int32, weights fp32 [T x k]; w1 codes [E x 2I x H] (gate rows, then
     up rows) with w1_scale_inv fp32 [E x 2I]; w2 codes [E x H x I] with
     w2_scale_inv fp32 [E x H]; workspace: moe_few_workspace(T, k, I), one for each
-    call that may run at the same time."""
+    call that may run at the same time. The order of the fp32 sums depends on the
+    call's routing (the same call gives the same bits)."""
     T, H, ldx = _rows(x, "x")
     k = _i32_2d(expert_idx, "expert_idx")[1]
     if expert_idx.shape[0] != T:

@@ -627,7 +627,11 @@ fp8_status_t fp8_mx_swiglu_backward(const uint16_t* da, int64_t rows, int64_t in
  * fp8_grouped_gemm_scaled takes. out: bf16 [tokens x hidden] (ldo). Entries
  * whose expert index is outside [0, num_experts) add nothing; a token without a
  * valid entry gets zeros; an expert named twice by a token counts with the sum
- * of the two weights. Each token's result depends on its own row alone.
+ * of the two weights. No other token's values enter a token's result (a NaN or
+ * Inf of theirs included), and the same call gives the same bits; the order of
+ * the fp32 sums, and so a result's last bits, depends on how many tokens each
+ * expert has and how many experts are in use, so a token alone and the same
+ * token in a batch agree to fp32 rounding, not in every bit.
  * workspace: tokens * topk * inter * 4 bytes, 16-byte aligned, workspace_bytes
  * at least that; free for other use once the call's work is done, and calls
  * that may run at the same time need one each. Formats: OCP e4m3 / e5m2 (fnuz:

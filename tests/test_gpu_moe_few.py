@@ -339,3 +339,18 @@ def test_moe_few_largest_activations(fp8, orc, sign):
     # two roundings of the activation, its two parts to 2^-16, the output's half step
     assert abs(got[5] - want) <= (BF + 2.0 ** -16 + 4 * layer.U) * abs(want) * (1 + BF)
     assert not got[:5].any() and not got[6:].any()
+
+
+@pytest.mark.parametrize("T,k", [(9, 2), (40, 3)])
+def test_moe_few_other_tokens_values(fp8, orc, T, k):
+    """With the same routing a token's bits do not depend on the other tokens' values,
+    NaN and Inf among them."""
+    rng = np.random.default_rng(T + 21)
+    d = make(orc, rng, T, k, 4, 144, 80)
+    say("moe few, other tokens' values", T, k)
+    want = call(fp8, d)
+    for t in (0, 5, T - 1):
+        x = workloads.bf16_bits(rng.standard_normal((T, 144)).astype(np.float32) * 100)
+        x[::2, 3], x[1::2, 4] = 0x7FC0, 0xFF80
+        x[t] = d["x"][t]
+        assert torch.equal(call(fp8, dict(d, x=x))[t], want[t]), t
