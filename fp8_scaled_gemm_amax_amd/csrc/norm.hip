@@ -558,11 +558,13 @@ unsigned row_grid(int64_t rows) { return (unsigned)(rows < kLaunchRows ? rows : 
 template <int F, bool LOOSE>
 hipError_t norm_quant_reg(const NormFwd& p, hipStream_t st) {
     const int64_t nch = (p.cols + 7) / 8;
-    // One wavefront a row where it holds the row (16384 x 2048: 32.0 us, 38.0 with
-    // four) unless the rows are few (1000 x 2048: 6.2 us with one, 4.7 with four;
-    // 16 x 2048: 5.4 and 3.4); longer rows as many wavefronts as they fill (8192 x
-    // 5120: 41.0 us with four, 37.6 with three; x 10240 76 with eight, 67.5 with
-    // five; two chunks a lane for these sizes 38.9 and 85).
+    // One wavefront a row where it holds the row (16384 x 2048: 22.9 us, 31.0 with
+    // the checkpoint; with four wavefronts 28.2 and 34.6) unless the rows are few
+    // (1000 x 2048: 3.5 and 4.2 us with four wavefronts, 4.1 and 5.4 with one; 16 x
+    // 2048: 2.8 and 3.0, 3.8 and 4.7); longer rows as many wavefronts as they fill
+    // (8192 x 5120: 27.4 and 38.7 us with three, 29.9 and 42.1 with four; x 10240 49.0
+    // and 68 with five, 54 and 76 with eight; two chunks a lane for these sizes, five
+    // and ten wavefronts, 29.8 and 39.3, 63 and 80). RMS, on the device.
     const bool wide = nch > 256 || (nch > 64 && p.rows < 1024);
     const dim3 grid((unsigned)(wide ? p.rows : (p.rows + kWaves - 1) / kWaves));
 #define FP8_NORM_CASE(C, W) \
