@@ -29,7 +29,9 @@ __all__ = [
     "fp8_swiglu_quantize_row", "fp8_moe_unpermute_combine", "fp8_blockwise_quantize_act",
     "fp8_blockwise_quantize_weight", "NORM_LAYER", "NORM_RMS", "MOE_FEW_TOKENS", "fp8_norm_quantize_row",
     "norm_workspace", "fp8_norm_backward", "fp8_mx_norm_backward", "fp8_swiglu_quantize_row_mx",
-    "fp8_swiglu_backward", "fp8_mx_swiglu_backward", "moe_few_workspace", "fp8_moe_few_tokens", "EXPORTED_SYMBOLS",
+    "fp8_swiglu_backward", "fp8_mx_swiglu_backward", "moe_few_workspace", "fp8_moe_few_tokens",
+    "fp8_add_norm_quantize_row", "fp8_add_norm_backward", "fp8_mx_add_norm_backward", "fp8_gemm_swiglu",
+    "fp8_gemm_swiglu_backward", "lora_workspace", "fp8_lora_add", "LORA_MAX_RANK", "EXPORTED_SYMBOLS",
 ]
 
 E4M3, E5M2, E4M3_FNUZ, E5M2_FNUZ = 0, 1, 2, 3
@@ -48,13 +50,15 @@ EXPORTED_SYMBOLS = (
     "fp8_swiglu_quantize_row", "fp8_moe_unpermute_combine", "fp8_blockwise_quantize_act",
     "fp8_blockwise_quantize_weight", "fp8_norm_quantize_row", "fp8_norm_backward_workspace", "fp8_norm_backward",
     "fp8_mx_norm_backward", "fp8_swiglu_quantize_row_mx", "fp8_swiglu_backward", "fp8_mx_swiglu_backward",
-    "fp8_moe_few_tokens",
+    "fp8_moe_few_tokens", "fp8_add_norm_quantize_row", "fp8_add_norm_backward", "fp8_mx_add_norm_backward",
+    "fp8_gemm_swiglu", "fp8_gemm_swiglu_backward", "fp8_lora_add", "fp8_lora_workspace",
 )
 
 GROUP_K_ALIGN = 256     # FP8_GROUP_K_ALIGN of the C header
 MAX_ROW_BATCH = 8       # FP8_MAX_ROW_BATCH of the C header
 MX_BLOCK = 32           # FP8_MX_BLOCK of the C header
 MOE_FEW_TOKENS = 64     # FP8_MOE_FEW_TOKENS of the C header
+LORA_MAX_RANK = 128     # FP8_LORA_MAX_RANK of the C header
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8amax.so")
 
@@ -109,6 +113,14 @@ def _load():
         "fp8_mx_swiglu_backward": [P, I64, I64, I64, P, I, I64, P, I64, P, I64, P, I64, P],
         "fp8_moe_few_tokens": [P, I64, I64, I64, P, P, I32, I32, P, I, I64, I64, P, P, I, I64, I64, P, I64, P, I64, P,
                                I64, P],
+        "fp8_add_norm_quantize_row": [P, I64, I64, I64, P, I64, P, I64, P, P, I, F, I, I, I32, P, I64, P, P, I64, P, P, P,
+                                      I, I64, P, I64, P],
+        "fp8_add_norm_backward": [P, I64, P, I64, I64, I64, P, I64, P, I, P, P, I, P, I64, P, P, P, I64, P],
+        "fp8_mx_add_norm_backward": [P, I64, P, I64, I64, I64, P, I, I64, P, I64, P, P, I, P, I, P, I64, P, P, P, I64, P,
+                                     I64, P],
+        "fp8_gemm_swiglu": [P, I, I64, P, I, I64, I64, I64, I64, P, I, P, I, P, I64, P, I64, P],
+        "fp8_gemm_swiglu_backward": [P, I, I64, P, I, I64, I64, I64, I64, P, I, P, I, P, I64, P, I64, P, I64, P],
+        "fp8_lora_add": [P, I64, I64, I64, P, P, I64, I64, P, I64, I64, P, I32, I32, I64, P, I64, P, I64, P, I64, P],
     }
     for name, args in sigs.items():
         fn = getattr(L, name)
@@ -116,6 +128,8 @@ def _load():
         fn.restype = I
     L.fp8_norm_backward_workspace.argtypes = [I64, I64]
     L.fp8_norm_backward_workspace.restype = I64
+    L.fp8_lora_workspace.argtypes = [I64, I32]
+    L.fp8_lora_workspace.restype = I64
     L.fp8_status_string.argtypes = [I]
     L.fp8_status_string.restype = ctypes.c_char_p
     L.fp8_last_error.argtypes = []
@@ -729,3 +743,146 @@ def fp8_moe_few_tokens(x, expert_idx, weights, w1, f1, w1_scale_inv, w2, f2, w2_
     _call(lib.fp8_moe_few_tokens, dev, _addr(x), T, H, ldx, _addr(expert_idx), _addr(weights), k, E, _addr(w1), f1,
           w1.stride(1), w1.stride(0) if E > 1 else 0, _addr(w1_scale_inv), _addr(w2), f2, w2.stride(1),
           w2.stride(0) if E > 1 else 0, _addr(w2_scale_inv), inter, _addr(out), ldo, ws, ws_bytes)
+
+
+def fp8_add_norm_quantize_row(x, res, sum_out, gamma, beta, eps, kind, fmt, margin, q, scale_inv_out, y=None,
+                              mean_out=None, rstd_out=None, xhat_q=None, xhat_fmt=E4M3, xhat_scale=None):
+    """fp8_norm_quantize_row of sum_out = bf16(x + res), all bf16 [rows x cols]: the
+    norm is that of the stored sum. sum_out may be res or x (the residual stream
+    updated in place); no other output may overlap another or an input."""
+    rows, cols, ldx = _rows(x, "x")
+    ldres, ldsum = _like(res, "res", rows, cols), _like(sum_out, "sum_out", rows, cols)
+    w_type = _norm_weights(gamma, beta, cols)
+    ldq = _like(q, "q", rows, cols, 1) if q is not None else cols
+    ldy = _like(y, "y", rows, cols) if y is not None else cols
+    for name, t in (("scale_inv_out", scale_inv_out), ("mean_out", mean_out), ("rstd_out", rstd_out)):
+        _vec(t, name, rows)
+    ldxq = lds = 0
+    if xhat_q is not None or xhat_scale is not None:
+        if xhat_q is None:
+            raise ValueError("xhat_scale needs xhat_q")
+        ldxq, lds = _checkpoint(xhat_q, "xhat_q", xhat_scale, rows, cols)
+    dev = _on(x, res, sum_out, gamma, beta, q, scale_inv_out, y, mean_out, rstd_out, xhat_q, xhat_scale)
+    _call(lib.fp8_add_norm_quantize_row, dev, _addr(x), rows, cols, ldx, _addr(res), ldres, _addr(sum_out), ldsum,
+          _addr(gamma), _addr(beta), w_type, eps, kind, fmt, margin, _addr(q), ldq, _addr(scale_inv_out), _addr(y), ldy,
+          _addr(mean_out), _addr(rstd_out), _addr(xhat_q), xhat_fmt, ldxq, _addr(xhat_scale), lds)
+
+
+def fp8_add_norm_backward(dsum, dy, sum, gamma, mean, rstd, kind, dx, dgamma=None, dbeta=None, workspace=None):
+    """The gradient of fp8_add_norm_quantize_row's two inputs, dx = dsum + the norm's
+    gradient of dy (dsum: what flows into the sum past the norm), all bf16 [rows x
+    cols]; otherwise as fp8_norm_backward. dx may be dsum."""
+    rows, cols, lddy = _rows(dy, "dy")
+    ldds, ldsum = _like(dsum, "dsum", rows, cols), _like(sum, "sum", rows, cols)
+    lddx = _like(dx, "dx", rows, cols)
+    w_type = _norm_weights(gamma, None, cols)
+    _vec(mean, "mean", rows)
+    _vec(rstd, "rstd", rows)
+    _vec(dgamma, "dgamma", cols)
+    _vec(dbeta, "dbeta", cols)
+    ws, ws_bytes = _workspace(workspace)
+    dev = _on(dy, dsum, sum, gamma, mean, rstd, dx, dgamma, dbeta, workspace)
+    _call(lib.fp8_add_norm_backward, dev, _addr(dsum), ldds, _addr(dy), rows, cols, lddy, _addr(sum), ldsum,
+          _addr(gamma), w_type, _addr(mean), _addr(rstd), kind, _addr(dx), lddx, _addr(dgamma), _addr(dbeta), ws,
+          ws_bytes)
+
+
+def fp8_mx_add_norm_backward(dsum, dy, xhat_q, xhat_fmt, xhat_scale, gamma, beta, rstd, kind, dx, dgamma=None,
+                             dbeta=None, y=None, workspace=None):
+    """fp8_add_norm_backward from the 8-bit checkpoint of the normalised rows, as
+    fp8_mx_norm_backward. dx may be dsum."""
+    rows, cols, lddy = _rows(dy, "dy")
+    ldds, lddx = _like(dsum, "dsum", rows, cols), _like(dx, "dx", rows, cols)
+    ldy = _like(y, "y", rows, cols) if y is not None else cols
+    ldxq, lds = _checkpoint(xhat_q, "xhat_q", xhat_scale, rows, cols)
+    w_type = _norm_weights(gamma, beta, cols)
+    _vec(rstd, "rstd", rows)
+    _vec(dgamma, "dgamma", cols)
+    _vec(dbeta, "dbeta", cols)
+    ws, ws_bytes = _workspace(workspace)
+    dev = _on(dy, dsum, xhat_q, xhat_scale, gamma, beta, rstd, dx, dgamma, dbeta, y, workspace)
+    _call(lib.fp8_mx_add_norm_backward, dev, _addr(dsum), ldds, _addr(dy), rows, cols, lddy, _addr(xhat_q), xhat_fmt,
+          ldxq, _addr(xhat_scale), lds, _addr(gamma), _addr(beta), w_type, _addr(rstd), kind, _addr(dx), lddx,
+          _addr(dgamma), _addr(dbeta), _addr(y), ldy, ws, ws_bytes)
+
+
+def _factors(t, name, mode, n):
+    _vec(t, name, n if mode == SCALE_VECTOR else 1)
+
+
+def fp8_gemm_swiglu(a, fa, b, fb, a_scale_inv, a_mode, b_scale_inv, b_mode, act, h=None):
+    """The gate and up projections with SwiGLU in one kernel: [g | u] = (a [m x k]
+    codes) * (b [2I x k] codes, gate rows then up rows)^T, scaled as
+    fp8_gemm_scaled; act bf16 [m x I] = silu(g) * u; h bf16 [m x 2I] (or None)
+    receives [g | u]. Outputs do not overlap each other or the inputs."""
+    m, k, lda = _rows(a, "a", 1)
+    two_i, kb, ldb = _rows(b, "b", 1)
+    if kb != k or two_i % 2:
+        raise ValueError(f"b must be [2I x {k}] (gate rows, then up rows), got {tuple(b.shape)}")
+    ldact = _like(act, "act", m, two_i // 2)
+    ldh = _like(h, "h", m, two_i) if h is not None else two_i
+    _factors(a_scale_inv, "a_scale_inv", a_mode, m)
+    _factors(b_scale_inv, "b_scale_inv", b_mode, two_i)
+    dev = _on(a, b, a_scale_inv, b_scale_inv, act, h)
+    _call(lib.fp8_gemm_swiglu, dev, _addr(a), fa, lda, _addr(b), fb, ldb, m, two_i // 2, k, _addr(a_scale_inv), a_mode,
+          _addr(b_scale_inv), b_mode, _addr(act), ldact, _addr(h), ldh)
+
+
+def fp8_gemm_swiglu_backward(a, fa, b, fb, a_scale_inv, a_mode, b_scale_inv, b_mode, h, dh, act=None):
+    """SwiGLU's backward pass in the product that gives the activation's gradient: da
+    = (a [m x k] codes) * (b [I x k] codes)^T, scaled as fp8_gemm_scaled and not
+    stored; dh bf16 [m x 2I] = [d(gate) | d(up)] from h bf16 [m x 2I]; act (bf16 [m
+    x I], or None) receives silu(gate) * up. Outputs do not overlap each other or
+    the inputs."""
+    m, k, lda = _rows(a, "a", 1)
+    inter, kb, ldb = _rows(b, "b", 1)
+    if kb != k:
+        raise ValueError(f"a has k = {k} but b has k = {kb}")
+    ldh, lddh = _like(h, "h", m, 2 * inter), _like(dh, "dh", m, 2 * inter)
+    ldact = _like(act, "act", m, inter) if act is not None else inter
+    _factors(a_scale_inv, "a_scale_inv", a_mode, m)
+    _factors(b_scale_inv, "b_scale_inv", b_mode, inter)
+    dev = _on(a, b, a_scale_inv, b_scale_inv, h, dh, act)
+    _call(lib.fp8_gemm_swiglu_backward, dev, _addr(a), fa, lda, _addr(b), fb, ldb, m, inter, k, _addr(a_scale_inv),
+          a_mode, _addr(b_scale_inv), b_mode, _addr(h), ldh, _addr(dh), lddh, _addr(act), max(ldact, 1))
+
+
+def lora_workspace(tokens, rank, device="cuda:0"):
+    """A workspace that fp8_lora_add accepts for these sizes."""
+    return torch.empty(lib.fp8_lora_workspace(tokens, rank) // 4, dtype=torch.float32, device=device)
+
+
+def _stack(t, name):
+    """(n, rows, cols, row stride, stride of the first dimension) of a bf16 [n x rows x cols] tensor."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D torch.bfloat16 tensor, got {tuple(t.shape)} {t.dtype}")
+    n, rows, cols = t.shape
+    if t.stride(2) != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    ld = t.stride(1) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name}'s rows overlap (row stride {ld}, {cols} columns): make it contiguous")
+    return n, rows, cols, ld, t.stride(0) if n > 1 else 0
+
+
+def fp8_lora_add(x, lora_a, lora_b, scaling, adapter_idx, base, out, workspace):
+    """Adapters of many requests beside a shared projection: out[t] = base[t] +
+    scaling[e] * (x_t A_e^T) B_e^T, e = adapter_idx[t] (outside [0, E): base is
+    copied). x bf16 [T x K]; lora_a bf16 [E x r x K]; lora_b bf16 [E x N x r];
+    scaling fp32 [E]; adapter_idx int32 [T] on the device; base (None for zeros),
+    out bf16 [T x N]; workspace: lora_workspace(T, r), one for each call that may
+    run at the same time. out may be base."""
+    T, K, ldx = _rows(x, "x")
+    E, r, ka, lda, gsa = _stack(lora_a, "lora_a")
+    eb, N, rb, ldb, gsb = _stack(lora_b, "lora_b")
+    if ka != K or eb != E or rb != r:
+        raise ValueError(f"lora_a {tuple(lora_a.shape)} and lora_b {tuple(lora_b.shape)} do not match each other or x's "
+                         f"{K} columns")
+    ldout = _like(out, "out", T, N)
+    ldbase = _like(base, "base", T, N) if base is not None else max(N, 1)
+    _vec(scaling, "scaling", E)
+    _vec(adapter_idx, "adapter_idx", T, torch.int32)
+    ws, ws_bytes = _workspace(workspace)
+    dev = _on(x, lora_a, lora_b, scaling, adapter_idx, base, out, workspace)
+    _call(lib.fp8_lora_add, dev, _addr(x), T, K, ldx, _addr(adapter_idx), _addr(lora_a), lda, gsa, _addr(lora_b), ldb,
+          gsb, _addr(scaling), E, r, N, _addr(base), ldbase, _addr(out), ldout, ws, ws_bytes)

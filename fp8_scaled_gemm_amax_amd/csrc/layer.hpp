@@ -16,6 +16,10 @@ constexpr int64_t kNormMaxBands = 512;              // bands of rows of the weig
 struct NormFwd {
     const uint16_t* x;
     int64_t rows, cols, ldx;
+    const uint16_t* res;                            // NULL: the norm of x, else of sum = bf16(x + res)
+    int64_t ldres;
+    uint16_t* sum;
+    int64_t ldsum;
     const void *gamma, *beta;
     int w_f32, rms, margin, ckpt_e5m2;
     float eps;
@@ -32,11 +36,13 @@ struct NormFwd {
 };
 
 // x (with mean and rstd) or xq / xs (with rstd): where the normalised rows come
-// from. partial: kNormMaxBands * 2 * cols floats at most; band, longer and bands
+// from. ds (NULL: none): what is added to dx. partial: kNormMaxBands * 2 * cols floats at most; band, longer and bands
 // are the launcher's.
 struct NormBwd {
     const uint16_t* dy;
     int64_t rows, cols, lddy;
+    const uint16_t* ds;
+    int64_t ldds;
     const uint16_t* x;
     int64_t ldx;
     const uint8_t* xq;
@@ -64,11 +70,13 @@ inline bool chunked(const void* p, int64_t ld, unsigned align) {
 }
 inline bool norm_vector_layout(const NormFwd& p) {
     return p.cols % 8 == 0 && p.cols <= kNormMaxVecCols && chunked(p.x, p.ldx, 16) && chunked(p.gamma, 0, 16) &&
-           chunked(p.beta, 0, 16) && chunked(p.q, p.ldq, 8) && chunked(p.y, p.ldy, 16);
+           chunked(p.beta, 0, 16) && chunked(p.q, p.ldq, 8) && chunked(p.y, p.ldy, 16) &&
+           chunked(p.res, p.ldres, 16) && chunked(p.sum, p.ldsum, 16);
 }
 inline bool norm_vector_layout(const NormBwd& p) {
     return p.cols % 8 == 0 && p.cols <= kNormMaxVecCols && chunked(p.dy, p.lddy, 16) && chunked(p.dx, p.lddx, 16) &&
-           chunked(p.gamma, 0, 16) && chunked(p.beta, 0, 16) && chunked(p.x, p.ldx, 16) && chunked(p.y, p.ldy, 16);
+           chunked(p.gamma, 0, 16) && chunked(p.beta, 0, 16) && chunked(p.x, p.ldx, 16) && chunked(p.y, p.ldy, 16) &&
+           chunked(p.ds, p.ldds, 16);
 }
 // Columns and slices of the rows of a workgroup of the weights' gradients in any
 // layout, and its grid over the columns: at most 2^21 workgroups side by side,

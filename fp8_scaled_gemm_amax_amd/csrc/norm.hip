@@ -8,6 +8,11 @@
 //   backward: w = dy gamma, dx = rstd (w - mean(w) - xh mean(w xh))
 //     (RMS: without mean(w)), dgamma = sum_r dy xh, dbeta = sum_r dy
 //
+// ADD: x is the sum of two inputs, s = bf16(x + r), formed in the same read and
+// stored; the norm takes the stored (rounded) values, which the backward pass will
+// read too. Backward, s's own gradient ds is added: dx = ds + the above, for both
+// inputs.
+//
 // Everything here is bound by HBM: the rows are held in registers from their
 // one read to their last use, and all statistics and sums are fp32.
 #include "layer.hpp"
@@ -58,7 +63,7 @@ __device__ __forceinline__ float load_weight(const void* w, int w_f32, int64_t c
 // WPR wavefronts per row. The variance is the second pass over the registers
 // (sum of (x - mu)^2), so a row whose mean is large against its deviation
 // loses nothing. y is formed in fp32 and cast from there.
-template <int F, int MAXC, int WPR, bool LOOSE>
+template <int F, int MAXC, int WPR, bool LOOSE, bool ADD>
 __global__ __launch_bounds__(WPR == 1 ? kBlock : WPR * 64) void k_norm_quant_row(NormFwd p) {
     __shared__ float red[3][WPR];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -70,17 +75,31 @@ __global__ __launch_bounds__(WPR == 1 ? kBlock : WPR * 64) void k_norm_quant_row
     const int nch = (int)((n + 7) >> 3);
     const float inv_n = 1.0f / (float)p.cols;
     const uint16_t* xr = p.x + row * p.ldx;
-    uint4 raw[MAXC];
+    uint4 raw[MAXC], res[ADD ? MAXC : 1];
 #pragma unroll
     for (int c = 0; c < MAXC; ++c) {
         const int ch = t + c * TPR;
         raw[c] = load_chunk<LOOSE>(xr, (uint32_t)(ch < nch ? ch : nch - 1), n);
+        if constexpr (ADD) res[c] = load_chunk<LOOSE>(p.res + row * p.ldres, (uint32_t)(ch < nch ? ch : nch - 1), n);
     }
     float v[MAXC][8];
 #pragma unroll
     for (int c = 0; c < MAXC; ++c) {
-        place_chunk<LOOSE>(&raw[c], (uint32_t)(t + c * TPR), n);
-        if (t + c * TPR >= nch) raw[c] = make_uint4(0u, 0u, 0u, 0u);        // past the row: zeros
+        const int ch = t + c * TPR;
+        place_chunk<LOOSE>(&raw[c], (uint32_t)ch, n);
+        if constexpr (ADD) {
+            place_chunk<LOOSE>(&res[c], (uint32_t)ch, n);
+            float x[8], r[8];
+            unpack8(raw[c], x);
+            unpack8(res[c], r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] += r[i];
+            // (the sum may take an input's place: a lane reads of a chunk only what it
+            // stores, the values of a cut chunk's neighbour aside, which it drops)
+            if (ch < nch) store_chunk<LOOSE>(p.sum + row * p.ldsum, (uint32_t)ch, n, x);
+            raw[c] = pack8(x);
+        }
+        if (ch >= nch) raw[c] = make_uint4(0u, 0u, 0u, 0u);                 // past the row: zeros
         unpack8(raw[c], v[c]);
     }
     float mean = 0.0f;
@@ -192,13 +211,20 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 }
 __device__ __forceinline__ float load_bf16(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 
-template <int F>
+template <int F, bool ADD>
 __global__ __launch_bounds__(kBlock) void k_norm_quant_row_any(NormFwd p) {
     __shared__ float red[kWaves];
     __shared__ uint32_t redu[kWaves];
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
     const uint16_t* xr = p.x + row * p.ldx;
+    if constexpr (ADD) {                // (a thread reads of the sum what it wrote)
+        const uint16_t* rr = p.res + row * p.ldres;
+        uint16_t* sr = p.sum + row * p.ldsum;
+        for (int64_t c = tid; c < p.cols; c += kBlock)
+            sr[c] = (uint16_t)f32_to_bf16(load_bf16(xr + c) + load_bf16(rr + c));
+        xr = sr;
+    }
     const float inv_n = 1.0f / (float)p.cols;
     float mean = 0.0f, s = 0.0f;
     if (!p.rms) {
@@ -250,16 +276,17 @@ __global__ __launch_bounds__(kBlock) void k_norm_quant_row_any(NormFwd p) {
 // workspace; k_norm_weight_grad adds the bands in order. No atomics: results
 // do not depend on timing.
 // SRC: 0 = x in bf16 with mean and rstd, 1 / 2 = the checkpoint in e4m3 / e5m2.
-template <int SRC, int MAXC>
+template <int SRC, int MAXC, bool ADD>
 struct RowData {
-    uint4 dy[MAXC];
+    uint4 dy[MAXC], ds[ADD && SRC == 0 ? MAXC : 1];
     uint32_t x[MAXC][SRC == 0 ? 4 : 2];
     uint32_t byte[MAXC];                // (SRC > 0: the block's scale)
     float mean, rstd;
 };
 
-template <int SRC, int TPR, int MAXC, bool LOOSE>
-__device__ __forceinline__ void load_row(const NormBwd& p, int row, uint32_t tt, uint32_t nch, RowData<SRC, MAXC>* d) {
+template <int SRC, int TPR, int MAXC, bool LOOSE, bool ADD>
+__device__ __forceinline__ void load_row(const NormBwd& p, int row, uint32_t tt, uint32_t nch,
+                                         RowData<SRC, MAXC, ADD>* d) {
     const uint32_t n = (uint32_t)p.cols;
     d->rstd = p.rstd[row];
     d->mean = SRC == 0 && p.mean ? p.mean[row] : 0.0f;
@@ -269,6 +296,7 @@ __device__ __forceinline__ void load_row(const NormBwd& p, int row, uint32_t tt,
         const uint32_t ch = tt + c * TPR;
         const uint32_t cc = ch < nch ? ch : nch - 1;    // (past the row: a duplicate, never stored)
         d->dy[c] = load_chunk<LOOSE>(dr, cc, n);
+        if constexpr (ADD && SRC == 0) d->ds[c] = load_chunk<LOOSE>(p.ds + row * p.ldds, cc, n);
         if constexpr (SRC == 0) {
             const uint4 x = load_chunk<LOOSE>(p.x + row * p.ldx, cc, n);
             d->x[c][0] = x.x;
@@ -298,8 +326,8 @@ __device__ __forceinline__ void store_sums(float* p, uint32_t ch, uint32_t n, co
 }
 
 // Chunk c of the row as fp32.
-template <int SRC, int MAXC>
-__device__ __forceinline__ void row_values(const RowData<SRC, MAXC>& d, int c, float* xh, float* dy) {
+template <int SRC, int MAXC, bool ADD>
+__device__ __forceinline__ void row_values(const RowData<SRC, MAXC, ADD>& d, int c, float* xh, float* dy) {
     unpack8(d.dy[c], dy);
     if constexpr (SRC == 0) {
         unpack8(make_uint4(d.x[c][0], d.x[c][1], d.x[c][2], d.x[c][3]), xh);
@@ -314,7 +342,7 @@ __device__ __forceinline__ void row_values(const RowData<SRC, MAXC>& d, int c, f
     }
 }
 
-template <int SRC, int TPR, int MAXC, int WG, bool LOOSE>
+template <int SRC, int TPR, int MAXC, int WG, bool LOOSE, bool ADD>
 __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
     constexpr int TEAMS = WG / TPR, NW = TPR / 64;
     __shared__ float2 red[2][WG / 64];
@@ -349,8 +377,8 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
         }
     }
     if (SRC > 0) __syncthreads();
-    RowData<SRC, MAXC> cur, nxt;
-    load_row<SRC, TPR, MAXC, LOOSE>(p, r0 + team < r1 ? r0 + team : r1 - 1, tt, nch, &cur);
+    RowData<SRC, MAXC, ADD> cur, nxt;
+    load_row<SRC, TPR, MAXC, LOOSE, ADD>(p, r0 + team < r1 ? r0 + team : r1 - 1, tt, nch, &cur);
     int buf = 0;
     for (int r = r0; r < r1; r += TEAMS, buf ^= 1) {
         const int row = r + team;
@@ -359,7 +387,19 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
         // tt opaque in every step: offsets are then formed where they are used,
         // next to scalar bases, and not kept as 64-bit pairs over the loop
         asm volatile("" : "+v"(tt));
-        load_row<SRC, TPR, MAXC, LOOSE>(p, next < r1 ? next : r1 - 1, tt, nch, &nxt);
+        load_row<SRC, TPR, MAXC, LOOSE, ADD>(p, next < r1 ? next : r1 - 1, tt, nch, &nxt);
+        // from a checkpoint, ds of the row at hand (a row ahead it spilled)
+        uint4 ds[ADD ? MAXC : 1];
+        if constexpr (ADD) {
+#pragma unroll
+            for (int c = 0; c < MAXC; ++c) {
+                const uint32_t ch = tt + c * TPR;
+                if constexpr (SRC > 0)
+                    ds[c] = load_chunk<LOOSE>(p.ds + (int64_t)(live_row ? row : r1 - 1) * p.ldds, ch < nch ? ch : nch - 1, n);
+                else
+                    ds[c] = cur.ds[c];
+            }
+        }
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int c = 0; c < MAXC; ++c) {
@@ -369,6 +409,7 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
             if (LOOSE && live) {
                 uint4 x = make_uint4(cur.x[c][0], cur.x[c][1], cur.x[c][SRC == 0 ? 2 : 0], cur.x[c][SRC == 0 ? 3 : 0]);
                 place_chunk<LOOSE>(&cur.dy[c], ch, n);
+                if constexpr (ADD) place_chunk<LOOSE>(&ds[c], ch, n);
                 place_chunk<LOOSE>(&x, ch, n);
                 cur.x[c][0] = x.x;
                 cur.x[c][1] = x.y;
@@ -426,6 +467,12 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
             row_values<SRC>(cur, c, xh, dy);
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = cur.rstd * (fmaf(-c1, xh[i], dy[i] * g[c][i]) - c2);
+            if constexpr (ADD) {
+                float d[8];
+                unpack8(ds[c], d);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] += d[i];
+            }
             if (live) store_chunk<LOOSE>(p.dx + row * p.lddx, ch, n, o);
             if (live_row) {         // (uniform; the duplicate of a row could add 0 * Inf)
 #pragma unroll
@@ -518,7 +565,8 @@ __global__ __launch_bounds__(kBlock) void k_norm_grad_row_any(NormBwd p) {
         for (int64_t c = tid; c < p.cols; c += kBlock) {
             const float w = load_bf16(dr + c) * (p.gamma ? load_weight(p.gamma, p.w_f32, c) : 1.0f);
             const float xh = (load_bf16(xr + c) - mean) * rstd;
-            p.dx[row * p.lddx + c] = (uint16_t)f32_to_bf16(rstd * (fmaf(-c1, xh, w) - c2));
+            const float ds = p.ds ? load_bf16(p.ds + row * p.ldds + c) : 0.0f;
+            p.dx[row * p.lddx + c] = (uint16_t)f32_to_bf16(ds + rstd * (fmaf(-c1, xh, w) - c2));
         }
     }
 }
@@ -555,7 +603,7 @@ unsigned row_grid(int64_t rows) { return (unsigned)(rows < kLaunchRows ? rows : 
 
 }  // namespace
 
-template <int F, bool LOOSE>
+template <int F, bool LOOSE, bool ADD>
 hipError_t norm_quant_reg(const NormFwd& p, hipStream_t st) {
     const int64_t nch = (p.cols + 7) / 8;
     // One wavefront a row where it holds the row (16384 x 2048: 22.9 us, 31.0 with
@@ -568,7 +616,7 @@ hipError_t norm_quant_reg(const NormFwd& p, hipStream_t st) {
     const bool wide = nch > 256 || (nch > 64 && p.rows < 1024);
     const dim3 grid((unsigned)(wide ? p.rows : (p.rows + kWaves - 1) / kWaves));
 #define FP8_NORM_CASE(C, W) \
-    hipLaunchKernelGGL((k_norm_quant_row<F, C, W, LOOSE>), grid, dim3(W == 1 ? kBlock : W * 64), 0, st, p)
+    hipLaunchKernelGGL((k_norm_quant_row<F, C, W, LOOSE, ADD>), grid, dim3(W == 1 ? kBlock : W * 64), 0, st, p)
     if (wide) {
         if (nch <= 256) FP8_NORM_CASE(1, 4);
         else if (nch <= 384) FP8_NORM_CASE(2, 3);
@@ -587,12 +635,17 @@ hipError_t norm_quant_reg(const NormFwd& p, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <int F, bool ADD>
+hipError_t norm_quant_add(const NormFwd& p, hipStream_t st) {
+    if (norm_vector_layout(p)) return norm_quant_reg<F, false, ADD>(p, st);
+    if (p.cols >= 8 && p.cols <= kNormMaxVecCols) return norm_quant_reg<F, true, ADD>(p, st);
+    hipLaunchKernelGGL((k_norm_quant_row_any<F, ADD>), dim3((unsigned)p.rows), dim3(kBlock), 0, st, p);
+    return hipGetLastError();
+}
+
 template <int F>
 hipError_t norm_quant_fmt(const NormFwd& p, hipStream_t st) {
-    if (norm_vector_layout(p)) return norm_quant_reg<F, false>(p, st);
-    if (p.cols >= 8 && p.cols <= kNormMaxVecCols) return norm_quant_reg<F, true>(p, st);
-    hipLaunchKernelGGL((k_norm_quant_row_any<F>), dim3((unsigned)p.rows), dim3(kBlock), 0, st, p);
-    return hipGetLastError();
+    return p.res ? norm_quant_add<F, true>(p, st) : norm_quant_add<F, false>(p, st);
 }
 
 hipError_t launch_norm_quant_row(const NormFwd& p0, int fmt, hipStream_t st) {
@@ -600,6 +653,10 @@ hipError_t launch_norm_quant_row(const NormFwd& p0, int fmt, hipStream_t st) {
         NormFwd p = p0;
         p.rows = p0.rows - r0 < kLaunchRows ? p0.rows - r0 : kLaunchRows;
         p.x += r0 * p.ldx;
+        if (p.res) {
+            p.res += r0 * p.ldres;
+            p.sum += r0 * p.ldsum;
+        }
         if (p.q) p.q += r0 * p.ldq;
         if (p.scale_inv) p.scale_inv += r0;
         if (p.y) p.y += r0 * p.ldy;
@@ -621,8 +678,8 @@ hipError_t launch_norm_quant_row(const NormFwd& p0, int fmt, hipStream_t st) {
     return hipSuccess;
 }
 
-template <int SRC, bool LOOSE>
-hipError_t norm_grad_src(NormBwd p, hipStream_t st) {
+template <int SRC, bool LOOSE, bool ADD>
+hipError_t norm_grad_add(NormBwd p, hipStream_t st) {
     const int64_t nch = (p.cols + 7) / 8;
     // 16 wavefronts a CU either way: as one workgroup they leave half as many
     // partial sums (8192 x 4096: 42.4 us with 1024 threads, 44.8 with 512), as two
@@ -639,7 +696,7 @@ hipError_t norm_grad_src(NormBwd p, hipStream_t st) {
     p.band = p.rows / p.bands;
     p.longer = p.rows % p.bands;
     const dim3 grid((unsigned)p.bands);
-#define FP8_NORM_CASE(T, C, W) hipLaunchKernelGGL((k_norm_grad<SRC, T, C, W, LOOSE>), grid, dim3(W), 0, st, p)
+#define FP8_NORM_CASE(T, C, W) hipLaunchKernelGGL((k_norm_grad<SRC, T, C, W, LOOSE, ADD>), grid, dim3(W), 0, st, p)
     if (nch <= 64) FP8_NORM_CASE(64, 1, 512);
     else if (nch <= 128) FP8_NORM_CASE(64, 2, 512);
     else if (nch <= 256) FP8_NORM_CASE(128, 2, 512);
@@ -656,6 +713,11 @@ hipError_t norm_grad_src(NormBwd p, hipStream_t st) {
         e = hipGetLastError();
     }
     return e;
+}
+
+template <int SRC, bool LOOSE>
+hipError_t norm_grad_src(const NormBwd& p, hipStream_t st) {
+    return p.ds ? norm_grad_add<SRC, LOOSE, true>(p, st) : norm_grad_add<SRC, LOOSE, false>(p, st);
 }
 
 hipError_t launch_norm_backward(const NormBwd& p0, hipStream_t st) {

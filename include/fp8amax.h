@@ -648,6 +648,112 @@ fp8_status_t fp8_moe_few_tokens(const uint16_t* x, int64_t tokens, int64_t hidde
                                 int64_t w2_expert_stride, const float* w2_scale_inv, int64_t inter, uint16_t* out,
                                 int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* ------------------------------- the residual's addition, the norm and the cast --
+ * fp8_norm_quantize_row of a sum: sum = bf16(x + res) (fp32, rounded once),
+ * stored, and the norm of the STORED values, so that the backward pass, which
+ * reads sum, differentiates what the forward pass computed. x, res, sum: bf16
+ * [rows x cols] (ldx, ldres, ldsum), 2-byte aligned. sum may be res or x itself
+ * (the same pointer and leading dimension: the residual stream updated in
+ * place); otherwise outputs do not overlap each other or the inputs. The rest is
+ * fp8_norm_quantize_row's, and so are the layouts, which take res and sum 16-byte
+ * aligned with ldres and ldsum multiples of 8 too. */
+fp8_status_t fp8_add_norm_quantize_row(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, const uint16_t* res,
+                                       int64_t ldres, uint16_t* sum, int64_t ldsum, const void* gamma,
+                                       const void* beta, fp8_out_t w_type, float eps, fp8_norm_t kind,
+                                       fp8_format_t fmt, int32_t margin, uint8_t* q, int64_t ldq,
+                                       float* scale_inv_out, uint16_t* y, int64_t ldy, float* mean_out,
+                                       float* rstd_out, uint8_t* xhat_q, fp8_format_t xhat_fmt, int64_t ldxq,
+                                       uint8_t* xhat_scale, int64_t ld_scale, void* stream);
+
+/* Backward: dx = dsum + the norm's gradient of dy (fp8_norm_backward's dx, both in
+ * fp32, rounded once), the gradient of x and of res alike. dsum: bf16 [rows x
+ * cols] (lddsum), what flows into sum past the norm; sum: the forward pass's.
+ * dx may be dsum itself (the same pointer and leading dimension). Otherwise as
+ * fp8_norm_backward, its workspace included. */
+fp8_status_t fp8_add_norm_backward(const uint16_t* dsum, int64_t lddsum, const uint16_t* dy, int64_t rows, int64_t cols,
+                                   int64_t lddy, const uint16_t* sum, int64_t ldsum, const void* gamma,
+                                   fp8_out_t w_type, const float* mean, const float* rstd, fp8_norm_t kind,
+                                   uint16_t* dx, int64_t lddx, float* dgamma, float* dbeta, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
+/* The same from the forward pass's checkpoint (fp8_mx_norm_backward with dsum added). */
+fp8_status_t fp8_mx_add_norm_backward(const uint16_t* dsum, int64_t lddsum, const uint16_t* dy, int64_t rows,
+                                      int64_t cols, int64_t lddy, const uint8_t* xhat_q, fp8_format_t xhat_fmt,
+                                      int64_t ldxq, const uint8_t* xhat_scale, int64_t ld_scale, const void* gamma,
+                                      const void* beta, fp8_out_t w_type, const float* rstd, fp8_norm_t kind,
+                                      uint16_t* dx, int64_t lddx, float* dgamma, float* dbeta, uint16_t* y,
+                                      int64_t ldy, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------ the gated block's FP8 products --
+ * The gate and up projections of a gated feed-forward block with SwiGLU in the
+ * product's epilogue:
+ *   g = (a Wg^T) * a_scale * b_scale, u = (a Wu^T) likewise (fp32 sums),
+ *   act = silu(g) * u = g / (1 + exp(-g)) * u
+ * a: codes [m x k] (lda); b: codes [2 inter x k] (ldb), the inter gate rows, then
+ * the inter up rows (the b of an fp8_gemm_scaled with n = 2 inter); factors as
+ * fp8_gemm_scaled (b_scale_inv [2 inter] with FP8_SCALE_VECTOR). act: bf16 [m x
+ * inter] (ldact); h: bf16 [m x 2 inter] (ldh) = [g | u] for the backward pass, or
+ * NULL. Sums and SwiGLU in fp32, each output rounded once (act is not formed from
+ * the rounded h); an exp(-g) of 2^128 or more counts as infinite. A row's results
+ * do not depend on the other rows' values; the same call gives the same bits.
+ * k % 16 == 0 (k = 0: zeros); a, b 16-byte aligned with lda, ldb multiples of 16;
+ * act, h 2-byte aligned, with full-speed stores where they are 16-byte aligned
+ * and ldact, ldh, inter multiples of 8. OCP e4m3 / e5m2 (fnuz:
+ * FP8_ERR_UNSUPPORTED). Outputs do not overlap each other or the inputs. */
+fp8_status_t fp8_gemm_swiglu(const uint8_t* a, fp8_format_t fa, int64_t lda, const uint8_t* b, fp8_format_t fb,
+                             int64_t ldb, int64_t m, int64_t inter, int64_t k, const float* a_scale_inv,
+                             fp8_scale_mode_t a_mode, const float* b_scale_inv, fp8_scale_mode_t b_mode, uint16_t* act,
+                             int64_t ldact, uint16_t* h, int64_t ldh, void* stream);
+
+/* Its backward pass, in the product that gives the activation's gradient (dY
+ * times the down projection's weights):
+ *   da = (a b^T) * a_scale * b_scale (fp32 sums, not rounded), s = 1 / (1 + exp(-gate)),
+ *   d(gate) = da * up * s * (1 + gate * (1 - s)),   d(up) = da * gate * s
+ * a: codes [m x k] (of dY, k the block's outputs); b: codes [inter x k] (of the
+ * down weights transposed, as fp8_quantize_col gives them); h: bf16 [m x 2 inter]
+ * (ldh) = [gate | up]; dh: bf16 [m x 2 inter] (lddh) = [d(gate) | d(up)]; act
+ * (bf16 [m x inter] (ldact), or NULL): silu(gate) * up from the same read, what
+ * the down projection's weight gradient takes. Requirements as fp8_gemm_swiglu;
+ * h 2-byte aligned. An infinite gate follows the formula's arithmetic. */
+fp8_status_t fp8_gemm_swiglu_backward(const uint8_t* a, fp8_format_t fa, int64_t lda, const uint8_t* b,
+                                      fp8_format_t fb, int64_t ldb, int64_t m, int64_t inter, int64_t k,
+                                      const float* a_scale_inv, fp8_scale_mode_t a_mode, const float* b_scale_inv,
+                                      fp8_scale_mode_t b_mode, const uint16_t* h, int64_t ldh, uint16_t* dh,
+                                      int64_t lddh, uint16_t* act, int64_t ldact, void* stream);
+
+/* --------------------------------------------- adapters of many requests at once --
+ * Low-rank adapters beside a projection that many requests share (serving: the
+ * shared product of all tokens is one fp8_gemm_scaled, fp8_gemm_mx, ..; each
+ * token's own adapter is added to it):
+ *   out[t] = bf16( base[t] + scaling[e] * (x_t A_e^T) B_e^T ), e = adapter_idx[t]
+ * x: bf16 [tokens x k] (ldx); A: bf16 [adapters x rank x k] (row stride ld_a,
+ * adapter stride a_stride, elements); B: bf16 [adapters x n x rank] likewise;
+ * scaling: fp32 [adapters]; adapter_idx: int32 [tokens] (device), an index
+ * outside [0, adapters) for a token without an adapter, whose base is copied;
+ * base, out: bf16 [tokens x n] (ldbase, ldout); base NULL for zeros. out may be
+ * base itself (the same pointer and leading dimension), else outputs do not
+ * overlap the inputs. fp32 sums; the rank-wide intermediate is kept to 16
+ * significant bits, the output rounded once. Adapters of smaller rank are padded
+ * with zeros. Any order of tokens is served; neighbouring tokens of one adapter
+ * share its loads. No other token's or adapter's values enter a token's result,
+ * and the same call gives the same bits; the order of the fp32 sums depends on
+ * the number of tokens.
+ * rank a multiple of 8, 8..FP8_LORA_MAX_RANK; k a multiple of 8, >= 8; adapters >=
+ * 1; x, A, B 16-byte aligned with ldx, ld_a, ld_b and the adapter strides multiples
+ * of 8 (strides >= 0); base, out 2-byte aligned, at full speed 16-byte aligned with
+ * ldbase, ldout multiples of 8. workspace: fp8_lora_workspace(tokens, rank) bytes
+ * at least, 16-byte aligned; free for other use once the call's work is done;
+ * calls that may run at the same time need one each. */
+#define FP8_LORA_MAX_RANK 128
+fp8_status_t fp8_lora_add(const uint16_t* x, int64_t tokens, int64_t k, int64_t ldx, const int32_t* adapter_idx,
+                          const uint16_t* a, int64_t ld_a, int64_t a_stride, const uint16_t* b, int64_t ld_b,
+                          int64_t b_stride, const float* scaling, int32_t adapters, int32_t rank, int64_t n,
+                          const uint16_t* base, int64_t ldbase, uint16_t* out, int64_t ldout, void* workspace,
+                          int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for these sizes; 0 for sizes that are not valid. */
+int64_t fp8_lora_workspace(int64_t tokens, int32_t rank);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,206 @@
+"""GPU parity of the gated FP8 products (gate and up with SwiGLU, and the backward
+pass's product with SwiGLU's gradient) against the fp64 definitions of
+oracle/block.py: every output within the fp32 evaluation's bound plus half a step
+of bf16. Sizes around every kernel's tile and every rule that chooses one, odd
+sizes, views with guard bands, scalar and vector factors, both formats."""
+import numpy as np
+import pytest
+import torch
+
+import workloads
+from helpers import check_guard, dev_bf16, dev_f32, dev_u8, guarded, host_bits, say
+from oracle import block, layer
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF = block.BF16
+
+
+@pytest.fixture(scope="module")
+def fp8():
+    import fp8_scaled_gemm_amax_amd as m
+    return m
+
+
+def within(got, want, tol, what):
+    bad = ~(np.abs(got - want) <= tol * (1 + BF) + BF * np.abs(want) + 2.0 ** -133)
+    assert not bad.any(), (f"{what}: {int(bad.sum())} values off, first {np.argwhere(bad)[0]}: "
+                           f"{got[bad][0]!r} for {want[bad][0]!r} +- {tol[bad][0]!r}")
+
+
+def bf16_of(t):
+    return layer.values(host_bits(t))
+
+
+def operand(rng, rows, cols, fmt, mode, std):
+    """(codes on the host, factors on the host [rows], codes and factors on the device)."""
+    q, s = block.codes(rng, rows, cols, fmt, std) if cols else (np.zeros((rows, 0), np.uint8), np.ones(rows, np.float32))
+    if mode == 0:
+        s = np.full(rows, np.float32(0.37 * std / max(cols, 1) ** 0.25), np.float32)
+    return q, s, s[:1] if mode == 0 else s
+
+
+def padded(codes, pad):
+    """codes on the device with pad more bytes a row, those 0x7F (NaN)."""
+    rows, cols = codes.shape
+    t = torch.full((rows, cols + pad), 0x7F, dtype=torch.uint8, device=DEV)
+    t[:, :cols] = dev_u8(codes)
+    return t[:, :cols]
+
+
+FORWARD = [  # m, k, inter, fa, fb, a_mode, b_mode, h, output row padding
+    (1, 16, 1, 0, 0, 1, 1, True, 0), (1, 4096, 64, 0, 0, 1, 1, False, 0), (1, 7168, 136, 0, 1, 0, 1, True, 8),
+    (3, 272, 40, 1, 0, 1, 0, True, 3), (16, 512, 72, 0, 0, 1, 1, True, 8), (17, 1040, 33, 1, 1, 1, 1, True, 1),
+    (31, 2048, 1408, 0, 0, 0, 0, False, 8), (64, 1024, 520, 0, 0, 1, 1, True, 8), (65, 768, 96, 0, 1, 1, 1, True, 8),
+    (128, 128, 64, 0, 0, 1, 1, True, 0), (129, 1024, 200, 1, 0, 1, 1, False, 24), (300, 512, 641, 0, 0, 1, 1, True, 7),
+    (777, 256, 1408, 0, 0, 0, 0, True, 8), (256, 256, 16384, 0, 0, 1, 1, False, 8),
+    (4000, 512, 1100, 0, 0, 1, 1, True, 4), (4097, 256, 1100, 1, 0, 1, 1, True, 0), (2049, 768, 2056, 0, 1, 0, 1, False, 8),
+    (8200, 256, 1026, 0, 0, 1, 0, True, 2), (5000, 272, 900, 0, 0, 1, 1, True, 4), (40, 0, 72, 0, 0, 1, 1, True, 8),
+    (300, 0, 200, 0, 0, 0, 0, True, 8),
+]
+
+
+@pytest.mark.parametrize("m,k,inter,fa,fb,am,bm,want_h,pad", FORWARD)
+def test_forward(fp8, m, k, inter, fa, fb, am, bm, want_h, pad):
+    rng = np.random.default_rng(m * 3 + k + inter)
+    qa, sa, sad = operand(rng, m, k, fa, am, 1.0)
+    qb, sb, sbd = operand(rng, 2 * inter, k, fb, bm, 1.3 / max(k, 1) ** 0.5)
+    h, tol = block.product(qa, fa, sa, qb, fb, sb)
+    g, u, gt, ut = h[:, :inter], h[:, inter:], tol[:, :inter], tol[:, inter:]
+    act, act_tol = block.swiglu(g, u, gt, ut)
+    d, dbuf, do = guarded(m, inter, torch.bfloat16, ld=inter + pad)
+    hd = None
+    if want_h:
+        hd, hbuf, ho = guarded(m, 2 * inter, torch.bfloat16, ld=2 * inter + pad)
+    say("gated product", m, k, inter, fa, fb, am, bm, want_h, pad)
+    args = (padded(qa, 16), fa, padded(qb, 32), fb, dev_f32(sad), am, dev_f32(sbd), bm)
+    fp8.fp8_gemm_swiglu(*args, d, h=hd)
+    torch.cuda.synchronize()
+    within(bf16_of(d), act, act_tol, "act")
+    check_guard(dbuf, do, m, inter)
+    if want_h:
+        within(bf16_of(hd), h, tol, "h")
+        check_guard(hbuf, ho, m, 2 * inter)
+    again = torch.empty((m, inter), dtype=torch.bfloat16, device=DEV)
+    fp8.fp8_gemm_swiglu(*args, again)
+    torch.cuda.synchronize()
+    assert torch.equal(again, d), "act depends on whether h is stored, or on its layout"
+
+
+BACKWARD = [  # m, k, inter, fa, fb, a_mode, b_mode, act, row padding
+    (1, 16, 1, 1, 0, 1, 1, True, 0), (3, 272, 40, 1, 0, 1, 0, True, 3), (64, 512, 136, 1, 0, 1, 1, False, 8),
+    (130, 1024, 200, 1, 0, 1, 1, True, 24), (300, 512, 641, 0, 1, 0, 1, True, 7), (1001, 256, 1408, 1, 0, 1, 1, False, 8),
+    (4000, 512, 2100, 1, 0, 1, 1, True, 4), (4097, 256, 2200, 0, 0, 1, 1, True, 0), (2049, 768, 4104, 1, 1, 0, 0, False, 8),
+    (8200, 256, 1026, 1, 0, 1, 0, True, 2), (5000, 272, 900, 0, 0, 1, 1, True, 4), (300, 0, 72, 0, 0, 1, 1, True, 8),
+    (256, 256, 32768, 1, 0, 1, 1, True, 8),
+]
+
+
+@pytest.mark.parametrize("m,k,inter,fa,fb,am,bm,want_act,pad", BACKWARD)
+def test_backward(fp8, m, k, inter, fa, fb, am, bm, want_act, pad):
+    rng = np.random.default_rng(m * 5 + k + inter)
+    qa, sa, sad = operand(rng, m, k, fa, am, 1e-3)
+    qb, sb, sbd = operand(rng, inter, k, fb, bm, 1.3 / max(k, 1) ** 0.5)
+    da, tol = block.product(qa, fa, sa, qb, fb, sb)
+    hb = workloads.bf16_bits((1.5 * rng.standard_normal((m, 2 * inter))).astype(np.float32))
+    hv = layer.values(hb)
+    want = block.swiglu_backward(da, hv[:, :inter], hv[:, inter:], tol)
+    h = torch.full((m, 2 * inter + pad), float("nan"), dtype=torch.bfloat16, device=DEV)[:, :2 * inter]
+    h.copy_(dev_bf16(hb))
+    dh, buf, o = guarded(m, 2 * inter, torch.bfloat16, ld=2 * inter + pad)
+    act = None
+    if want_act:
+        act, abuf, ao = guarded(m, inter, torch.bfloat16, ld=inter + pad)
+    say("gated product's gradient", m, k, inter, fa, fb, am, bm, want_act, pad)
+    args = (padded(qa, 16), fa, padded(qb, 32), fb, dev_f32(sad), am, dev_f32(sbd), bm, h)
+    fp8.fp8_gemm_swiglu_backward(*args, dh, act=act)
+    torch.cuda.synchronize()
+    got = bf16_of(dh)
+    within(got[:, :inter], want["dg"], want["dg_tol"], "d(gate)")
+    within(got[:, inter:], want["du"], want["du_tol"], "d(up)")
+    check_guard(buf, o, m, 2 * inter)
+    if want_act:
+        within(bf16_of(act), want["a"], want["a_tol"], "act")
+        check_guard(abuf, ao, m, inter)
+    again = torch.empty((m, 2 * inter), dtype=torch.bfloat16, device=DEV)
+    fp8.fp8_gemm_swiglu_backward(*args, again)
+    torch.cuda.synchronize()
+    assert torch.equal(again, dh), "dh depends on whether act is stored, or on its layout"
+
+
+@pytest.mark.parametrize("m,k,inter", [(4, 256, 80), (40, 1024, 64), (130, 256, 200), (4200, 256, 1100)])
+def test_rows_and_columns_stay_apart(fp8, m, k, inter):
+    """A NaN in a row of a, in a gate row and in an up row of b reaches that row and
+    those columns alone, in both directions; large gates give silu of 0 and g."""
+    rng = np.random.default_rng(k)
+    qa, sa, _ = operand(rng, m, k, 0, 1, 1.0)
+    qb, sb, _ = operand(rng, 2 * inter, k, 0, 1, 1.0)
+    a, b = dev_u8(qa), dev_u8(qb)
+    row, gate, up = m // 2, inter // 3, inter - 1
+    a[row, 3], b[gate, 5], b[inter + up, k - 1] = 0x7F, 0xFF, 0x7F
+    act = torch.empty((m, inter), dtype=torch.bfloat16, device=DEV)
+    h = torch.empty((m, 2 * inter), dtype=torch.bfloat16, device=DEV)
+    say("gated product, NaN", m, k, inter)
+    fp8.fp8_gemm_swiglu(a, 0, b, 0, dev_f32(sa), 1, dev_f32(sb), 1, act, h=h)
+    torch.cuda.synchronize()
+    bad = torch.zeros((m, 2 * inter), dtype=torch.bool, device=DEV)
+    bad[row] = True
+    bad[:, gate] = bad[:, inter + up] = True
+    assert torch.equal(torch.isnan(h), bad)
+    assert torch.equal(torch.isnan(act), bad[:, :inter] | bad[:, inter:])
+    hv = torch.randn((m, 2 * inter), device=DEV).to(torch.bfloat16)
+    hv[0, 0], hv[1, 1], hv[2, inter + 2] = float("nan"), 300.0, float("nan")
+    hv[1, 2] = -300.0
+    dh = torch.empty((m, 2 * inter), dtype=torch.bfloat16, device=DEV)
+    say("gated product's gradient, NaN", m, k, inter)
+    fp8.fp8_gemm_swiglu_backward(a, 0, b[:inter], 0, dev_f32(sa), 1, dev_f32(sb[:inter]), 1, hv, dh, act=act)
+    torch.cuda.synchronize()
+    da = torch.zeros((m, inter), dtype=torch.bool, device=DEV)
+    da[row] = True
+    da[:, gate] = True
+    nan_g, nan_u = torch.isnan(hv[:, :inter]), torch.isnan(hv[:, inter:])
+    assert torch.equal(torch.isnan(act), nan_g | nan_u)
+    assert torch.equal(torch.isnan(dh[:, :inter]), da | nan_g | nan_u)
+    assert torch.equal(torch.isnan(dh[:, inter:]), da | nan_g)
+    assert act[1, 1] == (300.0 * hv[1, inter + 1].float()).to(torch.bfloat16) and act[1, 2] == 0
+    if row != 1 and gate != 2:
+        assert dh[1, 2] == 0 and dh[1, inter + 2] == 0
+
+
+def test_empty(fp8):
+    say("gated product, no rows")
+    e = torch.empty
+    z = e((0, 64), dtype=torch.uint8, device=DEV)
+    b = torch.zeros((16, 64), dtype=torch.uint8, device=DEV)
+    one = torch.ones(1, device=DEV)
+    fp8.fp8_gemm_swiglu(z, 0, b, 0, one, 0, one, 0, e((0, 8), dtype=torch.bfloat16, device=DEV))
+    fp8.fp8_gemm_swiglu_backward(z, 0, b, 0, one, 0, one, 0, e((0, 32), dtype=torch.bfloat16, device=DEV),
+                                 e((0, 32), dtype=torch.bfloat16, device=DEV))
+    torch.cuda.synchronize()
+
+
+def test_gradient_against_differences(fp8):
+    """dh against central differences of act, in fp64 from the exact product: the
+    objective sum(act * da) of one element is act * da; the difference over a step
+    of 2^-6 is off by the third derivative's part, h^2 / 6 of at most |da u| (|silu'''| < 1)."""
+    rng = np.random.default_rng(5)
+    m, k, inter = 24, 64, 48
+    qa, sa, _ = operand(rng, m, k, 1, 1, 1.0)
+    qb, sb, _ = operand(rng, inter, k, 0, 1, 0.2)
+    da, tol = block.product(qa, 1, sa, qb, 0, sb)
+    hb = workloads.bf16_bits(rng.standard_normal((m, 2 * inter)).astype(np.float32))
+    hv = layer.values(hb)
+    g, u = hv[:, :inter], hv[:, inter:]
+    f = lambda g, u: g * layer.sigmoid(g) * u  # noqa: E731
+    step = 2.0 ** -6
+    dg = da * (f(g + step, u) - f(g - step, u)) / (2 * step)
+    du = da * (f(g, u + step) - f(g, u - step)) / (2 * step)
+    dh = torch.empty((m, 2 * inter), dtype=torch.bfloat16, device=DEV)
+    say("gated product's gradient against differences")
+    fp8.fp8_gemm_swiglu_backward(dev_u8(qa), 1, dev_u8(qb), 0, dev_f32(sa), 1, dev_f32(sb), 1, dev_bf16(hb), dh)
+    torch.cuda.synchronize()
+    want = block.swiglu_backward(da, g, u, tol)
+    got = bf16_of(dh)
+    within(got[:, :inter], dg, want["dg_tol"] + step ** 2 / 6 * np.abs(da * u), "d(gate)")
+    within(got[:, inter:], du, want["du_tol"] + 1e-9 * np.abs(du), "d(up)")

@@ -1,0 +1,161 @@
+"""GPU parity of the adapters of many requests against the fp64 definition of
+oracle/block.py: every output within the bound of an fp32 evaluation plus half a
+step of bf16. Ranks, odd lengths, requests in any order, tokens without an adapter,
+views with guard bands, in place, NaN and Inf in other requests' data."""
+import numpy as np
+import pytest
+import torch
+
+import workloads
+from helpers import check_guard, dev_bf16, guarded, host_bits, say
+from oracle import block, layer
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF = block.BF16
+
+
+@pytest.fixture(scope="module")
+def fp8():
+    import fp8_scaled_gemm_amax_amd as m
+    return m
+
+
+def within(got, want, tol, what):
+    bad = ~(np.abs(got - want) <= tol * (1 + BF) + BF * np.abs(want) + 2.0 ** -133)
+    assert not bad.any(), (f"{what}: {int(bad.sum())} values off, first {np.argwhere(bad)[0]}: "
+                           f"{got[bad][0]!r} for {want[bad][0]!r} +- {tol[bad][0]!r}")
+
+
+def normal(rng, *shape, std=1.0):
+    b = workloads.bf16_bits((std * rng.standard_normal(shape)).astype(np.float32).reshape(-1, shape[-1])).reshape(shape)
+    return b, layer.values(b)
+
+
+def adapters_of(rng, how, tokens, E):
+    if how == "one":
+        return np.zeros(tokens, np.int32)
+    if how == "none":
+        return np.full(tokens, -1, np.int32)
+    if how == "each":                           # every token another, out of range ones among them
+        return rng.integers(-2, E + 2, tokens).astype(np.int32)
+    idx = np.empty(tokens, np.int32)            # requests of neighbouring tokens of odd lengths
+    t = 0
+    while t < tokens:
+        n = int(rng.integers(1, 40))
+        idx[t:t + n] = rng.integers(-1, E)
+        t += n
+    return idx
+
+
+CASES = [  # tokens, k, n, rank, adapters, how, base, row padding of base and out
+    (1, 8, 1, 8, 1, "one", True, 0), (1, 4096, 4096, 16, 4, "each", True, 8), (1, 1024, 200, 128, 2, "one", False, 8),
+    (2, 72, 17, 24, 3, "each", True, 3), (15, 512, 256, 8, 40, "each", True, 8), (16, 520, 264, 16, 2, "each", True, 8),
+    (17, 4096, 512, 32, 64, "each", True, 0), (33, 1000, 1001, 40, 5, "runs", True, 1), (64, 2048, 640, 64, 7, "each", False, 8),
+    (100, 264, 130, 104, 3, "runs", True, 6), (300, 640, 392, 16, 9, "runs", True, 8), (257, 136, 96, 128, 4, "each", True, 8),
+    (40, 256, 128, 16, 3, "none", True, 8), (1025, 520, 264, 64, 3, "runs", True, 8), (2100, 264, 520, 16, 20, "each", True, 8),
+    (1300, 1024, 300, 8, 2, "one", True, 4), (9000, 64, 40, 16, 5, "runs", True, 8), (600, 2048, 72, 48, 1, "one", False, 8),
+]
+
+
+@pytest.mark.parametrize("tokens,k,n,rank,E,how,with_base,pad", CASES)
+def test_lora_add(fp8, tokens, k, n, rank, E, how, with_base, pad):
+    rng = np.random.default_rng(tokens + k * 3 + n)
+    xb, x = normal(rng, tokens, k)
+    ab, a = normal(rng, E, rank, k, std=k ** -0.5)
+    bb, b = normal(rng, E, n, rank, std=rank ** -0.5)
+    baseb, base = normal(rng, tokens, n)
+    if not with_base:
+        base = np.zeros_like(base)
+    scaling = (0.25 + rng.random(E)).astype(np.float32)
+    idx = adapters_of(rng, how, tokens, E)
+    want, tol = block.lora(x, a, b, scaling, idx, base)
+    xd = torch.full((tokens, k + 8), float("nan"), dtype=torch.bfloat16, device=DEV)[:, :k]
+    xd.copy_(dev_bf16(xb))
+    ad = torch.full((E, rank + 1, k + 16), float("nan"), dtype=torch.bfloat16, device=DEV)[:, :rank, :k]
+    ad.copy_(dev_bf16(ab))
+    bd = torch.full((E, n + 2, rank + 8), float("nan"), dtype=torch.bfloat16, device=DEV)[:, :n, :rank]
+    bd.copy_(dev_bf16(bb))
+    based = None
+    if with_base:
+        based = torch.full((tokens, n + pad), float("nan"), dtype=torch.bfloat16, device=DEV)[:, :n]
+        based.copy_(dev_bf16(baseb))
+    out, buf, o = guarded(tokens, n, torch.bfloat16, ld=n + pad)
+    ws = fp8.lora_workspace(tokens, rank)
+    guard = torch.full((ws.numel() + 64,), 3.0, device=DEV)
+    say("adapters", tokens, k, n, rank, E, how, with_base, pad)
+    args = (xd, ad, bd, torch.from_numpy(scaling).to(DEV), torch.from_numpy(idx).to(DEV))
+    fp8.fp8_lora_add(*args, based, out, guard[:ws.numel()])
+    torch.cuda.synchronize()
+    assert (guard[ws.numel():] == 3.0).all(), "writes past the workspace"
+    got = layer.values(host_bits(out))
+    within(got, want, tol, "out")
+    none = (idx < 0) | (idx >= E)
+    assert np.array_equal(got[none], base[none]), "a token without an adapter keeps its base"
+    check_guard(buf, o, tokens, n)
+    # the same bits again, and in place
+    again = torch.empty((tokens, n), dtype=torch.bfloat16, device=DEV)
+    if with_base:
+        again.copy_(based)
+        fp8.fp8_lora_add(*args, again, again, ws)
+    else:
+        fp8.fp8_lora_add(*args, None, again, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("tokens", [5, 40, 1100])
+def test_requests_stay_apart(fp8, tokens):
+    """NaN and Inf in a token, in an adapter and in a factor reach only the tokens
+    that they belong to; an infinite weight of B gives Inf, not NaN."""
+    rng = np.random.default_rng(tokens)
+    k, n, rank, E = 136, 72, 16, 6
+    idx = rng.integers(-1, E, tokens).astype(np.int32)
+    idx[:5] = [0, 1, 2, 3, 4]
+    x = torch.randn((tokens, k), device=DEV).to(torch.bfloat16)
+    a = torch.randn((E, rank, k), device=DEV).to(torch.bfloat16)
+    b = torch.randn((E, n, rank), device=DEV).to(torch.bfloat16)
+    base = torch.randn((tokens, n), device=DEV).to(torch.bfloat16)
+    base[3] = -0.0
+    sc = torch.ones(E, device=DEV)
+    ids = torch.from_numpy(idx).to(DEV)
+    ws = fp8.lora_workspace(tokens, rank)
+    clean, out = torch.empty_like(base), torch.empty_like(base)
+    say("adapters, NaN", tokens)
+    fp8.fp8_lora_add(x, a, b, sc, ids, base, clean, ws)
+    x[0, 7] = float("nan")
+    a[1, 3, k - 1] = float("inf")
+    sc[2] = float("nan")
+    b[4, n - 1, 2] = float("inf")
+    fp8.fp8_lora_add(x, a, b, sc, ids, base, out, ws)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[0]).all()
+    hit = torch.isin(ids, torch.tensor([1, 2, 4], device=DEV, dtype=torch.int32))
+    hit[0] = True
+    assert torch.equal(out[~hit], clean[~hit])
+    assert torch.isnan(out[2]).all() and not torch.isfinite(out[1]).any()
+    four = (ids == 4).nonzero()[:, 0]
+    assert torch.isinf(out[four, n - 1]).all() and torch.equal(out[four, :n - 1], clean[four, :n - 1])
+
+
+def test_negative_zero_base(fp8):
+    """The base of a token without an adapter is copied bit for bit."""
+    base = torch.tensor([[-0.0, 1.0, float("inf"), -0.0]], device=DEV).to(torch.bfloat16).repeat(3, 5)
+    x = torch.zeros((3, 8), dtype=torch.bfloat16, device=DEV)
+    a, b = torch.zeros((1, 8, 8), dtype=torch.bfloat16, device=DEV), torch.zeros((1, 20, 8), dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(base)
+    say("adapters, -0")
+    fp8.fp8_lora_add(x, a, b, torch.ones(1, device=DEV), torch.full((3,), -1, dtype=torch.int32, device=DEV), base, out,
+                     fp8.lora_workspace(3, 8))
+    torch.cuda.synchronize()
+    assert np.array_equal(host_bits(out), host_bits(base))
+
+
+def test_empty(fp8):
+    say("adapters, no tokens")
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    fp8.fp8_lora_add(torch.empty((0, 16), **bf), torch.zeros((1, 8, 16), **bf), torch.zeros((1, 32, 8), **bf),
+                     torch.ones(1, device=DEV), torch.empty(0, dtype=torch.int32, device=DEV), torch.empty((0, 32), **bf),
+                     torch.empty((0, 32), **bf), torch.empty(0, device=DEV))
+    torch.cuda.synchronize()
