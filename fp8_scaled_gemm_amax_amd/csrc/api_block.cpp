@@ -300,10 +300,11 @@ fp8_status_t fp8_lora_add(const uint16_t* x, int64_t tokens, int64_t k, int64_t 
     if (!aligned(base, 2) || !aligned(out, 2) || !aligned(adapter_idx, 4) || !aligned(scaling, 4) ||
         !aligned(workspace, 16))
         return fail(FP8_ERR_ALIGNMENT, "%s: misaligned pointer", fn);
-    // (a grid's threads stay below 2^32: 16 x 256 outputs a workgroup of 256 threads)
-    if (tokens >= ((int64_t)1 << 27) || n >= ((int64_t)1 << 31) ||
-        (tokens + 15) / 16 * ((n + 255) / 256) >= ((int64_t)1 << 24))
+    // (grids: 1024 threads for 16 tokens, 512 columns a workgroup in the second direction)
+    if (tokens >= ((int64_t)1 << 25) || n >= ((int64_t)1 << 24))
         return fail(FP8_ERR_UNSUPPORTED, "%s: %lld x %lld outputs", fn, (long long)tokens, (long long)n);
+    if (ldx >= (1 << 24) || ld_a >= (1 << 24) || ld_b >= (1 << 24) || (base && ldbase >= (1 << 24)) || ldout >= (1 << 24))
+        return fail(FP8_ERR_UNSUPPORTED, "%s: leading dimensions must be < 2^24 (rows use 32-bit offsets)", fn);
     if (tokens > 0 && n > 0 && (!workspace || workspace_bytes < fp8_lora_workspace(tokens, rank)))
         return fail(FP8_ERR_INVALID_ARG, "%s: a workspace of %lld bytes is needed", fn,
                     (long long)fp8_lora_workspace(tokens, rank));

@@ -739,7 +739,7 @@ fp8_status_t fp8_gemm_swiglu_backward(const uint8_t* a, fp8_format_t fa, int64_t
  * and the same call gives the same bits; the order of the fp32 sums depends on
  * the number of tokens.
  * rank a multiple of 8, 8..FP8_LORA_MAX_RANK; k a multiple of 8, >= 8; adapters >=
- * 1; x, A, B 16-byte aligned with ldx, ld_a, ld_b and the adapter strides multiples
+ * 1; tokens < 2^25, n < 2^24 (else FP8_ERR_UNSUPPORTED); x, A, B 16-byte aligned with ldx, ld_a, ld_b and the adapter strides multiples
  * of 8 (strides >= 0); base, out 2-byte aligned, at full speed 16-byte aligned with
  * ldbase, ldout multiples of 8. workspace: fp8_lora_workspace(tokens, rank) bytes
  * at least, 16-byte aligned; free for other use once the call's work is done;

@@ -56,6 +56,9 @@ CASES = [  # tokens, k, n, rank, adapters, how, base, row padding of base and ou
     (100, 264, 130, 104, 3, "runs", True, 6), (300, 640, 392, 16, 9, "runs", True, 8), (257, 136, 96, 128, 4, "each", True, 8),
     (40, 256, 128, 16, 3, "none", True, 8), (1025, 520, 264, 64, 3, "runs", True, 8), (2100, 264, 520, 16, 20, "each", True, 8),
     (1300, 1024, 300, 8, 2, "one", True, 4), (9000, 64, 40, 16, 5, "runs", True, 8), (600, 2048, 72, 48, 1, "one", False, 8),
+    (64, 128, 520, 32, 70, "each", True, 8), (65, 136, 1032, 64, 70, "each", True, 8), (512, 328, 776, 16, 3, "each", True, 8),
+    (513, 200, 264, 32, 2, "runs", True, 8), (514, 1032, 2000, 112, 1, "one", True, 8), (700, 64, 520, 16, 3, "none", True, 8),
+    (200, 64, 130, 8, 4, "one", True, 2),
 ]
 
 
@@ -105,7 +108,7 @@ def test_lora_add(fp8, tokens, k, n, rank, E, how, with_base, pad):
     assert torch.equal(again, out)
 
 
-@pytest.mark.parametrize("tokens", [5, 40, 1100])
+@pytest.mark.parametrize("tokens", [5, 40, 300, 1100])
 def test_requests_stay_apart(fp8, tokens):
     """NaN and Inf in a token, in an adapter and in a factor reach only the tokens
     that they belong to; an infinite weight of B gives Inf, not NaN."""
