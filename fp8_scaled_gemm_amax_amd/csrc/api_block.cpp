@@ -19,7 +19,13 @@ fp8_status_t check_same_rows(const char* fn, const char* names, const void* p, i
     return FP8_OK;
 }
 
-// Operands and factors of the gated products; n: rows of b.
+fp8_status_t check_wide(const char* fn, int64_t ld) {
+    if (ld >= (1 << 25))
+        return fail(FP8_ERR_UNSUPPORTED, "%s: leading dimension %lld: those of act, h and dh must be < 2^25", fn, (long long)ld);
+    return FP8_OK;
+}
+
+// Operands and factors of the gated products.
 fp8_status_t check_product(const char* fn, const uint8_t* a, int fa, int64_t lda, const uint8_t* b, int fb, int64_t ldb,
                            int64_t m, int64_t inter, int64_t k, const float* sa, int a_mode, const float* sb,
                            int b_mode) {
@@ -41,8 +47,10 @@ fp8_status_t check_product(const char* fn, const uint8_t* a, int fa, int64_t lda
     if (!aligned(sa, 4) || !aligned(sb, 4)) return fail(FP8_ERR_ALIGNMENT, "%s: misaligned scale pointer", fn);
     if (!ocp_fmt(fa) || !ocp_fmt(fb))
         return fail(FP8_ERR_UNSUPPORTED, "%s: fnuz operands (%d, %d): OCP e4m3 / e5m2 only", fn, fa, fb);
+    if (lda >= (1 << 24) || ldb >= (1 << 24) || inter >= (1 << 24))
+        return fail(FP8_ERR_UNSUPPORTED, "%s: lda, ldb and inter must be < 2^24 (tiles use 32-bit offsets)", fn);
     // (a grid's threads stay below 2^32: tiles of 128 x 64 outputs, 256 threads each)
-    if (m >= ((int64_t)1 << 30) || inter >= ((int64_t)1 << 30) || (m + 127) / 128 * ((inter + 63) / 64) >= (1 << 24))
+    if (m >= ((int64_t)1 << 30) || (m + 127) / 128 * ((inter + 63) / 64) >= (1 << 24))
         return fail(FP8_ERR_UNSUPPORTED, "%s: %lld x %lld outputs", fn, (long long)m, (long long)inter);
     return FP8_OK;
 }
@@ -214,6 +222,8 @@ fp8_status_t fp8_gemm_swiglu(const uint8_t* a, fp8_format_t fa, int64_t lda, con
     FP8_TRY(check_matrix(fn, "act", act, m, inter, ldact));
     if (h) FP8_TRY(check_matrix(fn, "h", h, m, 2 * inter, ldh));
     if (!aligned(act, 2) || !aligned(h, 2)) return fail(FP8_ERR_ALIGNMENT, "%s: misaligned output", fn);
+    FP8_TRY(check_wide(fn, ldact));
+    if (h) FP8_TRY(check_wide(fn, ldh));
     FP8_TRY(check_device());
     GluFwd p{};
     p.a = a;
@@ -247,6 +257,9 @@ fp8_status_t fp8_gemm_swiglu_backward(const uint8_t* a, fp8_format_t fa, int64_t
     if (act) FP8_TRY(check_matrix(fn, "act", act, m, inter, ldact));
     if (!aligned(h, 2) || !aligned(dh, 2) || !aligned(act, 2))
         return fail(FP8_ERR_ALIGNMENT, "%s: misaligned h, dh or act", fn);
+    FP8_TRY(check_wide(fn, ldh));
+    FP8_TRY(check_wide(fn, lddh));
+    if (act) FP8_TRY(check_wide(fn, ldact));
     FP8_TRY(check_device());
     GluBwd p{};
     p.a = a;

@@ -35,23 +35,16 @@ struct TileArgs {
 
 __device__ __forceinline__ int swz(int row, int chunk) { return row * kChunksPerRow + (chunk ^ (row & 7)); }
 
-// The rows of an operand's tile: the first `valid` ones from base on.
-struct TileRows {
-    const uint8_t* base;
-    int64_t ld, valid;
-    __device__ __forceinline__ bool has(int row) const { return row < valid; }
-    __device__ __forceinline__ const uint8_t* at(int row) const { return base + (int64_t)row * ld; }
-};
-
-template <int LOADS, class Rows>
-__device__ __forceinline__ void load_tile(uint4 (&r)[LOADS], const Rows& rows, int64_t k0, int64_t k) {
+template <int LOADS>
+__device__ __forceinline__ void load_tile(uint4 (&r)[LOADS], const uint8_t* base, int64_t ld, int64_t valid_rows,
+                                          int64_t k0, int64_t k) {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
         const int c = threadIdx.x + i * kThreads;
         const int row = c >> 3, kc = c & 7;
         const int64_t kk = k0 + kc * 16;
-        if (rows.has(row) && kk < k)
-            r[i] = *reinterpret_cast<const uint4*>(rows.at(row) + kk);
+        if (row < valid_rows && kk < k)
+            r[i] = *reinterpret_cast<const uint4*>(base + (int64_t)row * ld + kk);
         else
             r[i] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -82,9 +75,8 @@ __device__ __forceinline__ v8i load_frag(const uint4* lds, int row, int kk) {
 }
 
 // One BM x BN output tile: acc[mi][ni] holds the wavefront's 32x32 block (mi, ni).
-template <int FA, int FB, class RowsA, class RowsB>
-__device__ __forceinline__ void mma_rows(const RowsA& a, const RowsB& b, int64_t k, v16f (&acc)[2][2], uint4* As,
-                                         uint4* Bs) {
+template <int FA, int FB>
+__device__ __forceinline__ void mma_tile(const TileArgs& t, v16f (&acc)[2][2], uint4* As, uint4* Bs) {
     const int wave = threadIdx.x >> 6;
     const int lane = threadIdx.x & 63;
     const int wm = wave >> 1, wn = wave & 1;
@@ -95,11 +87,11 @@ __device__ __forceinline__ void mma_rows(const RowsA& a, const RowsB& b, int64_t
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.0f;
 
-    const int64_t nk = (k + BK - 1) / BK;
+    const int64_t nk = (t.k + BK - 1) / BK;
     uint4 ra[kLoadsA], rb[kLoadsB];
     if (nk > 0) {
-        load_tile<kLoadsA>(ra, a, 0, k);
-        load_tile<kLoadsB>(rb, b, 0, k);
+        load_tile<kLoadsA>(ra, t.a, t.lda, t.m_rows, 0, t.k);
+        load_tile<kLoadsB>(rb, t.b, t.ldb, t.n_rows, 0, t.k);
     }
     for (int64_t kt = 0; kt < nk; ++kt) {
         __syncthreads();
@@ -107,8 +99,8 @@ __device__ __forceinline__ void mma_rows(const RowsA& a, const RowsB& b, int64_t
         store_tile<kLoadsB>(rb, Bs);
         __syncthreads();
         if (kt + 1 < nk) {
-            load_tile<kLoadsA>(ra, a, (kt + 1) * BK, k);
-            load_tile<kLoadsB>(rb, b, (kt + 1) * BK, k);
+            load_tile<kLoadsA>(ra, t.a, t.lda, t.m_rows, (kt + 1) * BK, t.k);
+            load_tile<kLoadsB>(rb, t.b, t.ldb, t.n_rows, (kt + 1) * BK, t.k);
         }
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
@@ -125,11 +117,6 @@ __device__ __forceinline__ void mma_rows(const RowsA& a, const RowsB& b, int64_t
                         fa[mi], fb[ni], acc[mi][ni], MfmaFmt<FA>::v, MfmaFmt<FB>::v, 0, 0, 0, 0);
         }
     }
-}
-
-template <int FA, int FB>
-__device__ __forceinline__ void mma_tile(const TileArgs& t, v16f (&acc)[2][2], uint4* As, uint4* Bs) {
-    mma_rows<FA, FB>(TileRows{t.a, t.lda, t.m_rows}, TileRows{t.b, t.ldb, t.n_rows}, t.k, acc, As, Bs);
 }
 
 // ------------------------------------------------------------ large tiles --

@@ -32,80 +32,407 @@ __device__ __forceinline__ SwigluGrad swiglu_grad(float da, float g, float u) {
     return {da * u * (s * fmaf(g, 1.0f - s, 1.0f)), da * silu, silu * u};
 }
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ float bf16(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+// Eight columns of a row, at any alignment: a base that is uniform over the wavefront
+// and the lane's offset in bytes. Nontemporal both ways: h, read once, would push the
+// operand panels out of L2 (gradient at 8192 x 4096 x 14336: 519 us with ordinary
+// loads, 484 with these).
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+__device__ __forceinline__ void store8(uint16_t* base, uint32_t bytes, u32x4 v) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(reinterpret_cast<char*>(base) + bytes));
+}
+__device__ __forceinline__ u32x4 load8(const uint16_t* base, uint32_t bytes) {
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(reinterpret_cast<const char*>(base) + bytes));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2bf));
+}
+
+// --------------------------------------------------------------- few rows --
+// Up to kFewRows rows of a (decoding): bound by the weights' bytes, each read once. A
+// workgroup has 16 columns of act: its 16 gate rows and 16 up rows of b against tiles
+// of 16 rows of a (16x16x128 products), its wavefronts taking K in turn in blocks of
+// 256 bytes, their sums added in LDS. Weights are loaded in the order of the rows (16
+// lanes a row) and turned into the matrix cores' order (lane l: 32 bytes of row l % 16)
+// through LDS of the wavefront's own; the next block is on its way while one is
+// multiplied.
+constexpr int kFewRows = 32, kFewWaves = 4, kFewBlock = 256;
+
+template <int FA, int FB, int NT>
+__global__ __launch_bounds__(kFewWaves * 64) void k_glu_few(GluFwd p) {
+    // a wavefront's part: two tiles of 16 rows x 256 bytes, then its sums [2 NT][256]
+    constexpr int kPart = 8192 > NT * 2048 ? 8192 : NT * 2048;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kFewWaves][kPart];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, m = lane & 15;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int cols = p.inter - n0 < 16 ? (int)(p.inter - n0) : 16;
+    uint8_t* own = lds[wave];
+    // loads: chunk m of rows q, q + 4, .. of each tile
+    uint32_t wo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 4 * i + q;
+        wo[i] = (uint32_t)(row < cols ? row : cols - 1) * (uint32_t)p.ldb + (uint32_t)m * 16;
+    }
+    const uint8_t* wp[2] = {p.b + n0 * p.ldb, p.b + (p.inter + n0) * p.ldb};
+    // chunk c of row r at c ^ r: 16 rows of one chunk meet 16 different groups of banks
+    auto place = [](int row, int chunk) { return row * 256 + ((chunk ^ row) << 4); };
+    uint32_t xo[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int row = n * 16 + m;
+        xo[n] = (uint32_t)(row < p.m ? row : (int)p.m - 1) * (uint32_t)p.lda + (uint32_t)q * 32;
+    }
+    v4f acc[2][NT];
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[w][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t blocks = (p.k + kFewBlock - 1) / kFewBlock;
+    // chunks past k (in the last block) load the row's last one, for zeros
+    auto load = [&](int64_t b, u32x4 (&w)[2][4]) {
+        const int64_t left = p.k - b * kFewBlock;
+        const int last = left < kFewBlock ? (int)left / 16 - 1 : 15;
+        const uint32_t in = m <= last ? ~0u : 0u, back = m <= last ? 0u : (uint32_t)(m - last) * 16;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[t][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wp[t] + b * kFewBlock + (wo[i] - back))) & in;
+    };
+    auto work = [&](int64_t b, const u32x4 (&w)[2][4], u32x4 (*next)[2][4], int64_t nb) {
+        const int64_t left = p.k - b * kFewBlock;
+        u32x4 x[2][NT][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int at = s * 128 + q * 32 + h * 16;
+                    const uint32_t in = at < left ? ~0u : 0u;
+                    x[s][n][h] = *reinterpret_cast<const u32x4*>(p.a + b * kFewBlock + (xo[n] + (at < left ? s * 128 + h * 16 : 0) -
+                                                                                        (at < left ? 0 : q * 32))) & in;
+                }
+        __builtin_amdgcn_sched_barrier(0);              // (loads return in order: the rows of a first)
+        if (next) load(nb, *next);
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4*>(own + t * 4096 + place(4 * i + q, m)) = w[t][i];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const v8i f = big_join(*reinterpret_cast<const u32x4*>(own + t * 4096 + place(m, 8 * s + 2 * q)),
+                                       *reinterpret_cast<const u32x4*>(own + t * 4096 + place(m, 8 * s + 2 * q + 1)));
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    acc[t][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f, big_join(x[s][n][0], x[s][n][1]), acc[t][n],
+                                                                                 MfmaFmt<FB>::v, MfmaFmt<FA>::v, 0, 0, 0, 0);
+            }
+    };
+    {
+        u32x4 a[2][4], b[2][4];                         // in turn, so that no load waits to be copied
+        int64_t i = wave;
+        if (i < blocks) load(i, a);
+        for (; i < blocks; i += 2 * kFewWaves) {
+            const int64_t j = i + kFewWaves, k = j + kFewWaves;
+            work(i, a, j < blocks ? &b : nullptr, j);
+            if (j >= blocks) break;
+            work(j, b, k < blocks ? &a : nullptr, k);
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    float* sums = reinterpret_cast<float*>(own);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)                     // column (row of a) m, rows (of b) 4 q ..
+            *reinterpret_cast<v4f*>(sums + (n * 2 + t) * 256 + m * 16 + q * 4) = acc[t][n];
+    __syncthreads();
+    const int row16 = threadIdx.x >> 4, col = threadIdx.x & 15;
+    if (col >= cols) return;
+    const float sg = p.sb[p.sb_vec ? n0 + col : 0], su = p.sb[p.sb_vec ? p.inter + n0 + col : 0];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int64_t row = n * 16 + row16;
+        if (row >= p.m) break;
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w) {
+            const float* s = reinterpret_cast<const float*>(lds[w]) + n * 512 + threadIdx.x;
+            g += s[0];
+            u += s[256];
+        }
+        const float sa = p.sa[p.sa_vec ? row : 0];
+        g = g * sa * sg;
+        u = u * sa * su;
+        p.act[row * p.ldact + n0 + col] = (uint16_t)f32_to_bf16(swiglu(g, u));
+        if (p.h) {
+            p.h[row * p.ldh + n0 + col] = (uint16_t)f32_to_bf16(g);
+            p.h[row * p.ldh + p.inter + n0 + col] = (uint16_t)f32_to_bf16(u);
+        }
+    }
+}
 
 // ------------------------------------------------------- 128 x 128 tiles --
-// Any sizes (k in steps of 16). Rows of B of a tile: 32 gate rows, the 32 up rows
-// of the same columns, 32 gate rows, ..: block 0 of a wavefront is gate, block 1 up.
-struct GluRows {
-    const uint8_t* gate;        // of the tile's first column
-    int64_t up, ld, valid;      // up: bytes from a gate row to its up row
-    __device__ __forceinline__ int col(int row) const { return (row >> 6) * 32 + (row & 31); }
-    __device__ __forceinline__ bool has(int row) const { return col(row) < valid; }
-    __device__ __forceinline__ const uint8_t* at(int row) const {
-        return gate + ((row >> 5) & 1) * up + (int64_t)col(row) * ld;
-    }
-};
+// Any sizes (k in steps of 16), and the kernel where large tiles are too few for the
+// chip. Four wavefronts of 64 x 64 outputs (2 x 2 blocks of 32x32x64), K in steps of
+// 128 through four stages in LDS, direct global-to-LDS loads three steps ahead (one
+// step ahead in registers, 777 x 2048 x 1408 took 26 us). Rows past the operand's
+// last one are loaded as that one and not stored; the step that k ends in comes through
+// registers, zeros behind k.
+namespace mid {
+constexpr int kStages = 4, kOp = 128 * 128, kStage = 2 * kOp;
+constexpr int kScaleOff = kStages * kStage;             // 128 row factors, 128 column factors
+constexpr int kSmem = kScaleOff + 2 * 128 * 4;          // 129 KB
+}  // namespace mid
 
+// a, b: first rows (uniform over the wavefront: b may differ between wavefronts);
+// ao, bo: offsets of this lane's four rows, of which it loads chunk `slot` of each step.
 template <int FA, int FB>
-__global__ __launch_bounds__(kThreads) void k_glu(GluFwd p) {
-    __shared__ uint4 As[BM * kChunksPerRow];
-    __shared__ uint4 Bs[BN * kChunksPerRow];
-    const int64_t tiles_n = (p.inter + 63) / 64;
-    const int64_t row0 = (int64_t)(blockIdx.x / tiles_n) * BM, col0 = (int64_t)(blockIdx.x % tiles_n) * 64;
+__device__ __forceinline__ void mid_sums(uint8_t* smem, const uint8_t* a, const uint32_t (&ao)[4], const uint8_t* b,
+                                         const uint32_t (&bo)[4], int64_t k, v16f (&acc)[2][2]) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int64_t full = k / 128, nk = (k + 127) / 128;
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem)) + wave * 4096;
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.0f;
+    auto issue = [&](int64_t s) {
+        const uint32_t base = lds0 + (uint32_t)(s & (mid::kStages - 1)) * mid::kStage;
+        if (s < full) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lds_dma16_s(base + i * 1024, a + s * 128, ao[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lds_dma16_s(base + mid::kOp + i * 1024, b + s * 128, bo[i]);
+        } else if (s < nk) {
+            uint8_t* to = smem + (s & (mid::kStages - 1)) * mid::kStage + wave * 4096 + lane * 16;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // (the lane's chunk of the step: its offset modulo the row's 128 bytes)
+                const int chunk = k128_slot(8 * i + (lane >> 3), lane & 7);
+                u32x4 va = {0u, 0u, 0u, 0u}, vb = va;
+                if (s * 128 + chunk * 16 < k) {
+                    va = *reinterpret_cast<const u32x4*>(a + s * 128 + ao[i]);
+                    vb = *reinterpret_cast<const u32x4*>(b + s * 128 + bo[i]);
+                }
+                *reinterpret_cast<u32x4*>(to + i * 1024) = va;
+                *reinterpret_cast<u32x4*>(to + mid::kOp + i * 1024) = vb;
+            }
+        }
+    };
+    for (int s = 0; s < mid::kStages - 1; ++s) issue(s);
+    for (int64_t s = 0; s < nk; ++s) {
+        // this thread's loads of step s have landed (8 each of two later steps may not have)
+        if (s + 2 < full)
+            wait_vmcnt<16>();
+        else
+            wait_vmcnt<0>();
+        __syncthreads();                                // everyone's have, and step s - 1 is read
+        issue(s + mid::kStages - 1);
+        const uint8_t* ta = smem + (s & (mid::kStages - 1)) * mid::kStage;
+        const uint8_t* tb = ta + mid::kOp;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            v8i fa[2], fb[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int ra = wm * 64 + i * 32 + (lane & 31), rb = wn * 64 + i * 32 + (lane & 31);
+                fa[i] = big_join(k128_half<false>(ta, ra, h, 0), k128_half<false>(ta, ra, h, 1));
+                fb[i] = big_join(k128_half<false>(tb, rb, h, 0), k128_half<false>(tb, rb, h, 1));
+            }
+#pragma unroll
+            for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+                for (int ni = 0; ni < 2; ++ni) acc[mi][ni] = mfma64<FA, FB, false, 0>(fa[mi], fb[ni], acc[mi][ni], 0u, 0u);
+        }
+    }
+    __syncthreads();                                    // (the stages are free, the factors in place)
+}
+// Offsets of this lane's four rows row0 + 8 i + l / 8, the last valid one instead of
+// those past it, with the chunk that its slot holds.
+__device__ __forceinline__ void mid_offsets(uint32_t (&off)[4], int row0, int64_t valid, int64_t ld) {
+    const int lane = threadIdx.x & 63;
+    const int last = valid < (1 << 20) ? (int)valid - 1 : 1 << 20;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = row0 + 8 * i + (lane >> 3);
+        off[i] = (uint32_t)(row < last ? row : last) * (uint32_t)ld + (uint32_t)(k128_slot(8 * i + (lane >> 3), lane & 7) * 16);
+    }
+}
+
+// Eight of the columns col .. of a row of bf16 outputs, `left` of them there.
+__device__ __forceinline__ void store_chunk8(uint16_t* base, uint32_t bytes, int left, const float* f) {
+    if (left >= 8) {
+        store8(base, bytes, u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])});
+        return;
+    }
+    uint16_t* dst = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(base) + bytes);
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < left) dst[e] = (uint16_t)f32_to_bf16(f[e]);
+}
+
+// Tile: 128 rows x 64 columns of act; rows of b: 32 gate rows, the 32 up rows of the
+// same columns, 32 gate rows, ..: block 0 of a wavefront is gate, block 1 up.
+template <int FA, int FB>
+__global__ __launch_bounds__(256) void k_glu_mid(GluFwd p) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[mid::kSmem];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t tiles_m = (p.m + 127) / 128;
+    const int64_t row0 = (int64_t)(blockIdx.x % tiles_m) * 128, col0 = (int64_t)(blockIdx.x / tiles_m) * 64;
+    const int64_t half = (int64_t)(wave & 1) * p.inter;         // wavefront w loads gate (w even) or up rows
+    uint32_t ao[4], bo[4];
+    mid_offsets(ao, wave * 32, p.m - row0, p.lda);
+    mid_offsets(bo, (wave >> 1) * 32, p.inter - col0, p.ldb);
+    float* s_rows = reinterpret_cast<float*>(smem + mid::kScaleOff);
+    float* s_cols = s_rows + 128;
+    if (threadIdx.x < 128) {
+        const int64_t r = row0 + threadIdx.x, c = col0 + (threadIdx.x & 63);
+        s_rows[threadIdx.x] = p.sa[p.sa_vec ? (r < p.m ? r : p.m - 1) : 0];
+        // 64 gate factors, 64 up factors
+        s_cols[threadIdx.x] = p.sb[p.sb_vec ? (threadIdx.x >> 6) * p.inter + (c < p.inter ? c : p.inter - 1) : 0];
+    }
     v16f acc[2][2];
-    mma_rows<FA, FB>(TileRows{p.a + row0 * p.lda, p.lda, p.m - row0},
-                     GluRows{p.b + col0 * p.ldb, p.inter * p.ldb, p.ldb, p.inter - col0}, p.k, acc, As, Bs);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t col = col0 + (wave & 1) * 32 + (lane & 31);
-    if (col >= p.inter) return;
-    const float sg = p.sb[p.sb_vec ? col : 0], su = p.sb[p.sb_vec ? p.inter + col : 0];
+    mid_sums<FA, FB>(smem, p.a + row0 * p.lda, ao, p.b + (half + col0) * p.ldb, bo, p.k, acc);
+    // the wavefront's 64 rows x 32 columns of g and of u in LDS, then a lane takes rows
+    // of 8 columns
+    constexpr int kPitch = 68;                          // fp32 values: 32 of g, 32 of u
+    float* own = reinterpret_cast<float*>(smem) + wave * 64 * kPitch;
+    const int wm = wave >> 1, wn = wave & 1;
+    const float sg = s_cols[wn * 32 + (lane & 31)], su = s_cols[64 + wn * 32 + (lane & 31)];
 #pragma unroll
     for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int64_t row = row0 + (wave >> 1) * 64 + mi * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-            if (row >= p.m) continue;
-            const float sa = p.sa[p.sa_vec ? row : 0];
-            const float g = acc[mi][0][r] * sa * sg, u = acc[mi][1][r] * sa * su;
-            p.act[row * p.ldact + col] = (uint16_t)f32_to_bf16(swiglu(g, u));
-            if (p.h) {
-                p.h[row * p.ldh + col] = (uint16_t)f32_to_bf16(g);
-                p.h[row * p.ldh + p.inter + col] = (uint16_t)f32_to_bf16(u);
+            const int row = mi * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+            const float sa = s_rows[wm * 64 + row];
+            own[row * kPitch + (lane & 31)] = acc[mi][0][r] * sa * sg;
+            own[row * kPitch + 32 + (lane & 31)] = acc[mi][1][r] * sa * su;
+        }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int64_t wcol = col0 + wn * 32 + 8 * (lane & 3);
+    const int left = p.inter - wcol < 8 ? (int)(p.inter - wcol) : 8;
+    if (left <= 0) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int row = j * 16 + (lane >> 2);
+        const int64_t at = row0 + wm * 64 + row;
+        if (at >= p.m) continue;
+        float g[8], u[8], act[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const v4f vg = *reinterpret_cast<const v4f*>(own + row * kPitch + 8 * (lane & 3) + 4 * h);
+            const v4f vu = *reinterpret_cast<const v4f*>(own + row * kPitch + 32 + 8 * (lane & 3) + 4 * h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                g[4 * h + e] = vg[e];
+                u[4 * h + e] = vu[e];
+                act[4 * h + e] = swiglu(vg[e], vu[e]);
             }
         }
+        store_chunk8(p.act + at * p.ldact + wcol, 0, left, act);
+        if (p.h) {
+            store_chunk8(p.h + at * p.ldh + wcol, 0, left, g);
+            store_chunk8(p.h + at * p.ldh + p.inter + wcol, 0, left, u);
+        }
+    }
 }
 
+// Tile: 128 x 128 of da, a wavefront 64 x 64.
 template <int FA, int FB>
-__global__ __launch_bounds__(kThreads) void k_glu_grad(GluBwd p) {
-    __shared__ uint4 As[BM * kChunksPerRow];
-    __shared__ uint4 Bs[BN * kChunksPerRow];
-    const int64_t tiles_n = (p.inter + BN - 1) / BN;
-    const int64_t row0 = (int64_t)(blockIdx.x / tiles_n) * BM, col0 = (int64_t)(blockIdx.x % tiles_n) * BN;
+__global__ __launch_bounds__(256) void k_glu_grad_mid(GluBwd p) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[mid::kSmem];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t tiles_m = (p.m + 127) / 128;
+    const int64_t row0 = (int64_t)(blockIdx.x % tiles_m) * 128, col0 = (int64_t)(blockIdx.x / tiles_m) * 128;
+    uint32_t ao[4], bo[4];
+    mid_offsets(ao, wave * 32, p.m - row0, p.lda);
+    mid_offsets(bo, wave * 32, p.inter - col0, p.ldb);
+    float* s_rows = reinterpret_cast<float*>(smem + mid::kScaleOff);
+    float* s_cols = s_rows + 128;
+    if (threadIdx.x < 128) {
+        const int64_t r = row0 + threadIdx.x, c = col0 + threadIdx.x;
+        s_rows[threadIdx.x] = p.sa[p.sa_vec ? (r < p.m ? r : p.m - 1) : 0];
+        s_cols[threadIdx.x] = p.sb[p.sb_vec ? (c < p.inter ? c : p.inter - 1) : 0];
+    }
     v16f acc[2][2];
-    mma_rows<FA, FB>(TileRows{p.a + row0 * p.lda, p.lda, p.m - row0},
-                     TileRows{p.b + col0 * p.ldb, p.ldb, p.inter - col0}, p.k, acc, As, Bs);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    mid_sums<FA, FB>(smem, p.a + row0 * p.lda, ao, p.b + col0 * p.ldb, bo, p.k, acc);
+    constexpr int kPitch = 68;
+    float* own = reinterpret_cast<float*>(smem) + wave * 64 * kPitch;
+    const int wm = wave >> 1, wn = wave & 1;
+    const int64_t wcol = col0 + wn * 64 + 8 * (lane & 7);
+    const int left = p.inter - wcol < 8 ? (int)(p.inter - wcol) : 8;
+    const int64_t wrow = row0 + wm * 64;
+    // h, two rows ahead
+    u32x4 hg[3], hu[3];
+    auto load_h = [&](int j) {
+        const int64_t at = wrow + j * 8 + (lane >> 3);
+        hg[j % 3] = hu[j % 3] = u32x4{0u, 0u, 0u, 0u};
+        if (at >= p.m || left <= 0) return;
+        const uint16_t* src = p.h + at * p.ldh + wcol;
+        if (left >= 8) {
+            hg[j % 3] = load8(src, 0);
+            hu[j % 3] = load8(src + p.inter, 0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (e < left) {
+                    hg[j % 3][e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+                    hu[j % 3][e >> 1] |= (uint32_t)src[p.inter + e] << (16 * (e & 1));
+                }
+        }
+    };
+    load_h(0);
+    load_h(1);
 #pragma unroll
     for (int ni = 0; ni < 2; ++ni) {
-        const int64_t col = col0 + (wave & 1) * 64 + ni * 32 + (lane & 31);
-        if (col >= p.inter) continue;
-        const float sb = p.sb[p.sb_vec ? col : 0];
+        const float sb = s_cols[wn * 64 + ni * 32 + (lane & 31)];
 #pragma unroll
         for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const int64_t row = row0 + (wave >> 1) * 64 + mi * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-                if (row >= p.m) continue;
-                const uint16_t* hr = p.h + row * p.ldh + col;
-                const SwigluGrad d =
-                    swiglu_grad(acc[mi][ni][r] * p.sa[p.sa_vec ? row : 0] * sb, bf16(hr), bf16(hr + p.inter));
-                p.dh[row * p.lddh + col] = (uint16_t)f32_to_bf16(d.dg);
-                p.dh[row * p.lddh + p.inter + col] = (uint16_t)f32_to_bf16(d.du);
-                if (p.act) p.act[row * p.ldact + col] = (uint16_t)f32_to_bf16(d.act);
+                const int row = mi * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+                own[row * kPitch + ni * 32 + (lane & 31)] = acc[mi][ni][r] * s_rows[wm * 64 + row] * sb;
             }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (j + 2 < 8) load_h(j + 2);
+        const int row = j * 8 + (lane >> 3);
+        float dg[8], du[8], act[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const v4f da = *reinterpret_cast<const v4f*>(own + row * kPitch + 8 * (lane & 7) + 4 * h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t wg = hg[j % 3][2 * h + (e >> 1)], wu = hu[j % 3][2 * h + (e >> 1)];
+                const SwigluGrad d = swiglu_grad(da[e], e & 1 ? bf16_hi(wg) : bf16_lo(wg), e & 1 ? bf16_hi(wu) : bf16_lo(wu));
+                dg[4 * h + e] = d.dg;
+                du[4 * h + e] = d.du;
+                act[4 * h + e] = d.act;
+            }
+        }
+        const int64_t at = wrow + row;
+        if (at < p.m && left > 0) {
+            store_chunk8(p.dh + at * p.lddh + wcol, 0, left, dg);
+            store_chunk8(p.dh + at * p.lddh + p.inter + wcol, 0, left, du);
+            if (p.act) store_chunk8(p.act + at * p.ldact + wcol, 0, left, act);
+        }
     }
 }
 
@@ -181,18 +508,6 @@ __device__ __forceinline__ u32x4 unit_row(const u32x4 (&un)[4], int r) {
     for (int k = 0; k < 4; ++k) row[k] = __builtin_amdgcn_perm(un[k][2 + (r >> 1)], un[k][r >> 1], sel);
     return row;
 }
-// Eight columns of a row, at any alignment: a base that is uniform over the wavefront
-// and the lane's offset in bytes. Nontemporal both ways: h, read once, would push the
-// operand panels out of L2 (gradient at 8192 x 4096 x 14336: 519 us with ordinary
-// loads, 484 with these).
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-__device__ __forceinline__ void store8(uint16_t* base, uint32_t bytes, u32x4 v) {
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(reinterpret_cast<char*>(base) + bytes));
-}
-__device__ __forceinline__ u32x4 load8(const uint16_t* base, uint32_t bytes) {
-    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(reinterpret_cast<const char*>(base) + bytes));
-}
-
 // A tile's outputs: 256 rows x 128 columns of act. A wavefront has 128 rows x 64
 // columns: blocks 0 and 1 of its 128 columns of B are gate, 2 and 3 up. Staged
 // through 4 KB of LDS a wavefront (its own: no barrier): with SAVE 16 rows of [gate |
@@ -374,10 +689,10 @@ __device__ __forceinline__ void glu_grad_epilogue(uint8_t* smem, v16f (&acc)[4][
 #pragma unroll
         for (int ni = 0; ni < 4; ++ni) {
             const int col = 32 * ni + (lane & 31);
-            f32x4 v;
+            v4f v;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = acc[mi][ni][4 * q + i] * __uint_as_float(s4[i]) * sb[ni];
-            *reinterpret_cast<f32x4*>(ep + (lane >> 5) * 2048 + ((col ^ ((col >> 4) & 7)) << 4)) = v;
+            *reinterpret_cast<v4f*>(ep + (lane >> 5) * 2048 + ((col ^ ((col >> 4) & 7)) << 4)) = v;
         }
         wait_vmcnt<63, 0>();                             // this wavefront's staging writes are done
         __builtin_amdgcn_wave_barrier();
@@ -464,37 +779,37 @@ static int64_t persistent_grid(int64_t tiles) {
     const int64_t cus = current_device_props().cus, most = cus >= 8 ? cus / 8 * 8 : cus;
     return tiles < most ? tiles : most;
 }
-// (32-bit lane offsets: 256 rows of an operand, 32 of an output and its other half)
-static bool large_operands(int64_t k, int64_t inter, int64_t lda, int64_t ldb, int64_t ldh, int64_t ldd, int64_t ldact) {
-    return k > 0 && k % 256 == 0 && lda < (1 << 24) && ldb < (1 << 24) && inter < (1 << 25) && ldh < (1 << 25) &&
-           ldd < (1 << 25) && ldact < (1 << 25);
-}
-
 template <int FA, int FB>
 hipError_t glu_typed(const GluFwd& p, hipStream_t st) {
     const int64_t large = (p.m + 255) / 256 * ((p.inter + 127) / 128);
-    if (large_operands(p.k, p.inter, p.lda, p.ldb, p.ldh, 0, p.ldact) && p.m >= 256 && p.inter >= 128 && large >= 128) {
+    if (p.k > 0 && p.k % 256 == 0 && p.m >= 256 && p.inter >= 128 && large >= 128) {
         const dim3 grid((unsigned)persistent_grid(large));
         if (p.h) hipLaunchKernelGGL((k_glu_persist<FA, FB, true>), grid, dim3(256), 0, st, p);
         else hipLaunchKernelGGL((k_glu_persist<FA, FB, false>), grid, dim3(256), 0, st, p);
         return hipGetLastError();
     }
-    const int64_t tiles = (p.m + BM - 1) / BM * ((p.inter + 63) / 64);
-    hipLaunchKernelGGL((k_glu<FA, FB>), dim3((unsigned)tiles), dim3(kThreads), 0, st, p);
+    if (p.m <= kFewRows) {
+        const dim3 grid((unsigned)((p.inter + 15) / 16));
+        if (p.m <= 16) hipLaunchKernelGGL((k_glu_few<FA, FB, 1>), grid, dim3(kFewWaves * 64), 0, st, p);
+        else hipLaunchKernelGGL((k_glu_few<FA, FB, 2>), grid, dim3(kFewWaves * 64), 0, st, p);
+        return hipGetLastError();
+    }
+    const int64_t tiles = (p.m + 127) / 128 * ((p.inter + 63) / 64);
+    hipLaunchKernelGGL((k_glu_mid<FA, FB>), dim3((unsigned)tiles), dim3(256), 0, st, p);
     return hipGetLastError();
 }
 
 template <int FA, int FB>
 hipError_t glu_grad_typed(const GluBwd& p, hipStream_t st) {
     const int64_t large = (p.m + 255) / 256 * ((p.inter + 255) / 256);
-    if (large_operands(p.k, p.inter, p.lda, p.ldb, p.ldh, p.lddh, p.ldact) && p.m >= 256 && p.inter >= 256 && large >= 128) {
+    if (p.k > 0 && p.k % 256 == 0 && p.m >= 256 && p.inter >= 256 && large >= 128) {
         const dim3 grid((unsigned)persistent_grid(large));
         if (p.act) hipLaunchKernelGGL((k_glu_grad_persist<FA, FB, true>), grid, dim3(256), 0, st, p);
         else hipLaunchKernelGGL((k_glu_grad_persist<FA, FB, false>), grid, dim3(256), 0, st, p);
         return hipGetLastError();
     }
-    const int64_t tiles = (p.m + BM - 1) / BM * ((p.inter + BN - 1) / BN);
-    hipLaunchKernelGGL((k_glu_grad<FA, FB>), dim3((unsigned)tiles), dim3(kThreads), 0, st, p);
+    const int64_t tiles = (p.m + 127) / 128 * ((p.inter + 127) / 128);
+    hipLaunchKernelGGL((k_glu_grad_mid<FA, FB>), dim3((unsigned)tiles), dim3(256), 0, st, p);
     return hipGetLastError();
 }
 

@@ -29,13 +29,6 @@ constexpr int kStepK = 64;                      // columns of x of one step of a
 __device__ __forceinline__ v4f mfma(u32x4 a, u32x4 b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
-// 16 bytes where `in`, zeros elsewhere (nothing is read there).
-__device__ __forceinline__ u32x4 load_if(bool in, const uint16_t* p) {
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (in) v = *reinterpret_cast<const u32x4*>(p);
-    return v;
-}
-
 // Eight columns of base or out, at any alignment: a pointer that is uniform over the
 // wavefront and the lane's offset in bytes. Nontemporal: each is met once, and the
 // adapters' weights keep their place in the caches.
@@ -71,9 +64,6 @@ __device__ __forceinline__ void put_value(const Lora& p, int64_t t, int j, float
     *lo = (uint16_t)(finite ? f32_to_bf16(v - __uint_as_float(h << 16)) : 0u);
 }
 
-__device__ __forceinline__ bool finite4(v4f a) {
-    return __builtin_isfinite(a[0]) && __builtin_isfinite(a[1]) && __builtin_isfinite(a[2]) && __builtin_isfinite(a[3]);
-}
 // Orders this wavefront's LDS accesses on either side for the compiler (the
 // hardware keeps their order).
 __device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
@@ -231,9 +221,10 @@ struct UpLds {
 // base + v B^T (or the base's own bits, `add` false) for 16 NT tokens of one adapter
 // and the blocks nb, nb + step, .. of 256 columns, a wavefront 64 of them. Memory is
 // met 8 lanes a row of 128 bytes (B: as its rows lie): lane l has the tokens t0 + t[i],
-// rows 8 i + l / 8 of the 16 NT, where live, and 8 columns of each. (The product's own
-// order, 16 rows of 16 bytes a quarter of a load, ran at a third of this rate.)
-// The next block's weights and base are on their way while a block is multiplied.
+// rows 8 i + l / 8 of the 16 NT, where live, and 8 columns of each. (In the
+// product's own order, 16 rows of 16 bytes a quarter of a load, 5003 tokens of rank 64
+// took 131 us, in this one 97.) With two tiles of tokens the next block's weights and
+// base are on their way while a block is multiplied.
 template <int NT, int RS>
 __device__ __forceinline__ void up_blocks(const Lora& p, int e, int64_t t0, const int (&t)[2 * NT],
                                           const bool (&live)[2 * NT], const bool (&add)[2 * NT], UpLds<NT, RS>& lds,
@@ -334,7 +325,10 @@ __device__ __forceinline__ void up_blocks(const Lora& p, int e, int64_t t0, cons
         }
     };
     Block a;
-    if constexpr (RS == 4) {                    // (two blocks' weights: spills)
+    // A workgroup of few tokens has few blocks, and more of them fit without a second
+    // block in registers (128 tokens, rank 16, 4096 x 14336: 22 -> 19 us); of rank 128 two
+    // blocks do not fit.
+    if constexpr (NT == 1) {
         for (; nb < blocks_n; nb += step) {
             load(nb, a);
             work(nb, a);
@@ -370,11 +364,16 @@ struct OneAdapter {
         mine = mine >= 0 && mine < p.adapters ? mine : -1;
         const uint64_t some = __ballot(mine >= 0);
         without = ~some & (n < 64 ? (1ull << n) - 1ull : ~0ull);
-        bool first = mine >= 0;
-        for (int j = 0; j + 1 < n; ++j) first = first && !(lane > j && mine == __builtin_amdgcn_readlane(mine, j));
+        // the tokens that name this lane's adapter, bit by bit of its number
+        uint64_t same = some;
+        for (int bit = 0; (p.adapters - 1) >> bit; ++bit) {
+            const uint64_t set = __ballot((mine >> bit) & 1);
+            same &= (mine >> bit) & 1 ? set : ~set;
+        }
+        const uint64_t below = (1ull << lane) - 1ull;
+        const bool first = mine >= 0 && !(same & below);
         const uint64_t leaders = __ballot(first);
         if (slot >= __popcll(leaders)) return false;
-        const uint64_t below = (1ull << lane) - 1ull;
         const uint64_t lead = __ballot(first && __popcll(leaders & below) == slot);
         e = __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)lead) - 1);
         const uint64_t tokens = __ballot(mine == e);
@@ -414,7 +413,7 @@ __global__ __launch_bounds__(256) void k_lora_down_few(Lora p) {
 // Workgroup: one adapter's tokens of a group, blocks y, y + gridDim.y, .. of columns.
 // Slot 0 also copies the base of the tokens without an adapter.
 template <int RS>
-__global__ __launch_bounds__(256, RS == 1 ? 3 : 2) void k_lora_up_few(Lora p, int64_t blocks_n) {
+__global__ __launch_bounds__(256, RS == 1 ? 4 : RS == 2 ? 3 : 2) void k_lora_up_few(Lora p, int64_t blocks_n) {
     __shared__ UpLds<1, RS> lds;
     const int lane = threadIdx.x & 63;
     const int64_t t0 = (int64_t)blockIdx.x * kGroup;
@@ -560,7 +559,9 @@ int64_t at_most(int64_t a, int64_t b) { return a < b ? a : b; }
 hipError_t few_tokens(Lora p, hipStream_t st) {
     const int64_t groups = (p.tokens + kGroup - 1) / kGroup, steps = (p.k + kStepK - 1) / kStepK;
     const int64_t slots = at_most(at_most(p.tokens, kGroup), p.adapters), active = groups * slots;
-    // parts of k, and of the columns, that leave a few workgroups a CU
+    // Short workgroups, many of them: one spends its time on a chain of dependent loads.
+    // (128 tokens of as many requests, rank 16, 4096 x 14336: 4 blocks of columns a
+    // workgroup 20 us, 14 of them 34; one 26, for the values of v added up again.)
     p.parts = (int)at_most(at_most((2048 + active - 1) / active, 16), (steps + 3) / 4);        // (16 * kFewTokens = kLoraPartRows)
 #define CALL(RT)                                                                                              \
     hipLaunchKernelGGL((k_lora_down_few<RT>), dim3((unsigned)groups, (unsigned)p.parts, (unsigned)slots), dim3(256), 0, \
@@ -570,7 +571,7 @@ hipError_t few_tokens(Lora p, hipStream_t st) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t blocks_n = (p.n + 255) / 256;
-    const dim3 grid((unsigned)groups, (unsigned)at_most((1024 + active - 1) / active, blocks_n), (unsigned)slots);
+    const dim3 grid((unsigned)groups, (unsigned)at_most((4096 + active - 1) / active, blocks_n), (unsigned)slots);
 #define CALL(RS) hipLaunchKernelGGL((k_lora_up_few<RS>), grid, dim3(256), 0, st, p, blocks_n)
     FP8_LORA_BY_STEPS(CALL);
 #undef CALL

@@ -387,8 +387,8 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
         // tt opaque in every step: offsets are then formed where they are used,
         // next to scalar bases, and not kept as 64-bit pairs over the loop
         asm volatile("" : "+v"(tt));
-        load_row<SRC, TPR, MAXC, LOOSE, ADD>(p, next < r1 ? next : r1 - 1, tt, nch, &nxt);
-        // from a checkpoint, ds of the row at hand (a row ahead it spilled)
+        // from a checkpoint, ds of the row at hand (a row ahead it spilled), asked for
+        // before the next row, since loads return in order
         uint4 ds[ADD ? MAXC : 1];
         if constexpr (ADD) {
 #pragma unroll
@@ -400,6 +400,7 @@ __global__ __launch_bounds__(WG, 4) void k_norm_grad(NormBwd p) {
                     ds[c] = cur.ds[c];
             }
         }
+        load_row<SRC, TPR, MAXC, LOOSE, ADD>(p, next < r1 ? next : r1 - 1, tt, nch, &nxt);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int c = 0; c < MAXC; ++c) {

@@ -697,9 +697,10 @@ fp8_status_t fp8_mx_add_norm_backward(const uint16_t* dsum, int64_t lddsum, cons
  * the rounded h); an exp(-g) of 2^128 or more counts as infinite. A row's results
  * do not depend on the other rows' values; the same call gives the same bits.
  * k % 16 == 0 (k = 0: zeros); a, b 16-byte aligned with lda, ldb multiples of 16;
- * act, h 2-byte aligned, with full-speed stores where they are 16-byte aligned
- * and ldact, ldh, inter multiples of 8. OCP e4m3 / e5m2 (fnuz:
- * FP8_ERR_UNSUPPORTED). Outputs do not overlap each other or the inputs. */
+ * act, h 2-byte aligned, at full speed where they are 16-byte aligned and ldact,
+ * ldh, inter multiples of 8. lda, ldb, inter < 2^24, ldact, ldh < 2^25 (else
+ * FP8_ERR_UNSUPPORTED). OCP e4m3 / e5m2 (fnuz: FP8_ERR_UNSUPPORTED). Outputs do not
+ * overlap each other or the inputs. */
 fp8_status_t fp8_gemm_swiglu(const uint8_t* a, fp8_format_t fa, int64_t lda, const uint8_t* b, fp8_format_t fb,
                              int64_t ldb, int64_t m, int64_t inter, int64_t k, const float* a_scale_inv,
                              fp8_scale_mode_t a_mode, const float* b_scale_inv, fp8_scale_mode_t b_mode, uint16_t* act,
@@ -713,8 +714,8 @@ fp8_status_t fp8_gemm_swiglu(const uint8_t* a, fp8_format_t fa, int64_t lda, con
  * down weights transposed, as fp8_quantize_col gives them); h: bf16 [m x 2 inter]
  * (ldh) = [gate | up]; dh: bf16 [m x 2 inter] (lddh) = [d(gate) | d(up)]; act
  * (bf16 [m x inter] (ldact), or NULL): silu(gate) * up from the same read, what
- * the down projection's weight gradient takes. Requirements as fp8_gemm_swiglu;
- * h 2-byte aligned. An infinite gate follows the formula's arithmetic. */
+ * the down projection's weight gradient takes. Requirements as fp8_gemm_swiglu,
+ * dh's as h's. An infinite gate follows the formula's arithmetic. */
 fp8_status_t fp8_gemm_swiglu_backward(const uint8_t* a, fp8_format_t fa, int64_t lda, const uint8_t* b,
                                       fp8_format_t fb, int64_t ldb, int64_t m, int64_t inter, int64_t k,
                                       const float* a_scale_inv, fp8_scale_mode_t a_mode, const float* b_scale_inv,
@@ -739,7 +740,7 @@ fp8_status_t fp8_gemm_swiglu_backward(const uint8_t* a, fp8_format_t fa, int64_t
  * and the same call gives the same bits; the order of the fp32 sums depends on
  * the number of tokens.
  * rank a multiple of 8, 8..FP8_LORA_MAX_RANK; k a multiple of 8, >= 8; adapters >=
- * 1; tokens < 2^25, n < 2^24 (else FP8_ERR_UNSUPPORTED); x, A, B 16-byte aligned with ldx, ld_a, ld_b and the adapter strides multiples
+ * 1; tokens < 2^25, n and the leading dimensions < 2^24 (else FP8_ERR_UNSUPPORTED); x, A, B 16-byte aligned with ldx, ld_a, ld_b and the adapter strides multiples
  * of 8 (strides >= 0); base, out 2-byte aligned, at full speed 16-byte aligned with
  * ldbase, ldout multiples of 8. workspace: fp8_lora_workspace(tokens, rank) bytes
  * at least, 16-byte aligned; free for other use once the call's work is done;

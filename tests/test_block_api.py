@@ -73,7 +73,8 @@ def test_gemm_swiglu(fp8):
         ({8: 72, 2: 96, 5: 96}, IA), ({8: -16}, IA), ({9: None}, IA), ({11: None}, IA), ({10: 2}, IA), ({12: -1}, IA),
         ({13: None}, IA), ({14: 31}, IA), ({16: 63}, IA), ({0: off(8)}, AL), ({3: off(8)}, AL), ({2: 72}, AL), ({5: 72}, AL),
         ({9: off(2)}, AL), ({11: off(1)}, AL), ({13: off(1)}, AL), ({15: off(1)}, AL), ({1: 2}, UN), ({4: 3}, UN),
-        ({6: 1 << 30}, UN), ({7: 1 << 30, 14: 1 << 30, 16: 1 << 31}, UN), ({6: 1 << 24, 7: 1 << 20, 14: 1 << 20, 16: 1 << 21}, UN)])
+        ({6: 1 << 30}, UN), ({7: 1 << 24, 14: 1 << 24, 16: 1 << 25}, UN), ({6: 1 << 24, 7: 1 << 20, 14: 1 << 20, 16: 1 << 21}, UN),
+        ({2: 1 << 24}, UN), ({5: 1 << 24}, UN), ({14: 1 << 25}, UN), ({16: 1 << 25}, UN)])
 
 
 def test_gemm_swiglu_backward(fp8):
@@ -83,7 +84,8 @@ def test_gemm_swiglu_backward(fp8):
     refuse(fp8, "fp8_gemm_swiglu_backward", good, [
         ({0: None}, IA), ({3: None}, IA), ({1: 4}, IA), ({2: 48}, IA), ({6: -1}, IA), ({8: 8}, IA), ({9: None}, IA), ({12: 2}, IA),
         ({13: None}, IA), ({15: None}, IA), ({14: 63}, IA), ({16: 63}, IA), ({18: 31}, IA), ({0: off(8)}, AL), ({5: 72}, AL),
-        ({13: off(1)}, AL), ({15: off(1)}, AL), ({17: off(1)}, AL), ({4: 2}, UN), ({6: 1 << 30}, UN)])
+        ({13: off(1)}, AL), ({15: off(1)}, AL), ({17: off(1)}, AL), ({4: 2}, UN), ({6: 1 << 30}, UN), ({2: 1 << 24}, UN),
+        ({5: 1 << 24}, UN), ({14: 1 << 25}, UN), ({16: 1 << 25}, UN), ({18: 1 << 25}, UN)])
 
 
 def test_lora_add(fp8):
@@ -100,7 +102,9 @@ def test_lora_add(fp8):
         ({13: 12}, IA), ({13: 136}, IA), ({14: -1}, IA), ({16: 31}, IA), ({16: 40}, IA), ({17: None}, IA), ({18: 31}, IA),
         ({19: None}, IA), ({20: ws - 1}, IA), ({0: off(8)}, AL), ({3: 68}, AL), ({5: off(2)}, AL), ({6: 68}, AL), ({7: 1028}, AL),
         ({8: off(8)}, AL), ({9: 20}, AL), ({10: 516}, AL), ({15: off(1)}, AL), ({17: off(1)}, AL), ({4: off(2)}, AL),
-        ({11: off(1)}, AL), ({19: off(8)}, AL), ({1: 1 << 25}, UN), ({14: 1 << 24, 16: 1 << 24, 18: 1 << 24}, UN)])
+        ({11: off(1)}, AL), ({19: off(8)}, AL), ({1: 1 << 25}, UN), ({14: 1 << 24, 16: 1 << 24, 18: 1 << 24}, UN),
+        ({3: 1 << 24}, UN), ({6: 1 << 24}, UN), ({9: 1 << 24}, UN), ({16: 1 << 24, 18: 1 << 24}, UN),
+        ({15: off(1 << 16), 16: 1 << 24}, UN), ({15: None, 18: 1 << 24}, UN)])
 
 
 def bf(*shape):

@@ -57,7 +57,9 @@ FORWARD = [  # m, k, inter, fa, fb, a_mode, b_mode, h, output row padding
     (777, 256, 1408, 0, 0, 0, 0, True, 8), (256, 256, 16384, 0, 0, 1, 1, False, 8),
     (4000, 512, 1100, 0, 0, 1, 1, True, 4), (4097, 256, 1100, 1, 0, 1, 1, True, 0), (2049, 768, 2056, 0, 1, 0, 1, False, 8),
     (8200, 256, 1026, 0, 0, 1, 0, True, 2), (5000, 272, 900, 0, 0, 1, 1, True, 4), (40, 0, 72, 0, 0, 1, 1, True, 8),
-    (300, 0, 200, 0, 0, 0, 0, True, 8),
+    (300, 0, 200, 0, 0, 0, 0, True, 8), (48, 1296, 24, 0, 0, 1, 1, True, 8), (33, 256, 7, 1, 0, 1, 1, True, 2),
+    (5, 2304, 50, 0, 0, 1, 0, True, 8), (70, 128, 5, 0, 0, 1, 1, True, 1), (200, 384, 64, 0, 1, 1, 1, False, 8),
+    (129, 400, 72, 0, 0, 1, 1, True, 8), (500, 1008, 136, 1, 0, 0, 1, True, 8), (255, 4096, 16392, 0, 0, 1, 1, False, 8),
 ]
 
 
@@ -93,7 +95,8 @@ BACKWARD = [  # m, k, inter, fa, fb, a_mode, b_mode, act, row padding
     (130, 1024, 200, 1, 0, 1, 1, True, 24), (300, 512, 641, 0, 1, 0, 1, True, 7), (1001, 256, 1408, 1, 0, 1, 1, False, 8),
     (4000, 512, 2100, 1, 0, 1, 1, True, 4), (4097, 256, 2200, 0, 0, 1, 1, True, 0), (2049, 768, 4104, 1, 1, 0, 0, False, 8),
     (8200, 256, 1026, 1, 0, 1, 0, True, 2), (5000, 272, 900, 0, 0, 1, 1, True, 4), (300, 0, 72, 0, 0, 1, 1, True, 8),
-    (256, 256, 32768, 1, 0, 1, 1, True, 8),
+    (256, 256, 32768, 1, 0, 1, 1, True, 8), (129, 400, 72, 1, 0, 1, 1, True, 8), (70, 128, 5, 0, 0, 1, 1, True, 1),
+    (200, 1520, 129, 1, 0, 1, 1, True, 3),
 ]
 
 
@@ -129,7 +132,7 @@ def test_backward(fp8, m, k, inter, fa, fb, am, bm, want_act, pad):
     assert torch.equal(again, dh), "dh depends on whether act is stored, or on its layout"
 
 
-@pytest.mark.parametrize("m,k,inter", [(4, 256, 80), (40, 1024, 64), (130, 256, 200), (4200, 256, 1100)])
+@pytest.mark.parametrize("m,k,inter", [(4, 256, 80), (40, 1024, 64), (20, 272, 33), (130, 256, 200), (130, 400, 72), (4200, 256, 1100)])
 def test_rows_and_columns_stay_apart(fp8, m, k, inter):
     """A NaN in a row of a, in a gate row and in an up row of b reaches that row and
     those columns alone, in both directions; large gates give silu of 0 and g."""
