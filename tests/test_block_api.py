@@ -206,3 +206,24 @@ def test_no_warnings(source):
                           "-packed-fp32-ops", "--cuda-device-only", "-O1", "-c", "-o", os.devnull,
                           os.path.join(CSRC, source)], capture_output=True, text=True)
     assert out.returncode == 0 and "warning" not in out.stderr, out.stderr[-3000:]
+
+
+def test_m0_only_feeds_direct_loads():
+    """In the gated products' kernels M0 is only the LDS base of direct loads, with the
+    wait states that an assembly statement has to bring along."""
+    from test_isa_guards import kernels
+    out = subprocess.run([HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off", "-Xclang",
+                          "-target-feature", "-Xclang", "-packed-fp32-ops", "--cuda-device-only", "-S", "-o", "-",
+                          os.path.join(CSRC, "gemm_swiglu.hip")], capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr[-2000:]
+    found, loads = kernels(out.stdout), 0
+    for name, body in found.items():
+        lines = [l.strip() for l in body.splitlines() if l.strip() and not l.strip().startswith(";")]
+        for i, l in enumerate(lines):
+            if re.search(r"\bm0\b", l):
+                assert re.match(r"s_mov_b32 m0, (s\d+|vcc_lo|vcc_hi)$", l), (name, l)
+                assert lines[i + 1] in ("s_nop 0", "s_nop 4"), (name, l)
+                m = re.match(r"global_load_lds_dword(x4)? v\S+, (off|s\[\d+:\d+\]|vcc)$", lines[i + 2])
+                assert m and (m.group(2) == "off" or lines[i + 1] == "s_nop 4"), (name, lines[i + 2])
+                loads += 1
+    assert loads > 0
