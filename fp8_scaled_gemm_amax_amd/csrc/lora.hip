@@ -7,8 +7,8 @@
 // holds never enters a token's result.
 //
 // Up to kFewTokens (decoding: most tokens have an adapter of their own) a workgroup
-// takes one adapter's tokens out of 64, wherever they stand, so that the adapter's
-// weights are read once for them; the sums of v are split over parts of k, for there
+// takes up to 16 tokens of one adapter out of 64, wherever they stand, so that the
+// adapter's weights are read once for them; the sums of v are split over parts of k, for there
 // are few of them. More tokens (prompts: neighbours share an adapter) are taken 16 or
 // 32 neighbours at a time, through the adapters that they name.
 //
@@ -352,10 +352,11 @@ __device__ __forceinline__ void up_blocks(const Lora& p, int e, int64_t t0, cons
 // -------------------------------------------------------------- few tokens --
 constexpr int kFewTokens = 512, kGroup = 64;
 
-// The slot-th adapter that a group of 64 tokens names (in the order of the first
-// tokens), and its tokens: lane r holds the r-th one's place in the group.
-struct OneAdapter {
-    int e, count, token;
+// Up to 16 tokens of one adapter out of a group of 64: the slot-th such unit (by its
+// first token), an adapter of more tokens has several. Lane r holds the place in the
+// group of the adapter's r-th token; the unit's are c0 .. c0 + count - 1.
+struct Unit {
+    int e, c0, count, token;
     uint64_t without;                           // tokens without an adapter
     __device__ __forceinline__ bool find(const Lora& p, int64_t t0, int slot) {
         const int lane = threadIdx.x & 63;
@@ -366,24 +367,26 @@ struct OneAdapter {
         without = ~some & (n < 64 ? (1ull << n) - 1ull : ~0ull);
         // the tokens that name this lane's adapter, bit by bit of its number
         uint64_t same = some;
-        for (int bit = 0; (p.adapters - 1) >> bit; ++bit) {
+        for (int bit = 0; bit < 31 && (p.adapters - 1) >> bit; ++bit) {
             const uint64_t set = __ballot((mine >> bit) & 1);
             same &= (mine >> bit) & 1 ? set : ~set;
         }
         const uint64_t below = (1ull << lane) - 1ull;
-        const bool first = mine >= 0 && !(same & below);
-        const uint64_t leaders = __ballot(first);
-        if (slot >= __popcll(leaders)) return false;
-        const uint64_t lead = __ballot(first && __popcll(leaders & below) == slot);
-        e = __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)lead) - 1);
+        const int rank = __popcll(same & below);
+        const uint64_t heads = __ballot(mine >= 0 && rank % kTile == 0);
+        if (slot >= __popcll(heads)) return false;
+        const uint64_t one = __ballot(((heads >> lane) & 1u) && __popcll(heads & below) == slot);
+        const int head = __ffsll((unsigned long long)one) - 1;
+        e = __builtin_amdgcn_readlane(mine, head);
+        c0 = __builtin_amdgcn_readlane(rank, head);
         const uint64_t tokens = __ballot(mine == e);
-        count = __popcll(tokens);
-        const int to = mine == e ? __popcll(tokens & below) : count + __popcll(~tokens & below);
+        const int all = __popcll(tokens), to = mine == e ? __popcll(tokens & below) : all + __popcll(~tokens & below);
         token = __builtin_amdgcn_ds_permute(4 * to, lane);
+        count = all - c0 < kTile ? all - c0 : kTile;
         return true;
     }
-    // the c-th token (the first one past the last: loads of it are not used)
-    __device__ __forceinline__ int at(int c) const { return __shfl(token, c < count ? c : 0, 64); }
+    // the c-th token of the unit (the first one past the last: loads of it are not used)
+    __device__ __forceinline__ int at(int c) const { return __shfl(token, c0 + (c < count ? c : 0), 64); }
 };
 
 template <int RT>
@@ -391,36 +394,33 @@ __global__ __launch_bounds__(256) void k_lora_down_few(Lora p) {
     __shared__ DownLds<1, RT, 4> lds;
     const int lane = threadIdx.x & 63;
     const int64_t t0 = (int64_t)blockIdx.x * kGroup;
-    OneAdapter one;
-    if (!one.find(p, t0, blockIdx.z)) return;
+    Unit unit;
+    if (!unit.find(p, t0, blockIdx.z)) return;
     const int64_t steps = (p.k + kStepK - 1) / kStepK;
     const int64_t s0 = steps * blockIdx.y / p.parts, s1 = steps * (blockIdx.y + 1) / p.parts;
     uint32_t ao[RT][2], xo[1][2];
     a_offsets<RT>(p, ao);
-    for (int c0 = 0; c0 < one.count; c0 += kTile) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            xo[0][i] = (uint32_t)one.at(c0 + i * 8 + (lane >> 3)) * (uint32_t)p.ldx * 2 + (lane & 7) * 16;
-        v4f acc[1][RT];
-        down_sums<1, RT, 4>(p, lds, p.x + t0 * p.ldx, xo, p.a + one.e * p.gsa, ao, s0, s1, acc);
-        const int c = c0 + (threadIdx.x >> 4), token = one.at(c);        // (256 threads: 16 columns a pass)
-        add_waves<1, RT, 4>(p, lds, acc, [&](int, int, int row, float v) {
-            if (c < one.count) p.ws[((int64_t)blockIdx.y * p.tokens + t0 + token) * p.rank + row] = v;
-        });
-    }
+    for (int i = 0; i < 2; ++i) xo[0][i] = (uint32_t)unit.at(i * 8 + (lane >> 3)) * (uint32_t)p.ldx * 2 + (lane & 7) * 16;
+    v4f acc[1][RT];
+    down_sums<1, RT, 4>(p, lds, p.x + t0 * p.ldx, xo, p.a + unit.e * p.gsa, ao, s0, s1, acc);
+    const int c = threadIdx.x >> 4, token = unit.at(c);         // (256 threads: 16 columns a pass)
+    add_waves<1, RT, 4>(p, lds, acc, [&](int, int, int row, float v) {
+        if (c < unit.count) p.ws[((int64_t)blockIdx.y * p.tokens + t0 + token) * p.rank + row] = v;
+    });
 }
 
-// Workgroup: one adapter's tokens of a group, blocks y, y + gridDim.y, .. of columns.
+// Workgroup: a unit, blocks y, y + gridDim.y, .. of columns.
 // Slot 0 also copies the base of the tokens without an adapter.
 template <int RS>
 __global__ __launch_bounds__(256, RS == 1 ? 4 : RS == 2 ? 3 : 2) void k_lora_up_few(Lora p, int64_t blocks_n) {
     __shared__ UpLds<1, RS> lds;
     const int lane = threadIdx.x & 63;
     const int64_t t0 = (int64_t)blockIdx.x * kGroup;
-    OneAdapter one;
-    const bool any = one.find(p, t0, blockIdx.z);
+    Unit unit;
+    const bool any = unit.find(p, t0, blockIdx.z);
     if (blockIdx.z == 0 && p.base != p.out) {
-        for (uint64_t left = one.without; left; left &= left - 1) {
+        for (uint64_t left = unit.without; left; left &= left - 1) {
             const int64_t t = t0 + __ffsll((unsigned long long)left) - 1;
             for (int64_t nb = blockIdx.y; nb < blocks_n; nb += gridDim.y) {
                 const int64_t n = nb * 256 + threadIdx.x;
@@ -429,25 +429,22 @@ __global__ __launch_bounds__(256, RS == 1 ? 4 : RS == 2 ? 3 : 2) void k_lora_up_
         }
     }
     if (!any) return;
-    for (int c0 = 0; c0 < one.count; c0 += kTile) {
-        __syncthreads();                                    // (vs is free)
-        lds.fill(p, [&](int tok, int* e) {
-            const int token = one.at(c0 + tok);
-            *e = c0 + tok < one.count ? one.e : -1;
-            return t0 + token;
-        });
-        __syncthreads();
-        int t[2];
-        bool live[2], add[2];
+    lds.fill(p, [&](int tok, int* e) {
+        const int token = unit.at(tok);
+        *e = tok < unit.count ? unit.e : -1;
+        return t0 + token;
+    });
+    __syncthreads();
+    int t[2];
+    bool live[2], add[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int c = c0 + i * 8 + (lane >> 3);
-            t[i] = one.at(c);
-            live[i] = c < one.count;
-            add[i] = true;
-        }
-        up_blocks<1, RS>(p, one.e, t0, t, live, add, lds, blockIdx.y, gridDim.y, blocks_n);
+    for (int i = 0; i < 2; ++i) {
+        const int c = i * 8 + (lane >> 3);
+        t[i] = unit.at(c);
+        live[i] = c < unit.count;
+        add[i] = true;
     }
+    up_blocks<1, RS>(p, unit.e, t0, t, live, add, lds, blockIdx.y, gridDim.y, blocks_n);
 }
 
 // ------------------------------------------------------------- many tokens --
@@ -558,7 +555,8 @@ int64_t at_most(int64_t a, int64_t b) { return a < b ? a : b; }
 
 hipError_t few_tokens(Lora p, hipStream_t st) {
     const int64_t groups = (p.tokens + kGroup - 1) / kGroup, steps = (p.k + kStepK - 1) / kStepK;
-    const int64_t slots = at_most(at_most(p.tokens, kGroup), p.adapters), active = groups * slots;
+    // units of a group: one a token at most, and one an adapter and one for 16 tokens
+    const int64_t most = at_most(p.tokens, kGroup), slots = at_most(most, p.adapters + most / kTile), active = groups * slots;
     // Short workgroups, many of them: one spends its time on a chain of dependent loads.
     // (128 tokens of as many requests, rank 16, 4096 x 14336: 4 blocks of columns a
     // workgroup 20 us, 14 of them 34; one 26, for the values of v added up again.)
