@@ -7,11 +7,6 @@
 
 namespace fp8amax {
 
-// Whether rows of bf16 values take 16-byte accesses (NULL: yes).
-inline bool chunk_aligned(const void* p, int64_t ld) {
-    return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0);
-}
-
 // The gated product: h = a b^T with b's gate rows 0 .. inter-1 and up rows inter ..
 // 2 inter-1, act = silu(h gate) * h up; h NULL: not stored.
 struct GluFwd {
@@ -56,7 +51,7 @@ hipError_t launch_gemm_swiglu_backward(const GluBwd& p, int fa, int fb, hipStrea
 // Adapters: out = base + scaling_e (x A_e^T) B_e^T, e = adapter[token], in two
 // launches; ws holds the sums of x A^T over parts of k.
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraMaxParts = 64;               // parts of k
+constexpr int kLoraMaxParts = 16;               // parts of k
 constexpr int64_t kLoraPartRows = 8192;         // parts * tokens, unless one part each is more
 
 struct Lora {
