@@ -184,27 +184,34 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_glu_few(GluFwd p) {
 // Any sizes (k in steps of 16), and the kernel where large tiles are too few for the
 // chip. Four wavefronts of 64 x 64 outputs (2 x 2 blocks of 32x32x64), K in steps of
 // 128 through four stages in LDS, direct global-to-LDS loads three steps ahead (one
-// step ahead in registers, 777 x 2048 x 1408 took 26 us). Rows past the operand's
-// last one are loaded as that one and not stored; the step that k ends in comes through
-// registers, zeros behind k.
-namespace mid {
-constexpr int kStages = 4, kOp = 128 * 128, kStage = 2 * kOp;
-constexpr int kScaleOff = kStages * kStage;             // 128 row factors, 128 column factors
-constexpr int kSmem = kScaleOff + 2 * 128 * 4;          // 129 KB
-}  // namespace mid
+// step ahead in registers, 777 x 2048 x 1408 took 26 us), one half of a step read from
+// LDS while the other multiplies (15.8 -> 15.0 us). An XCD takes neighbouring tiles,
+// which share operand panels in its L2 (gradient of 1000 x 4112 x 14336 136 -> 130 us).
+// Rows past the operand's last one are loaded as that one and not stored; the step that
+// k ends in comes through registers, zeros behind k.
+//
+// MB: blocks of 32 rows a wavefront, 2 or, for tiles of 64 rows, 1 (mid_rows64).
+template <int MB>
+struct Mid {
+    static constexpr int kStages = 4, kA = MB * 64 * 128, kStage = kA + 128 * 128;
+    static constexpr int kScaleOff = kStages * kStage;              // MB * 64 row factors, 128 column factors
+    static constexpr int kSmem = kScaleOff + (MB * 64 + 128) * 4;   // 129 KB, 97 KB
+};
 
 // a, b: first rows (uniform over the wavefront: b may differ between wavefronts);
-// ao, bo: offsets of this lane's four rows, of which it loads chunk `slot` of each step.
-template <int FA, int FB>
-__device__ __forceinline__ void mid_sums(uint8_t* smem, const uint8_t* a, const uint32_t (&ao)[4], const uint8_t* b,
-                                         const uint32_t (&bo)[4], int64_t k, v16f (&acc)[2][2]) {
+// ao, bo: offsets of this lane's rows, of which it loads chunk `slot` of each step.
+template <int FA, int FB, int MB>
+__device__ __forceinline__ void mid_sums(uint8_t* smem, const uint8_t* a, const uint32_t (&ao)[2 * MB], const uint8_t* b,
+                                         const uint32_t (&bo)[4], int64_t k, v16f (&acc)[MB][2]) {
+    using mid = Mid<MB>;
     const int lane = threadIdx.x & 63;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
+    constexpr int kLoads = 2 * MB + 4;                  // of a thread and step
     const int64_t full = k / 128, nk = (k + 127) / 128;
-    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem)) + wave * 4096;
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
 #pragma unroll
-    for (int mi = 0; mi < 2; ++mi)
+    for (int mi = 0; mi < MB; ++mi)
 #pragma unroll
         for (int ni = 0; ni < 2; ++ni)
 #pragma unroll
@@ -213,60 +220,84 @@ __device__ __forceinline__ void mid_sums(uint8_t* smem, const uint8_t* a, const 
         const uint32_t base = lds0 + (uint32_t)(s & (mid::kStages - 1)) * mid::kStage;
         if (s < full) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) lds_dma16_s(base + i * 1024, a + s * 128, ao[i]);
+            for (int i = 0; i < 2 * MB; ++i) lds_dma16_s(base + wave * (MB * 2048) + i * 1024, a + s * 128, ao[i]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) lds_dma16_s(base + mid::kOp + i * 1024, b + s * 128, bo[i]);
+            for (int i = 0; i < 4; ++i) lds_dma16_s(base + mid::kA + wave * 4096 + i * 1024, b + s * 128, bo[i]);
         } else if (s < nk) {
-            uint8_t* to = smem + (s & (mid::kStages - 1)) * mid::kStage + wave * 4096 + lane * 16;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // (the lane's chunk of the step: its offset modulo the row's 128 bytes)
+            // (the lane's chunk of the step: its offset modulo the row's 128 bytes)
+            auto put = [&](uint8_t* to, const uint8_t* from, uint32_t off, int i) {
                 const int chunk = k128_slot(8 * i + (lane >> 3), lane & 7);
-                u32x4 va = {0u, 0u, 0u, 0u}, vb = va;
-                if (s * 128 + chunk * 16 < k) {
-                    va = *reinterpret_cast<const u32x4*>(a + s * 128 + ao[i]);
-                    vb = *reinterpret_cast<const u32x4*>(b + s * 128 + bo[i]);
-                }
-                *reinterpret_cast<u32x4*>(to + i * 1024) = va;
-                *reinterpret_cast<u32x4*>(to + mid::kOp + i * 1024) = vb;
-            }
+                u32x4 v = {0u, 0u, 0u, 0u};
+                if (s * 128 + chunk * 16 < k) v = *reinterpret_cast<const u32x4*>(from + s * 128 + off);
+                *reinterpret_cast<u32x4*>(to + lane * 16 + i * 1024) = v;
+            };
+            uint8_t* to = smem + (s & (mid::kStages - 1)) * mid::kStage;
+#pragma unroll
+            for (int i = 0; i < 2 * MB; ++i) put(to + wave * (MB * 2048), a, ao[i], i);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put(to + mid::kA + wave * 4096, b, bo[i], i);
         }
     };
-    for (int s = 0; s < mid::kStages - 1; ++s) issue(s);
-    for (int64_t s = 0; s < nk; ++s) {
-        // this thread's loads of step s have landed (8 each of two later steps may not have)
+    struct Half {
+        v8i a[MB], b[2];
+    };
+    auto read = [&](int64_t s, int h, Half& f) {
+        const uint8_t* ta = smem + (s & (mid::kStages - 1)) * mid::kStage;
+        const uint8_t* tb = ta + mid::kA;
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+            const int r = (wm * MB + i) * 32 + (lane & 31);
+            f.a[i] = big_join(k128_half<false>(ta, r, h, 0), k128_half<false>(ta, r, h, 1));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = (wn * 2 + i) * 32 + (lane & 31);
+            f.b[i] = big_join(k128_half<false>(tb, r, h, 0), k128_half<false>(tb, r, h, 1));
+        }
+    };
+    auto multiply = [&](const Half& f) {
+#pragma unroll
+        for (int mi = 0; mi < MB; ++mi)
+#pragma unroll
+            for (int ni = 0; ni < 2; ++ni) acc[mi][ni] = mfma64<FA, FB, false, 0>(f.a[mi], f.b[ni], acc[mi][ni], 0u, 0u);
+    };
+    // this thread's loads of step s have landed (those of two later steps may not have),
+    // then everyone's, and everyone has read step s - 1
+    auto arrive = [&](int64_t s) {
         if (s + 2 < full)
-            wait_vmcnt<16>();
+            wait_vmcnt<2 * kLoads>();
         else
             wait_vmcnt<0>();
-        __syncthreads();                                // everyone's have, and step s - 1 is read
-        issue(s + mid::kStages - 1);
-        const uint8_t* ta = smem + (s & (mid::kStages - 1)) * mid::kStage;
-        const uint8_t* tb = ta + mid::kOp;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            v8i fa[2], fb[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int ra = wm * 64 + i * 32 + (lane & 31), rb = wn * 64 + i * 32 + (lane & 31);
-                fa[i] = big_join(k128_half<false>(ta, ra, h, 0), k128_half<false>(ta, ra, h, 1));
-                fb[i] = big_join(k128_half<false>(tb, rb, h, 0), k128_half<false>(tb, rb, h, 1));
-            }
-#pragma unroll
-            for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-                for (int ni = 0; ni < 2; ++ni) acc[mi][ni] = mfma64<FA, FB, false, 0>(fa[mi], fb[ni], acc[mi][ni], 0u, 0u);
+        __syncthreads();
+    };
+    for (int s = 0; s < mid::kStages - 1; ++s) issue(s);
+    if (nk > 0) {
+        Half f0, f1;                                    // the halves of a step in turn: one is read while the other multiplies
+        arrive(0);
+        issue(mid::kStages - 1);
+        read(0, 0, f0);
+        for (int64_t s = 0; s + 1 < nk; ++s) {
+            read(s, 1, f1);
+            multiply(f0);
+            arrive(s + 1);
+            issue(s + mid::kStages);
+            read(s + 1, 0, f0);
+            multiply(f1);
         }
+        read(nk - 1, 1, f1);
+        multiply(f0);
+        multiply(f1);
     }
     __syncthreads();                                    // (the stages are free, the factors in place)
 }
-// Offsets of this lane's four rows row0 + 8 i + l / 8, the last valid one instead of
+// Offsets of this lane's N rows row0 + 8 i + l / 8, the last valid one instead of
 // those past it, with the chunk that its slot holds.
-__device__ __forceinline__ void mid_offsets(uint32_t (&off)[4], int row0, int64_t valid, int64_t ld) {
+template <int N>
+__device__ __forceinline__ void mid_offsets(uint32_t (&off)[N], int row0, int64_t valid, int64_t ld) {
     const int lane = threadIdx.x & 63;
     const int last = valid < (1 << 20) ? (int)valid - 1 : 1 << 20;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
         const int row = row0 + 8 * i + (lane >> 3);
         off[i] = (uint32_t)(row < last ? row : last) * (uint32_t)ld + (uint32_t)(k128_slot(8 * i + (lane >> 3), lane & 7) * 16);
     }
@@ -284,41 +315,43 @@ __device__ __forceinline__ void store_chunk8(uint16_t* base, uint32_t bytes, int
         if (e < left) dst[e] = (uint16_t)f32_to_bf16(f[e]);
 }
 
-// Tile: 128 rows x 64 columns of act; rows of b: 32 gate rows, the 32 up rows of the
+// Tile: 64 MB rows x 64 columns of act; rows of b: 32 gate rows, the 32 up rows of the
 // same columns, 32 gate rows, ..: block 0 of a wavefront is gate, block 1 up.
-template <int FA, int FB>
+template <int FA, int FB, int MB>
 __global__ __launch_bounds__(256) void k_glu_mid(GluFwd p) {
-    __shared__ __attribute__((aligned(16))) uint8_t smem[mid::kSmem];
+    __shared__ __attribute__((aligned(16))) uint8_t smem[Mid<MB>::kSmem];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t tiles_m = (p.m + 127) / 128;
-    const int64_t row0 = (int64_t)(blockIdx.x % tiles_m) * 128, col0 = (int64_t)(blockIdx.x / tiles_m) * 64;
+    const int64_t tiles_m = (p.m + MB * 64 - 1) / (MB * 64);
+    int64_t pm, pn;
+    big_tile_coords(blockIdx.x, tiles_m, (p.inter + 63) / 64, &pm, &pn);
+    const int64_t row0 = pm * (MB * 64), col0 = pn * 64;
     const int64_t half = (int64_t)(wave & 1) * p.inter;         // wavefront w loads gate (w even) or up rows
-    uint32_t ao[4], bo[4];
-    mid_offsets(ao, wave * 32, p.m - row0, p.lda);
+    uint32_t ao[2 * MB], bo[4];
+    mid_offsets(ao, wave * (MB * 16), p.m - row0, p.lda);
     mid_offsets(bo, (wave >> 1) * 32, p.inter - col0, p.ldb);
-    float* s_rows = reinterpret_cast<float*>(smem + mid::kScaleOff);
-    float* s_cols = s_rows + 128;
+    float* s_rows = reinterpret_cast<float*>(smem + Mid<MB>::kScaleOff);
+    float* s_cols = s_rows + MB * 64;
     if (threadIdx.x < 128) {
         const int64_t r = row0 + threadIdx.x, c = col0 + (threadIdx.x & 63);
-        s_rows[threadIdx.x] = p.sa[p.sa_vec ? (r < p.m ? r : p.m - 1) : 0];
+        if (threadIdx.x < MB * 64) s_rows[threadIdx.x] = p.sa[p.sa_vec ? (r < p.m ? r : p.m - 1) : 0];
         // 64 gate factors, 64 up factors
         s_cols[threadIdx.x] = p.sb[p.sb_vec ? (threadIdx.x >> 6) * p.inter + (c < p.inter ? c : p.inter - 1) : 0];
     }
-    v16f acc[2][2];
-    mid_sums<FA, FB>(smem, p.a + row0 * p.lda, ao, p.b + (half + col0) * p.ldb, bo, p.k, acc);
-    // the wavefront's 64 rows x 32 columns of g and of u in LDS, then a lane takes rows
+    v16f acc[MB][2];
+    mid_sums<FA, FB, MB>(smem, p.a + row0 * p.lda, ao, p.b + (half + col0) * p.ldb, bo, p.k, acc);
+    // the wavefront's 32 MB rows x 32 columns of g and of u in LDS, then a lane takes rows
     // of 8 columns
     constexpr int kPitch = 68;                          // fp32 values: 32 of g, 32 of u
-    float* own = reinterpret_cast<float*>(smem) + wave * 64 * kPitch;
+    float* own = reinterpret_cast<float*>(smem) + wave * (MB * 32) * kPitch;
     const int wm = wave >> 1, wn = wave & 1;
     const float sg = s_cols[wn * 32 + (lane & 31)], su = s_cols[64 + wn * 32 + (lane & 31)];
 #pragma unroll
-    for (int mi = 0; mi < 2; ++mi)
+    for (int mi = 0; mi < MB; ++mi)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             const int row = mi * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-            const float sa = s_rows[wm * 64 + row];
+            const float sa = s_rows[wm * (MB * 32) + row];
             own[row * kPitch + (lane & 31)] = acc[mi][0][r] * sa * sg;
             own[row * kPitch + 32 + (lane & 31)] = acc[mi][1][r] * sa * su;
         }
@@ -327,9 +360,9 @@ __global__ __launch_bounds__(256) void k_glu_mid(GluFwd p) {
     const int left = p.inter - wcol < 8 ? (int)(p.inter - wcol) : 8;
     if (left <= 0) return;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2 * MB; ++j) {
         const int row = j * 16 + (lane >> 2);
-        const int64_t at = row0 + wm * 64 + row;
+        const int64_t at = row0 + wm * (MB * 32) + row;
         if (at >= p.m) continue;
         float g[8], u[8], act[8];
 #pragma unroll
@@ -351,32 +384,34 @@ __global__ __launch_bounds__(256) void k_glu_mid(GluFwd p) {
     }
 }
 
-// Tile: 128 x 128 of da, a wavefront 64 x 64.
-template <int FA, int FB>
+// Tile: 64 MB x 128 of da, a wavefront 32 MB x 64.
+template <int FA, int FB, int MB>
 __global__ __launch_bounds__(256) void k_glu_grad_mid(GluBwd p) {
-    __shared__ __attribute__((aligned(16))) uint8_t smem[mid::kSmem];
+    __shared__ __attribute__((aligned(16))) uint8_t smem[Mid<MB>::kSmem];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t tiles_m = (p.m + 127) / 128;
-    const int64_t row0 = (int64_t)(blockIdx.x % tiles_m) * 128, col0 = (int64_t)(blockIdx.x / tiles_m) * 128;
-    uint32_t ao[4], bo[4];
-    mid_offsets(ao, wave * 32, p.m - row0, p.lda);
+    const int64_t tiles_m = (p.m + MB * 64 - 1) / (MB * 64);
+    int64_t pm, pn;
+    big_tile_coords(blockIdx.x, tiles_m, (p.inter + 127) / 128, &pm, &pn);
+    const int64_t row0 = pm * (MB * 64), col0 = pn * 128;
+    uint32_t ao[2 * MB], bo[4];
+    mid_offsets(ao, wave * (MB * 16), p.m - row0, p.lda);
     mid_offsets(bo, wave * 32, p.inter - col0, p.ldb);
-    float* s_rows = reinterpret_cast<float*>(smem + mid::kScaleOff);
-    float* s_cols = s_rows + 128;
+    float* s_rows = reinterpret_cast<float*>(smem + Mid<MB>::kScaleOff);
+    float* s_cols = s_rows + MB * 64;
     if (threadIdx.x < 128) {
         const int64_t r = row0 + threadIdx.x, c = col0 + threadIdx.x;
-        s_rows[threadIdx.x] = p.sa[p.sa_vec ? (r < p.m ? r : p.m - 1) : 0];
+        if (threadIdx.x < MB * 64) s_rows[threadIdx.x] = p.sa[p.sa_vec ? (r < p.m ? r : p.m - 1) : 0];
         s_cols[threadIdx.x] = p.sb[p.sb_vec ? (c < p.inter ? c : p.inter - 1) : 0];
     }
-    v16f acc[2][2];
-    mid_sums<FA, FB>(smem, p.a + row0 * p.lda, ao, p.b + col0 * p.ldb, bo, p.k, acc);
-    constexpr int kPitch = 68;
-    float* own = reinterpret_cast<float*>(smem) + wave * 64 * kPitch;
+    v16f acc[MB][2];
+    mid_sums<FA, FB, MB>(smem, p.a + row0 * p.lda, ao, p.b + col0 * p.ldb, bo, p.k, acc);
+    constexpr int kPitch = 68, kPasses = MB * 4;
+    float* own = reinterpret_cast<float*>(smem) + wave * (MB * 32) * kPitch;
     const int wm = wave >> 1, wn = wave & 1;
     const int64_t wcol = col0 + wn * 64 + 8 * (lane & 7);
     const int left = p.inter - wcol < 8 ? (int)(p.inter - wcol) : 8;
-    const int64_t wrow = row0 + wm * 64;
+    const int64_t wrow = row0 + wm * (MB * 32);
     // h, two rows ahead
     u32x4 hg[3], hu[3];
     auto load_h = [&](int j) {
@@ -400,19 +435,19 @@ __global__ __launch_bounds__(256) void k_glu_grad_mid(GluBwd p) {
     load_h(1);
 #pragma unroll
     for (int ni = 0; ni < 2; ++ni) {
-        const float sb = s_cols[wn * 64 + ni * 32 + (lane & 31)];
+        const float sb = s_cols[(wn * 2 + ni) * 32 + (lane & 31)];
 #pragma unroll
-        for (int mi = 0; mi < 2; ++mi)
+        for (int mi = 0; mi < MB; ++mi)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int row = mi * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-                own[row * kPitch + ni * 32 + (lane & 31)] = acc[mi][ni][r] * s_rows[wm * 64 + row] * sb;
+                own[row * kPitch + ni * 32 + (lane & 31)] = acc[mi][ni][r] * s_rows[wm * (MB * 32) + row] * sb;
             }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (j + 2 < 8) load_h(j + 2);
+    for (int j = 0; j < kPasses; ++j) {
+        if (j + 2 < kPasses) load_h(j + 2);
         const int row = j * 8 + (lane >> 3);
         float dg[8], du[8], act[8];
 #pragma unroll
@@ -779,6 +814,13 @@ static int64_t persistent_grid(int64_t tiles) {
     const int64_t cus = current_device_props().cus, most = cus >= 8 ? cus / 8 * 8 : cus;
     return tiles < most ? tiles : most;
 }
+// Tiles of 64 rows where those of 128 would leave half of the CUs idle, or half of
+// each tile empty. With them and without: product of 300 x 2048 x 1408 10.2 and 13.7 us,
+// 64 x 4096 x 14336 30 and 32, gradient of 1001 x 2048 x 1408 13.5 and 19.2. Past the limit:
+// product of 777 x 2048 x 1408 (154 tiles of 128) 18.8 and 14.9, gradient of
+// 200 x 4096 x 14336 (224) 35 and 29.
+static bool mid_rows64(int64_t m, int64_t tiles128) { return m <= 64 || tiles128 <= 128; }
+
 template <int FA, int FB>
 hipError_t glu_typed(const GluFwd& p, hipStream_t st) {
     const int64_t large = (p.m + 255) / 256 * ((p.inter + 127) / 128);
@@ -794,8 +836,13 @@ hipError_t glu_typed(const GluFwd& p, hipStream_t st) {
         else hipLaunchKernelGGL((k_glu_few<FA, FB, 2>), grid, dim3(kFewWaves * 64), 0, st, p);
         return hipGetLastError();
     }
-    const int64_t tiles = (p.m + 127) / 128 * ((p.inter + 63) / 64);
-    hipLaunchKernelGGL((k_glu_mid<FA, FB>), dim3((unsigned)tiles), dim3(256), 0, st, p);
+    const int64_t tiles_n = (p.inter + 63) / 64, tiles = (p.m + 127) / 128 * tiles_n;
+    if (mid_rows64(p.m, tiles)) {
+        const dim3 grid((unsigned)((p.m + 63) / 64 * tiles_n));
+        hipLaunchKernelGGL((k_glu_mid<FA, FB, 1>), grid, dim3(256), 0, st, p);
+    } else {
+        hipLaunchKernelGGL((k_glu_mid<FA, FB, 2>), dim3((unsigned)tiles), dim3(256), 0, st, p);
+    }
     return hipGetLastError();
 }
 
@@ -808,8 +855,13 @@ hipError_t glu_grad_typed(const GluBwd& p, hipStream_t st) {
         else hipLaunchKernelGGL((k_glu_grad_persist<FA, FB, false>), grid, dim3(256), 0, st, p);
         return hipGetLastError();
     }
-    const int64_t tiles = (p.m + 127) / 128 * ((p.inter + 127) / 128);
-    hipLaunchKernelGGL((k_glu_grad_mid<FA, FB>), dim3((unsigned)tiles), dim3(256), 0, st, p);
+    const int64_t tiles_n = (p.inter + 127) / 128, tiles = (p.m + 127) / 128 * tiles_n;
+    if (mid_rows64(p.m, tiles)) {
+        const dim3 grid((unsigned)((p.m + 63) / 64 * tiles_n));
+        hipLaunchKernelGGL((k_glu_grad_mid<FA, FB, 1>), grid, dim3(256), 0, st, p);
+    } else {
+        hipLaunchKernelGGL((k_glu_grad_mid<FA, FB, 2>), dim3((unsigned)tiles), dim3(256), 0, st, p);
+    }
     return hipGetLastError();
 }
 

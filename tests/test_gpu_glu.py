@@ -59,6 +59,7 @@ FORWARD = [  # m, k, inter, fa, fb, a_mode, b_mode, h, output row padding
     (8200, 256, 1026, 0, 0, 1, 0, True, 2), (5000, 272, 900, 0, 0, 1, 1, True, 4), (40, 0, 72, 0, 0, 1, 1, True, 8),
     (300, 0, 200, 0, 0, 0, 0, True, 8), (48, 1296, 24, 0, 0, 1, 1, True, 8), (33, 256, 7, 1, 0, 1, 1, True, 2),
     (5, 2304, 50, 0, 0, 1, 0, True, 8), (70, 128, 5, 0, 0, 1, 1, True, 1), (200, 384, 64, 0, 1, 1, 1, False, 8),
+    (130, 1008, 4233, 0, 0, 1, 1, True, 3), (1030, 144, 1000, 0, 1, 0, 1, False, 8), (63, 640, 8300, 1, 0, 1, 1, True, 4),
     (129, 400, 72, 0, 0, 1, 1, True, 8), (500, 1008, 136, 1, 0, 0, 1, True, 8), (255, 4096, 16392, 0, 0, 1, 1, False, 8),
 ]
 
@@ -92,6 +93,7 @@ def test_forward(fp8, m, k, inter, fa, fb, am, bm, want_h, pad):
 
 BACKWARD = [  # m, k, inter, fa, fb, a_mode, b_mode, act, row padding
     (1, 16, 1, 1, 0, 1, 1, True, 0), (3, 272, 40, 1, 0, 1, 0, True, 3), (64, 512, 136, 1, 0, 1, 1, False, 8),
+    (130, 1008, 8261, 1, 0, 1, 1, True, 3), (1100, 144, 2060, 0, 1, 0, 1, False, 8), (63, 640, 8300, 1, 0, 1, 1, True, 4),
     (130, 1024, 200, 1, 0, 1, 1, True, 24), (300, 512, 641, 0, 1, 0, 1, True, 7), (1001, 256, 1408, 1, 0, 1, 1, False, 8),
     (4000, 512, 2100, 1, 0, 1, 1, True, 4), (4097, 256, 2200, 0, 0, 1, 1, True, 0), (2049, 768, 4104, 1, 1, 0, 0, False, 8),
     (8200, 256, 1026, 1, 0, 1, 0, True, 2), (5000, 272, 900, 0, 0, 1, 1, True, 4), (300, 0, 72, 0, 0, 1, 1, True, 8),
