@@ -57,13 +57,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // lanes a row) and turned into the matrix cores' order (lane l: 32 bytes of row l % 16)
 // through LDS of the wavefront's own; the next block is on its way while one is
 // multiplied.
-constexpr int kFewRows = 32, kFewWaves = 4, kFewBlock = 256;
+constexpr int kFewRows = 32, kFewBlock = 256;
 
-template <int FA, int FB, int NT>
-__global__ __launch_bounds__(kFewWaves * 64) void k_glu_few(GluFwd p) {
+template <int FA, int FB, int NT, int W>
+__global__ __launch_bounds__(W * 64) void k_glu_few(GluFwd p) {
     // a wavefront's part: two tiles of 16 rows x 256 bytes, then its sums [2 NT][256]
     constexpr int kPart = 8192 > NT * 2048 ? 8192 : NT * 2048;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kFewWaves][kPart];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[W][kPart];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, m = lane & 15;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int cols = p.inter - n0 < 16 ? (int)(p.inter - n0) : 16;
@@ -140,8 +140,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_glu_few(GluFwd p) {
         u32x4 a[2][4], b[2][4];                         // in turn, so that no load waits to be copied
         int64_t i = wave;
         if (i < blocks) load(i, a);
-        for (; i < blocks; i += 2 * kFewWaves) {
-            const int64_t j = i + kFewWaves, k = j + kFewWaves;
+        for (; i < blocks; i += 2 * W) {
+            const int64_t j = i + W, k = j + W;
             work(i, a, j < blocks ? &b : nullptr, j);
             if (j >= blocks) break;
             work(j, b, k < blocks ? &a : nullptr, k);
@@ -155,17 +155,17 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_glu_few(GluFwd p) {
         for (int t = 0; t < 2; ++t)                     // column (row of a) m, rows (of b) 4 q ..
             *reinterpret_cast<v4f*>(sums + (n * 2 + t) * 256 + m * 16 + q * 4) = acc[t][n];
     __syncthreads();
-    const int row16 = threadIdx.x >> 4, col = threadIdx.x & 15;
+    const int col = threadIdx.x & 15;
     if (col >= cols) return;
     const float sg = p.sb[p.sb_vec ? n0 + col : 0], su = p.sb[p.sb_vec ? p.inter + n0 + col : 0];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int64_t row = n * 16 + row16;
+    for (int i = threadIdx.x; i < NT * 256; i += W * 64) {
+        const int64_t row = i >> 4;
         if (row >= p.m) break;
         float g = 0.0f, u = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kFewWaves; ++w) {
-            const float* s = reinterpret_cast<const float*>(lds[w]) + n * 512 + threadIdx.x;
+        for (int w = 0; w < W; ++w) {
+            const float* s = reinterpret_cast<const float*>(lds[w]) + (i >> 8) * 512 + (i & 255);
             g += s[0];
             u += s[256];
         }
@@ -814,6 +814,11 @@ static int64_t persistent_grid(int64_t tiles) {
     const int64_t cus = current_device_props().cus, most = cus >= 8 ? cus / 8 * 8 : cus;
     return tiles < most ? tiles : most;
 }
+// Large tiles where those of a quarter of their size would take a CU more than one.
+// Product of 512 x 4096 x 7168 (112 large tiles) 41 us, 45 in 128 x 128 tiles; of
+// 256 x 4096 x 8192 (64) 41 and 24; gradient of 2048 x 4096 x 4096 (128) 50 and 58, of
+// 1024 x 4096 x 4096 (64) 46 and 29.
+constexpr int64_t kMidLarge = 64;
 // Tiles of 64 rows where those of 128 would leave half of the CUs idle, or half of
 // each tile empty. With them and without: product of 300 x 2048 x 1408 10.2 and 13.7 us,
 // 64 x 4096 x 14336 30 and 32, gradient of 1001 x 2048 x 1408 13.5 and 19.2. Past the limit:
@@ -824,16 +829,27 @@ static bool mid_rows64(int64_t m, int64_t tiles128) { return m <= 64 || tiles128
 template <int FA, int FB>
 hipError_t glu_typed(const GluFwd& p, hipStream_t st) {
     const int64_t large = (p.m + 255) / 256 * ((p.inter + 127) / 128);
-    if (p.k > 0 && p.k % 256 == 0 && p.m >= 256 && p.inter >= 128 && large >= 128) {
+    if (p.k > 0 && p.k % 256 == 0 && p.m >= 256 && p.inter >= 128 && large > kMidLarge) {
         const dim3 grid((unsigned)persistent_grid(large));
         if (p.h) hipLaunchKernelGGL((k_glu_persist<FA, FB, true>), grid, dim3(256), 0, st, p);
         else hipLaunchKernelGGL((k_glu_persist<FA, FB, false>), grid, dim3(256), 0, st, p);
         return hipGetLastError();
     }
+    // (32 rows, 2048 x 1408: 6.4 us, 9.0 in tiles of 64 rows; 4096 x 14336: 32.6 and 29.4;
+    // 33 rows 42 and 30)
     if (p.m <= kFewRows) {
         const dim3 grid((unsigned)((p.inter + 15) / 16));
-        if (p.m <= 16) hipLaunchKernelGGL((k_glu_few<FA, FB, 1>), grid, dim3(kFewWaves * 64), 0, st, p);
-        else hipLaunchKernelGGL((k_glu_few<FA, FB, 2>), grid, dim3(kFewWaves * 64), 0, st, p);
+        // Fewer workgroups than CUs: eight wavefronts each, else four. One row, 2048 x 1408
+        // (88 workgroups) 4.4 and 4.9 us; 32 rows, 4096 x 4096 (256) 12.7 and 11.3.
+#define CALL(NT, W) hipLaunchKernelGGL((k_glu_few<FA, FB, NT, W>), grid, dim3(W * 64), 0, st, p)
+        if (grid.x < 256) {
+            if (p.m <= 16) CALL(1, 8);
+            else CALL(2, 8);
+        } else {
+            if (p.m <= 16) CALL(1, 4);
+            else CALL(2, 4);
+        }
+#undef CALL
         return hipGetLastError();
     }
     const int64_t tiles_n = (p.inter + 63) / 64, tiles = (p.m + 127) / 128 * tiles_n;
@@ -849,7 +865,7 @@ hipError_t glu_typed(const GluFwd& p, hipStream_t st) {
 template <int FA, int FB>
 hipError_t glu_grad_typed(const GluBwd& p, hipStream_t st) {
     const int64_t large = (p.m + 255) / 256 * ((p.inter + 255) / 256);
-    if (p.k > 0 && p.k % 256 == 0 && p.m >= 256 && p.inter >= 256 && large >= 128) {
+    if (p.k > 0 && p.k % 256 == 0 && p.m >= 256 && p.inter >= 256 && large > kMidLarge) {
         const dim3 grid((unsigned)persistent_grid(large));
         if (p.act) hipLaunchKernelGGL((k_glu_grad_persist<FA, FB, true>), grid, dim3(256), 0, st, p);
         else hipLaunchKernelGGL((k_glu_grad_persist<FA, FB, false>), grid, dim3(256), 0, st, p);
