@@ -313,7 +313,7 @@ fp8_status_t fp8_lora_add(const uint16_t* x, int64_t tokens, int64_t k, int64_t 
     if (!aligned(base, 2) || !aligned(out, 2) || !aligned(adapter_idx, 4) || !aligned(scaling, 4) ||
         !aligned(workspace, 16))
         return fail(FP8_ERR_ALIGNMENT, "%s: misaligned pointer", fn);
-    // (grids: 1024 threads for 16 tokens, 512 columns a workgroup in the second direction)
+    // (grids: 64 tokens a workgroup in the first direction, at most one for 256 columns in the second)
     if (tokens >= ((int64_t)1 << 25) || n >= ((int64_t)1 << 24))
         return fail(FP8_ERR_UNSUPPORTED, "%s: %lld x %lld outputs", fn, (long long)tokens, (long long)n);
     if (ldx >= (1 << 24) || ld_a >= (1 << 24) || ld_b >= (1 << 24) || (base && ldbase >= (1 << 24)) || ldout >= (1 << 24))
