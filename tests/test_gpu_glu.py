@@ -209,3 +209,32 @@ def test_gradient_against_differences(fp8):
     got = bf16_of(dh)
     within(got[:, :inter], dg, want["dg_tol"] + step ** 2 / 6 * np.abs(da * u), "d(gate)")
     within(got[:, inter:], du, want["du_tol"] + 1e-9 * np.abs(du), "d(up)")
+
+
+def spread(t, ld):
+    """t with its rows ld elements apart."""
+    rows, cols = t.shape
+    far = torch.empty((rows - 1) * ld + cols, dtype=t.dtype, device=DEV).as_strided((rows, cols), (ld, 1))
+    return far.copy_(t)
+
+
+@pytest.mark.parametrize("m,k,inter", [(7, 272, 24), (70, 272, 24), (300, 256, 4300)])
+def test_rows_far_apart(fp8, m, k, inter):
+    """Leading dimensions at their limits: the rows of one tile span 4 GiB and more."""
+    rng = np.random.default_rng(m)
+    qa, sa, sad = operand(rng, m, k, 0, 1, 1.0)
+    qb, sb, sbd = operand(rng, 2 * inter, k, 0, 1, 0.1)
+    qd, sd, sdd = operand(rng, inter, k, 0, 1, 0.1)
+    ldf, ldo = (1 << 24) - 16, (1 << 25) - 8
+    a, b, d = padded(qa, 16), padded(qb, 32), padded(qd, 32)
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    say("gated product, rows far apart", m, k, inter)
+    fa, fb, fd = spread(a, ldf), (spread(b, ldf) if inter < 100 else b), (spread(d, ldf) if inter < 100 else d)
+    near = [torch.zeros((m, w * inter), **bf) for w in (1, 2, 2, 1)]
+    far = [spread(t, ldo) for t in near]
+    for q, w, v, o in ((a, b, d, near), (fa, fb, fd, far)):
+        fp8.fp8_gemm_swiglu(q, 0, w, 0, dev_f32(sad), 1, dev_f32(sbd), 1, o[0], h=o[1])
+        fp8.fp8_gemm_swiglu_backward(q, 0, v, 0, dev_f32(sad), 1, dev_f32(sdd), 1, o[1], o[2], act=o[3])
+    torch.cuda.synchronize()
+    for n, f in zip(near, far):
+        assert torch.equal(n, f)

@@ -162,3 +162,45 @@ def test_empty(fp8):
                      torch.ones(1, device=DEV), torch.empty(0, dtype=torch.int32, device=DEV), torch.empty((0, 32), **bf),
                      torch.empty((0, 32), **bf), torch.empty(0, device=DEV))
     torch.cuda.synchronize()
+
+
+def spread(t, ld):
+    """t with its rows ld elements apart."""
+    rows, cols = t.shape
+    far = torch.empty((rows - 1) * ld + cols, dtype=t.dtype, device=DEV).as_strided((rows, cols), (ld, 1))
+    return far.copy_(t)
+
+
+def test_rows_far_apart(fp8):
+    """Leading dimensions at their limit: the rows of one workgroup span 2 GiB."""
+    tokens, k, n, rank, E, ld = 130, 72, 43, 16, 3, (1 << 24) - 8
+    x = torch.randn((tokens, k), device=DEV).to(torch.bfloat16)
+    a = torch.randn((E, rank, k), device=DEV).to(torch.bfloat16)
+    b = torch.randn((E, n, rank), device=DEV).to(torch.bfloat16)
+    base = torch.randn((tokens, n), device=DEV).to(torch.bfloat16)
+    ids = (torch.arange(tokens, device=DEV, dtype=torch.int32) * 7) % 5 - 1
+    sc, ws = torch.rand(E, device=DEV), fp8.lora_workspace(tokens, rank)
+    near = torch.empty_like(base)
+    say("adapters, rows far apart")
+    fp8.fp8_lora_add(x, a, b, sc, ids, base, near, ws)
+    af = spread(a.reshape(E * rank, k), ld).as_strided((E, rank, k), (rank * ld, ld, 1))
+    bf = spread(b.reshape(E * n, rank), ld).as_strided((E, n, rank), (n * ld, ld, 1))
+    out = spread(torch.zeros_like(base), ld)
+    fp8.fp8_lora_add(spread(x, ld), af, bf, sc, ids, spread(base, ld), out, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out, near)
+
+
+@pytest.mark.parametrize("index", [-(1 << 31), -1, 3, (1 << 31) - 1])
+def test_indices_without_an_adapter(fp8, index):
+    tokens, k, n, rank, E = 70, 64, 300, 8, 3
+    x = torch.full((tokens, k), float("nan"), dtype=torch.bfloat16, device=DEV)
+    a = torch.full((E, rank, k), float("nan"), dtype=torch.bfloat16, device=DEV)
+    b = torch.full((E, n, rank), float("nan"), dtype=torch.bfloat16, device=DEV)
+    base = torch.randn((tokens, n), device=DEV).to(torch.bfloat16)
+    out = torch.full_like(base, 3.0)
+    ids = torch.full((tokens,), index, dtype=torch.int32, device=DEV)
+    say("adapters, index", index)
+    fp8.fp8_lora_add(x, a, b, torch.ones(E, device=DEV), ids, base, out, fp8.lora_workspace(tokens, rank))
+    torch.cuda.synchronize()
+    assert torch.equal(out, base)
