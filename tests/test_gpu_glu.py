@@ -238,3 +238,25 @@ def test_rows_far_apart(fp8, m, k, inter):
     torch.cuda.synchronize()
     for n, f in zip(near, far):
         assert torch.equal(n, f)
+
+
+@pytest.mark.parametrize("m,k,inter,fa,fb,am,bm,want_h,pad", [
+    (4100, 768, 2184, 0, 1, 1, 1, True, 8), (4100, 512, 3976, 0, 0, 1, 1, True, 0)])
+def test_forward_of_many_tiles(fp8, m, k, inter, fa, fb, am, bm, want_h, pad):
+    """More large tiles than CUs: a workgroup goes on to its second (306 tiles, six steps
+    of K) and third one (544 tiles), with h and without."""
+    test_forward(fp8, m, k, inter, fa, fb, am, bm, want_h, pad)
+
+
+def test_backward_of_many_tiles(fp8):
+    """The same of the gradient (306 tiles, six steps of K), with act and without."""
+    test_backward(fp8, 4100, 768, 4360, 1, 0, 1, 1, True, 8)
+
+
+@pytest.mark.parametrize("m,k,inter,fa,fb,am,bm,want_h,pad", [
+    (1, 1040, 4104, 0, 0, 1, 1, True, 3), (2, 4096, 8200, 0, 1, 1, 0, True, 8), (16, 528, 4120, 1, 0, 0, 1, True, 8),
+    (17, 2304, 4097, 0, 0, 1, 1, True, 1), (32, 768, 5000, 1, 1, 1, 1, True, 8), (32, 1040, 14336, 0, 0, 1, 1, True, 0),
+    (24, 512, 8192, 0, 0, 1, 1, True, 8)])
+def test_forward_of_few_rows_and_many_columns(fp8, m, k, inter, fa, fb, am, bm, want_h, pad):
+    """A decoding batch at the widths that are served: as many workgroups as CUs and more."""
+    test_forward(fp8, m, k, inter, fa, fb, am, bm, want_h, pad)

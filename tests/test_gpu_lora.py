@@ -204,3 +204,24 @@ def test_indices_without_an_adapter(fp8, index):
     fp8.fp8_lora_add(x, a, b, torch.ones(E, device=DEV), ids, base, out, fp8.lora_workspace(tokens, rank))
     torch.cuda.synchronize()
     assert torch.equal(out, base)
+
+
+@pytest.mark.parametrize("tokens", [1, 20, 300])
+def test_largest_values(fp8, tokens):
+    """A value between bf16's largest and fp32's stays finite (the definition's output is 64
+    times its quotient by 2^126); past fp32's it is Inf, for that adapter's tokens alone."""
+    k, n, rank = 8, 40, 8
+    x = torch.zeros((tokens, k), device=DEV)
+    x[:, 1] = 2.0 ** 63
+    a, b = torch.zeros((3, rank, k), device=DEV), torch.zeros((3, n, rank), device=DEV)
+    a[:, 3, 1] = 2.0 ** 63
+    b[:, :, 3] = 2.0 ** -120
+    sc = torch.tensor([4 * (1 - 2.0 ** -24), 4.5, -4 * (1 - 2.0 ** -10)], device=DEV)
+    ids = torch.arange(tokens, device=DEV, dtype=torch.int32) % 3
+    out = torch.empty((tokens, n), dtype=torch.bfloat16, device=DEV)
+    say("adapters, largest values", tokens)
+    fp8.fp8_lora_add(x.to(torch.bfloat16), a.to(torch.bfloat16), b.to(torch.bfloat16), sc, ids, None, out,
+                     fp8.lora_workspace(tokens, rank))
+    torch.cuda.synchronize()
+    want = torch.tensor([256.0, float("inf"), -256.0], device=DEV)      # (255.99998 and 255.75 in bf16, whose step there is 1)
+    assert torch.equal(out.float(), want[ids.long()][:, None].expand(tokens, n))
