@@ -420,6 +420,7 @@ __global__ __launch_bounds__(256, RS == 1 ? 4 : RS == 2 ? 3 : 2) void k_lora_up(
     } while (0)
 
 int64_t at_most(int64_t a, int64_t b) { return a < b ? a : b; }
+int64_t at_least(int64_t a, int64_t b) { return a > b ? a : b; }
 
 }  // namespace
 
@@ -430,13 +431,14 @@ hipError_t launch_lora_add(const Lora& call, hipStream_t st) {
     // units of a group: at most one a token, and one an adapter (or none) and one for 16 tokens
     const int64_t most = at_most(p.tokens, kGroup), slots = at_most(most, (int64_t)p.adapters + 1 + most / kTile);
     const int64_t active = groups * slots;
-    // Short workgroups, many of them: one spends its time on a chain of dependent loads.
-    // (128 tokens of as many requests, rank 16, 4096 x 14336: 4 blocks of columns a
-    // workgroup 20 us, 14 of them 34; one 26, for the values of v added up again. One token,
-    // k = 14336: 16 parts 4.7 + 4.5 us, 8 of them 6.0 + 4.3, 56 of them 3.6 + 6.4.)
-    const int64_t parts = at_most(at_most((2048 + active - 1) / active, kLoraMaxParts),
-                                  at_most((steps + 3) / 4, kLoraPartRows / p.tokens));
-    p.parts = (int)(parts < 1 ? 1 : parts);
+    // Parts of k for few tokens, as short workgroups, many of them: one spends its time on a
+    // chain of dependent loads. (One token, k = 14336: 16 parts 4.7 + 4.5 us, 8 of them 6.0 + 4.3,
+    // 56 of them 3.6 + 6.4. 1500 tokens of 9 requests, rank 16, 4096 x 4096: 5 parts 6.7 + 12.1,
+    // 2 of them 9.4 + 10.5; 512 of as many requests: 8 parts 10.8 + 15.7, 16 of them 14 + 16.) By
+    // the sizes alone: the order of a token's sums must not change with the adapters that are
+    // loaded beside its own.
+    const int64_t by_tokens = at_least(at_most(kLoraMaxParts, 4096 / p.tokens), at_most(8, kLoraPartRows / p.tokens));
+    p.parts = (int)at_least(at_most(by_tokens, (steps + 3) / 4), 1);
 #define CALL(RT)                                                                                              \
     hipLaunchKernelGGL((k_lora_down<RT>), dim3((unsigned)groups, (unsigned)p.parts, (unsigned)slots), dim3(256), 0, \
                        st, p)
@@ -444,6 +446,8 @@ hipError_t launch_lora_add(const Lora& call, hipStream_t st) {
 #undef CALL
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    // (128 tokens of as many requests, rank 16, 4096 x 14336: 4 blocks of columns a workgroup
+    // 20 us, 14 of them 34; one 26, for the values of v added up again.)
     const int64_t blocks_n = (p.n + 255) / 256;
     const dim3 grid((unsigned)groups, (unsigned)at_most((4096 + active - 1) / active, blocks_n), (unsigned)slots);
 #define CALL(RS) hipLaunchKernelGGL((k_lora_up<RS>), grid, dim3(256), 0, st, p, blocks_n)

@@ -737,8 +737,8 @@ fp8_status_t fp8_gemm_swiglu_backward(const uint8_t* a, fp8_format_t fa, int64_t
  * significant bits, the output rounded once. Adapters of smaller rank are padded
  * with zeros. Any order of tokens is served; tokens of one adapter among 64
  * neighbours share its loads. No other token's or adapter's values enter a token's result,
- * and the same call gives the same bits; the order of the fp32 sums depends on
- * the number of tokens.
+ * and the same call gives the same bits, whatever other adapters are loaded; the
+ * order of the fp32 sums depends on the number of tokens and on k.
  * rank a multiple of 8, 8..FP8_LORA_MAX_RANK; k a multiple of 8, >= 8; adapters >=
  * 1; tokens < 2^25, n and the leading dimensions < 2^24 (else FP8_ERR_UNSUPPORTED);
  * x, A, B 16-byte aligned with ldx, ld_a, ld_b and the adapter strides multiples of

@@ -225,3 +225,24 @@ def test_largest_values(fp8, tokens):
     torch.cuda.synchronize()
     want = torch.tensor([256.0, float("inf"), -256.0], device=DEV)      # (255.99998 and 255.75 in bf16, whose step there is 1)
     assert torch.equal(out.float(), want[ids.long()][:, None].expand(tokens, n))
+
+
+@pytest.mark.parametrize("tokens,k,n,rank", [(5, 4096, 4096, 16), (300, 4096, 4096, 16), (1000, 2048, 1024, 40), (2100, 1024, 512, 8)])
+def test_bits_do_not_depend_on_the_adapters_loaded(fp8, tokens, k, n, rank):
+    """An adapter that is loaded beside the others changes no request's bits."""
+    x = torch.randn((tokens, k), device=DEV).to(torch.bfloat16)
+    a = (torch.randn((200, rank, k), device=DEV) * k ** -0.5).to(torch.bfloat16)
+    b = (torch.randn((200, n, rank), device=DEV) * rank ** -0.5).to(torch.bfloat16)
+    base = torch.randn((tokens, n), device=DEV).to(torch.bfloat16)
+    sc, ws = torch.rand(200, device=DEV) + 0.5, fp8.lora_workspace(tokens, rank)
+    ids = torch.randint(-1, 8, (tokens,), device=DEV, dtype=torch.int32)
+    ids[ids < 0] = -1
+    outs = []
+    for E in (8, 9, 64, 200):
+        out = torch.empty_like(base)
+        say("adapters loaded", tokens, k, n, rank, E)
+        fp8.fp8_lora_add(x, a[:E], b[:E], sc[:E], ids, base, out, ws)
+        torch.cuda.synchronize()
+        outs.append(out)
+    for out in outs[1:]:
+        assert torch.equal(out, outs[0])
