@@ -27,6 +27,7 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 constexpr int kTile = 16;                       // tokens of a product
 constexpr int kStepK = 64;                      // columns of x of one step of a wavefront
 constexpr int kWaves = 4, kGroup = 64;          // wavefronts of a workgroup, tokens that it looks at
+constexpr int64_t kUpWorkgroups = 2560;         // of the second launch
 
 __device__ __forceinline__ v4f mfma(u32x4 a, u32x4 b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
@@ -45,10 +46,12 @@ __device__ __forceinline__ void store8(uint16_t* base, uint32_t bytes, u32x4 v) 
 // Up to 16 tokens of one adapter out of a group of 64: the slot-th such unit (by its
 // first token), an adapter of more tokens has several. Tokens without an adapter are
 // units too, those of e = p.adapters. Lane r holds the place in the group of the
-// adapter's r-th token; the unit's are c0 .. c0 + count - 1.
+// adapter's r-th token; the unit's are c0 .. c0 + count - 1. pick(number of units): the
+// workgroup's, no unit past the last.
 struct Unit {
     int e, c0, count, token;
-    __device__ __forceinline__ bool find(const Lora& p, int64_t t0, int slot) {
+    template <typename Pick>
+    __device__ __forceinline__ bool find(const Lora& p, int64_t t0, Pick pick) {
         const int lane = threadIdx.x & 63;
         const int n = p.tokens - t0 < kGroup ? (int)(p.tokens - t0) : kGroup;
         int mine = lane < n ? p.adapter[t0 + lane] : p.adapters;
@@ -63,7 +66,8 @@ struct Unit {
         const uint64_t below = (1ull << lane) - 1ull;
         const int rank = __popcll(same & below);
         const uint64_t heads = __ballot(lane < n && rank % kTile == 0);
-        if (slot >= __popcll(heads)) return false;
+        const int units = __popcll(heads), slot = pick(units);
+        if (slot >= units) return false;
         const uint64_t one = __ballot(((heads >> lane) & 1u) && __popcll(heads & below) == slot);
         const int head = __ffsll((unsigned long long)one) - 1;
         e = __builtin_amdgcn_readlane(mine, head);
@@ -223,7 +227,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_lora_down(Lora p) {
     const int lane = threadIdx.x & 63;
     const int64_t t0 = (int64_t)blockIdx.x * kGroup;
     Unit unit;
-    if (!unit.find(p, t0, blockIdx.z) || unit.e == p.adapters) return;
+    if (!unit.find(p, t0, [](int) { return (int)blockIdx.z; }) || unit.e == p.adapters) return;
     const int64_t steps = (p.k + kStepK - 1) / kStepK;
     const int64_t s0 = steps * blockIdx.y / p.parts, s1 = steps * (blockIdx.y + 1) / p.parts;
     uint32_t ao[RT][2], xo[2];
@@ -377,14 +381,31 @@ __device__ __forceinline__ void copy_blocks(const Lora& p, int64_t t0, const int
     }
 }
 
-// Workgroup: a unit, blocks y, y + gridDim.y, .. of columns.
+// a / b, a below 4096 (the reciprocal's error, 2^-10 of 1 / b, is far from the quotient's
+// distance to a whole number, half of 1 / b).
+__device__ __forceinline__ int small_quotient(int a, int b) {
+    return (int)(((float)a + 0.5f) * __builtin_amdgcn_rcpf((float)b));
+}
+
+// Workgroup: a unit, blocks share, share + shares, .. of columns. The group's `workgroups`
+// are shared out among the units that it has, not the adapters loaded, up to most_shares
+// of them a unit (and each unit has one: the grid has workgroups + the most units - 1).
 template <int RS>
-__global__ __launch_bounds__(256, RS == 1 ? 4 : RS == 2 ? 3 : 2) void k_lora_up(Lora p, int64_t blocks_n) {
+__global__ __launch_bounds__(256, RS == 1 ? 4 : RS == 2 ? 3 : 2) void k_lora_up(Lora p, int64_t blocks_n, int workgroups,
+                                                                                         int most_shares) {
     __shared__ UpLds<RS> lds;
     const int lane = threadIdx.x & 63;
     const int64_t t0 = (int64_t)blockIdx.x * kGroup;
     Unit unit;
-    if (!unit.find(p, t0, blockIdx.z)) return;
+    int share, shares;
+    const bool found = unit.find(p, t0, [&](int units) {
+        const int even = small_quotient(workgroups + units - 1, units);
+        shares = even < most_shares ? even : most_shares;
+        const int slot = small_quotient(blockIdx.y, shares);
+        share = (int)blockIdx.y - slot * shares;
+        return slot;
+    });
+    if (!found) return;
     int t[2];
     bool live[2];
 #pragma unroll
@@ -394,12 +415,12 @@ __global__ __launch_bounds__(256, RS == 1 ? 4 : RS == 2 ? 3 : 2) void k_lora_up(
         live[i] = c < unit.count;
     }
     if (unit.e == p.adapters) {
-        if (p.base != p.out) copy_blocks(p, t0, t, live, blockIdx.y, gridDim.y, blocks_n);
+        if (p.base != p.out) copy_blocks(p, t0, t, live, share, shares, blocks_n);
         return;
     }
     lds.fill(p, unit, t0);
     __syncthreads();
-    up_blocks<RS>(p, unit.e, t0, t, live, lds, blockIdx.y, gridDim.y, blocks_n);
+    up_blocks<RS>(p, unit.e, t0, t, live, lds, share, shares, blocks_n);
 }
 
 // 16-row tiles of the rank of the first launch.
@@ -430,7 +451,6 @@ hipError_t launch_lora_add(const Lora& call, hipStream_t st) {
     const int64_t groups = (p.tokens + kGroup - 1) / kGroup, steps = (p.k + kStepK - 1) / kStepK;
     // units of a group: at most one a token, and one an adapter (or none) and one for 16 tokens
     const int64_t most = at_most(p.tokens, kGroup), slots = at_most(most, (int64_t)p.adapters + 1 + most / kTile);
-    const int64_t active = groups * slots;
     // Parts of k for few tokens, as short workgroups, many of them: one spends its time on a
     // chain of dependent loads. (One token, k = 14336: 16 parts 4.7 + 4.5 us, 8 of them 6.0 + 4.3,
     // 56 of them 3.6 + 6.4. 1500 tokens of 9 requests, rank 16, 4096 x 4096: 5 parts 6.7 + 12.1,
@@ -446,11 +466,17 @@ hipError_t launch_lora_add(const Lora& call, hipStream_t st) {
 #undef CALL
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // (128 tokens of as many requests, rank 16, 4096 x 14336: 4 blocks of columns a workgroup
-    // 20 us, 14 of them 34; one 26, for the values of v added up again.)
-    const int64_t blocks_n = (p.n + 255) / 256;
-    const dim3 grid((unsigned)groups, (unsigned)at_most((4096 + active - 1) / active, blocks_n), (unsigned)slots);
-#define CALL(RS) hipLaunchKernelGGL((k_lora_up<RS>), grid, dim3(256), 0, st, p, blocks_n)
+    // Ten workgroups a CU in all where every unit has work for so many: those of a group of
+    // tokens are shared out among its units, whatever is loaded. (128 tokens of as many
+    // requests, rank 16, 4096 x 14336, 64 adapters: 16 a CU 18 us, 10 of them 15.) A unit has
+    // no more than the rest of the rule gives it with 12 units a group: beyond that the values of
+    // v are added up again too often (20000 tokens of 9 requests, rank 64: 148 us without the
+    // limit, 101 with it). One adapter of 5003 tokens, rank 64, 4096 x 14336, takes 97 us
+    // whether 8 or 64 are loaded (shared out among the adapters loaded: 95 and 122).
+    const int64_t blocks_n = (p.n + 255) / 256, shares = at_most((4096 + 12 * groups - 1) / (12 * groups), blocks_n);
+    const int64_t workgroups = at_most((kUpWorkgroups + groups - 1) / groups, slots * shares);
+    const dim3 grid((unsigned)groups, (unsigned)(workgroups + slots - 1));
+#define CALL(RS) hipLaunchKernelGGL((k_lora_up<RS>), grid, dim3(256), 0, st, p, blocks_n, (int)workgroups, (int)shares)
     FP8_LORA_BY_STEPS(CALL);
 #undef CALL
     return hipGetLastError();
