@@ -13,8 +13,8 @@
 // out, read and written once, and few ones the latency of two short launches (one
 // token 4 + 5 us). For few tokens the sums of v are split over parts of k.
 //
-// v c_e is kept as the sum of two bf16 numbers and multiplied in two products, so
-// that the only rounding that counts is the output's.
+// v c_e, fp32, is multiplied as the sum of three bf16 numbers of 8 bits each in three
+// products: no bit of it is lost.
 #include "block.hpp"
 #include "layer_device.hpp"
 
@@ -82,10 +82,10 @@ struct Unit {
     __device__ __forceinline__ int at(int c) const { return __shfl(token, c0 + (c < count ? c : 0), 64); }
 };
 
-// v = sum of its parts times the factor, as a high and a low bf16 number. (An Inf or
-// NaN is carried by the high part alone; a finite value that bf16 would round to Inf
-// is bf16's largest and the rest.)
-__device__ __forceinline__ void put_value(const Lora& p, int64_t t, int j, float c, uint16_t* hi, uint16_t* lo) {
+// v = sum of its parts times the factor, as a high, a middle and a low bf16 number, whose
+// sum it is. (An Inf or NaN is carried by the high part alone; a finite value that bf16
+// would round to Inf is bf16's largest and the rest.)
+__device__ __forceinline__ void put_value(const Lora& p, int64_t t, int j, float c, uint16_t (&out)[3]) {
     const float* src = p.ws + t * p.rank + j;
     const int64_t step = p.tokens * p.rank;
     float v = 0.0f;
@@ -102,8 +102,11 @@ __device__ __forceinline__ void put_value(const Lora& p, int64_t t, int j, float
     const bool finite = __builtin_isfinite(v);
     uint32_t h = f32_to_bf16(v);
     h -= finite && (h & 0x7fffu) == 0x7f80u ? 1u : 0u;
-    *hi = (uint16_t)h;
-    *lo = (uint16_t)(finite ? f32_to_bf16(v - __uint_as_float(h << 16)) : 0u);
+    const float rest = finite ? v - __uint_as_float(h << 16) : 0.0f;
+    const uint32_t mid = f32_to_bf16(rest);
+    out[0] = (uint16_t)h;
+    out[1] = (uint16_t)mid;
+    out[2] = (uint16_t)f32_to_bf16(rest - __uint_as_float(mid << 16));
 }
 
 // Orders this wavefront's LDS accesses on either side for the compiler (the
@@ -242,26 +245,36 @@ __global__ __launch_bounds__(kWaves * 64) void k_lora_down(Lora p) {
     });
 }
 
-// LDS of the second product. vs: 16 tokens' values of v, high and low parts, zeros
-// behind the rank. A wavefront's own 16-byte aligned part: its 64 rows of B (padded
-// to RS steps of 32), then, in their place, its sums (fp32, 16 tokens x 64
-// columns). Both pitches put 16 neighbouring rows on 16 different groups of banks.
+// LDS of the second product. A wavefront's own 16-byte aligned part: its 64 rows of B
+// (padded to RS steps of 32), then, in their place, its sums (fp32, 16 tokens x 64
+// columns). Both pitches put 16 neighbouring rows on 16 different groups of banks. In the
+// beginning 16 tokens' values of v stand there, three parts each, zeros behind the rank,
+// until every wavefront has its share of them in registers.
 template <int RS>
 struct UpLds {
     static constexpr int kPitch = RS * 32 + 8, kSums = 68;          // bf16 values, fp32 values
     static constexpr int kB = 64 * kPitch * 2, kS = kTile * kSums * 4;
-    uint16_t vs[2][kTile * kPitch];
     __attribute__((aligned(16))) uint8_t own[kWaves][kB > kS ? kB : kS];
 
-    __device__ __forceinline__ void fill(const Lora& p, const Unit& unit, int64_t t0) {
+    __device__ __forceinline__ void values(const Lora& p, const Unit& unit, int64_t t0, u32x4 (&v)[3][RS]) {
+        constexpr int kPart = kTile * kPitch;
+        static_assert(3 * kPart * 2 <= (int)sizeof(own), "the values of v stand in the wavefronts' parts");
+        uint16_t* vs = reinterpret_cast<uint16_t*>(own);
         const float c = p.scaling[unit.e];
         for (int i = threadIdx.x; i < kTile * (RS * 32); i += 256) {
             const int tok = i / (RS * 32), j = i % (RS * 32), token = unit.at(tok);
-            uint16_t hi = 0, lo = 0;
-            if (tok < unit.count && j < p.rank) put_value(p, t0 + token, j, c, &hi, &lo);
-            vs[0][tok * kPitch + j] = hi;
-            vs[1][tok * kPitch + j] = lo;
+            uint16_t part[3] = {0, 0, 0};
+            if (tok < unit.count && j < p.rank) put_value(p, t0 + token, j, c, part);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) vs[k * kPart + tok * kPitch + j] = part[k];
         }
+        __syncthreads();
+        const int q = (threadIdx.x & 63) >> 4, m = threadIdx.x & 15;
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int s = 0; s < RS; ++s) v[k][s] = *reinterpret_cast<const u32x4*>(&vs[k * kPart + m * kPitch + s * 32 + q * 8]);
+        __syncthreads();
     }
 };
 
@@ -274,7 +287,8 @@ struct UpLds {
 // 4096 x 14336: 22 -> 19 us).
 template <int RS>
 __device__ __forceinline__ void up_blocks(const Lora& p, int e, int64_t t0, const int (&t)[2], const bool (&live)[2],
-                                          UpLds<RS>& lds, int64_t nb, int64_t step, int64_t blocks_n) {
+                                          UpLds<RS>& lds, const u32x4 (&v)[3][RS], int64_t nb, int64_t step,
+                                          int64_t blocks_n) {
     using L = UpLds<RS>;
     constexpr int CH = RS * 4;                  // 16-byte chunks of a padded row of B
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, m = lane & 15;
@@ -316,9 +330,9 @@ __device__ __forceinline__ void up_blocks(const Lora& p, int e, int64_t t0, cons
 #pragma unroll
             for (int s = 0; s < RS; ++s) {
                 const u32x4 w = *reinterpret_cast<const u32x4*>(bl + (i * 16 + m) * L::kPitch + s * 32 + q * 8);
-                const int at = m * L::kPitch + s * 32 + q * 8;
-                hi = mfma(w, *reinterpret_cast<const u32x4*>(&lds.vs[0][at]), hi);
-                lo = mfma(w, *reinterpret_cast<const u32x4*>(&lds.vs[1][at]), lo);
+                hi = mfma(w, v[0][s], hi);
+                lo = mfma(w, v[1][s], lo);
+                lo = mfma(w, v[2][s], lo);
             }
             // (an infinite weight: the low parts, of either sign or 0, would make NaN of Inf)
 #pragma unroll
@@ -418,9 +432,9 @@ __global__ __launch_bounds__(256, RS == 1 ? 4 : RS == 2 ? 3 : 2) void k_lora_up(
         if (p.base != p.out) copy_blocks(p, t0, t, live, share, shares, blocks_n);
         return;
     }
-    lds.fill(p, unit, t0);
-    __syncthreads();
-    up_blocks<RS>(p, unit.e, t0, t, live, lds, share, shares, blocks_n);
+    u32x4 v[3][RS];
+    lds.values(p, unit, t0, v);
+    up_blocks<RS>(p, unit.e, t0, t, live, lds, v, share, shares, blocks_n);
 }
 
 // 16-row tiles of the rank of the first launch.

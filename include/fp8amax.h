@@ -733,8 +733,8 @@ fp8_status_t fp8_gemm_swiglu_backward(const uint8_t* a, fp8_format_t fa, int64_t
  * outside [0, adapters) for a token without an adapter, whose base is copied;
  * base, out: bf16 [tokens x n] (ldbase, ldout); base NULL for zeros. out may be
  * base itself (the same pointer and leading dimension), else outputs do not
- * overlap the inputs. fp32 sums; the rank-wide intermediate is kept to 16
- * significant bits, the output rounded once. Adapters of smaller rank are padded
+ * overlap the inputs. Sums and the rank-wide intermediate are fp32, the output is
+ * rounded once. Adapters of smaller rank are padded
  * with zeros. Any order of tokens is served; tokens of one adapter among 64
  * neighbours share its loads. No other token's or adapter's values enter a token's result,
  * and the same call gives the same bits, whatever other adapters are loaded; the

@@ -61,8 +61,8 @@ def swiglu_backward(da, g, u, da_tol):
 
 def lora(x, a, b, scaling, idx, base):
     """base + scaling_e (x A_e^T) B_e^T and its bound: v = x A^T as a matrix-core sum
-    (and up to 64 parts and 4 wavefronts added), v times the factor kept to 16 bits (2^-16 relative), the
-    second product as two sums."""
+    (and up to 16 parts and 4 wavefronts added), v times the factor rounded to fp32, the
+    second product as two sums, of up to 2 r products."""
     out = base.copy()
     tol = np.zeros_like(out)
     K, r = x.shape[1], a.shape[1]
@@ -72,9 +72,9 @@ def lora(x, a, b, scaling, idx, base):
             continue
         c = float(scaling[e])
         v = x[t] @ a[e].T
-        v_tol = 2 * (K + 80) * U * (np.abs(x[t]) @ np.abs(a[e]).T)
+        v_tol = 2 * (K + 20) * U * (np.abs(x[t]) @ np.abs(a[e]).T)
         out[t] += c * (v @ b[e].T)
-        w_tol = abs(c) * (v_tol + np.abs(v) * (2.0 ** -16 + 2 * U))
+        w_tol = abs(c) * (v_tol + np.abs(v) * 2 * U)
         tol[t] = w_tol @ np.abs(b[e]).T + 2 * (2 * r + 4) * U * ((abs(c) * np.abs(v) + w_tol) @ np.abs(b[e]).T)
         tol[t] += 2 * U * (np.abs(base[t]) + np.abs(out[t]))
     return out, tol

@@ -246,3 +246,21 @@ def test_bits_do_not_depend_on_the_adapters_loaded(fp8, tokens, k, n, rank):
         outs.append(out)
     for out in outs[1:]:
         assert torch.equal(out, outs[0])
+
+
+@pytest.mark.parametrize("tokens,n,rank", [(1, 64, 8), (40, 300, 24), (70, 264, 64), (600, 72, 128)])
+def test_rank_wide_values_keep_24_bits(fp8, tokens, n, rank):
+    """Two values of x A^T that differ in their 18th bit, subtracted by B: each sum of the
+    definition is exact in fp32, and so is the difference."""
+    k = 72
+    x = torch.zeros((tokens, k), device=DEV)
+    x[:, :3] = torch.tensor([1.0, 2.0 ** -9, 2.0 ** -18], device=DEV)
+    a, b = torch.zeros((1, rank, k), device=DEV), torch.zeros((1, n, rank), device=DEV)
+    a[0, 0, :3], a[0, rank - 1, :2] = 1.0, 1.0
+    b[0, :, 0], b[0, :, rank - 1] = 3.0, -3.0
+    out = torch.empty((tokens, n), dtype=torch.bfloat16, device=DEV)
+    say("adapters, 24 bits", tokens, n, rank)
+    fp8.fp8_lora_add(x.to(torch.bfloat16), a.to(torch.bfloat16), b.to(torch.bfloat16), torch.ones(1, device=DEV),
+                     torch.zeros(tokens, dtype=torch.int32, device=DEV), None, out, fp8.lora_workspace(tokens, rank))
+    torch.cuda.synchronize()
+    assert (out.float() == 3 * 2.0 ** -18).all(), out.float().unique()
