@@ -16,20 +16,35 @@
 namespace fp8amax {
 namespace {
 
-// sigma(g) = 1 / (1 + 2^(-g log2 e)): the exponent's rounding is an error of |g|
-// 2^-24 relative to the exponential, far below the outputs' 2^-9; 2^128 and more
-// count as infinite (sigma 0), which the reciprocal of Inf gives.
-__device__ __forceinline__ float sigma(float g) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
-}
-__device__ __forceinline__ float swiglu(float g, float u) { return g * sigma(g) * u; }
+// sigma(g) = 1 / (1 + t) and 1 - sigma(g) = t sigma(g), t = exp(-g), with a relative error
+// of 2^-20 at most for every g. t = 2^n exp(e): n = -g log2 e as rounded, and e = -g - n ln 2,
+// |e| < 2^-16, what that rounding lost (without it t's error grows with |g|, to 2^-17). The
+// sum is formed times 2^-24, so that its reciprocal is normal as long as t is finite: the
+// hardware's has no subnormal results, and sigma would vanish from t = 2^126. (A t of 2^128 and
+// more is infinite, and sigma 0. Past +-200, where sigma is 1 or 0, g counts as that: e stays
+// small. A NaN g gives any sigma; what it is multiplied with is NaN.)
+struct Sigma {
+    float sig, t, r;                                    // t 2^-24, sigma 2^24
+    __device__ __forceinline__ explicit Sigma(float g) {
+        constexpr float kDown = 5.9604644775390625e-8f; // 2^-24
+        const float c = __builtin_amdgcn_fmed3f(g, -200.0f, 200.0f), n = c * -1.44269504f;
+        const float e = fmaf(n, -0.693147182f, -c);
+        t = __builtin_amdgcn_exp2f(n) * fmaf(e, kDown, kDown);
+        r = __builtin_amdgcn_rcpf(t + kDown);
+        sig = r * kDown;
+    }
+    // (t is infinite only with sigma 0)
+    __device__ __forceinline__ float complement() const { return __builtin_fminf(t, 3.40282347e38f) * r; }
+};
+__device__ __forceinline__ float swiglu(float g, float u) { return g * Sigma(g).sig * u; }
 
 struct SwigluGrad {
     float dg, du, act;
 };
 __device__ __forceinline__ SwigluGrad swiglu_grad(float da, float g, float u) {
-    const float s = sigma(g), silu = g * s;
-    return {da * u * (s * fmaf(g, 1.0f - s, 1.0f)), da * silu, silu * u};
+    const Sigma s(g);
+    const float silu = g * s.sig;
+    return {da * u * (s.sig * fmaf(g, s.complement(), 1.0f)), da * silu, silu * u};
 }
 
 typedef float v4f __attribute__((ext_vector_type(4)));

@@ -29,11 +29,16 @@ def product(qa, fa, sa, qb, fb, sb):
     return y, 2 * (k + 2) * U * mag + 2 * U * np.abs(y)
 
 
+def exp_rel(g):
+    """t = exp(-g) in fp32 as 2^n exp(e): the exponential 2 U, 1 + e and its product with it
+    2 U, the constant of n ln 2 off by 1.9e-9: |n| 1.9e-9 < |g| U / 16."""
+    return (4 + np.abs(g) / 16) * U
+
+
 def sigma_rel(g):
-    """sigma(g) = 1 / (1 + 2^(-g log2 e)) in fp32: the exponent's product and its
-    constant are off by 2 U |g log2 e| (|g| 2 U relative to the exponential), the
-    exponential by 2 U, the sum by U, the reciprocal by 2 U."""
-    return (2 * np.abs(g) + 6) * U
+    """sigma(g) = 1 / (1 + t): t's error in the share that t has of the sum, the sum U, the
+    reciprocal 2 U."""
+    return exp_rel(g) * sigmoid(-g) + 3 * U
 
 
 def swiglu(g, u, g_tol, u_tol):
@@ -49,7 +54,8 @@ def swiglu_backward(da, g, u, da_tol):
     silu = g * s
     f = s * (1 + g * c)
     rel = sigma_rel(g)
-    f_tol = np.abs(f) * (rel + 2 * U) + s * (np.abs(g) * (s * rel + 2 * U) + U * (1 + np.abs(g * c)))
+    c_tol = c * (exp_rel(g) * s + 4 * U)        # 1 - sigma = t sigma: what t's error leaves, sigma's other 3 U, the product
+    f_tol = np.abs(f) * (rel + 2 * U) + s * (np.abs(g) * c_tol + U * (1 + np.abs(g * c)))
     dg, du, a = da * u * f, da * silu, silu * u
     far = np.abs(da) + da_tol
     tiny = TINY * (1 + far) * (1 + np.abs(g)) ** 2 * (1 + np.abs(u))

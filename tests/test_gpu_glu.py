@@ -260,3 +260,68 @@ def test_backward_of_many_tiles(fp8):
 def test_forward_of_few_rows_and_many_columns(fp8, m, k, inter, fa, fb, am, bm, want_h, pad):
     """A decoding batch at the widths that are served: as many workgroups as CUs and more."""
     test_forward(fp8, m, k, inter, fa, fb, am, bm, want_h, pad)
+
+
+# What the epilogue makes of exact sums: a and b have a single column that is not 0, so
+# that a sum is a product of factors, any fp32 number. The other factor of an output is
+# then set such that the exact output lies 32 or 48 U (U = 2^-24) beside the middle
+# between two bf16 numbers, and the output has to be the nearer one: an error of more
+# than that in sigma, 1 - sigma or a product gives another.
+def unit_codes(rows, k):
+    q = torch.zeros((rows, k), dtype=torch.uint8, device=DEV)
+    q[:, 0] = 0x38                              # 1 in e4m3
+    return q
+
+
+def beside_middle(rng, factor, shift):
+    """(other factor in fp32, the nearest bf16 of the product) for exact factors."""
+    at = (np.floor(rng.random(factor.shape) * 128) + 0.5) / 128 + 1
+    side = np.where(rng.random(factor.shape) < 0.5, -1.0, 1.0)
+    other = (at * (1 + side * shift * block.U) / np.abs(factor)).astype(np.float32)
+    exact = other.astype(np.float64) * factor
+    assert (np.abs(np.abs(exact) - at) >= (shift - 2) * block.U * at).all()
+    return other, np.sign(factor) * (at + side / 256)
+
+
+def check_nearest(got, want, g, what):
+    bad = got != want
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.size} not the nearest, the first at gate "
+                           f"{np.broadcast_to(g, bad.shape)[bad][0]!r}: {got[bad][0]!r} for {want[bad][0]!r}")
+
+
+@pytest.mark.parametrize("m,k,inter", [(3, 16, 1000), (3, 16, 4096), (70, 16, 4096), (200, 16, 4608), (600, 256, 4096)])
+def test_sigma_of_exact_gates(fp8, m, k, inter):
+    """act = g sigma(g) u of gates from -88.7, where exp(-g) is just finite, to 88. sigma is
+    off by 15 U at most: exp(-g) 2 U by the exponential, 2 by its two products and 4 by ln
+    2's constant, the sum 1, the reciprocal 2, 4 where sigma is subnormal; then two products."""
+    rng = np.random.default_rng(m + inter)
+    g = np.concatenate([rng.uniform(-88.72, -87.3, inter // 4), rng.uniform(-88, 88, inter - inter // 4)]).astype(np.float32)
+    u, want = beside_middle(rng, g.astype(np.float64) * layer.sigmoid(g.astype(np.float64)), 32)
+    one = torch.ones(1, device=DEV)
+    act = torch.empty((m, inter), dtype=torch.bfloat16, device=DEV)
+    say("gated product, exact gates", m, k, inter)
+    fp8.fp8_gemm_swiglu(unit_codes(m, k), 0, unit_codes(2 * inter, k), 0, one, 0, dev_f32(np.concatenate([g, u])), 1, act)
+    torch.cuda.synchronize()
+    check_nearest(bf16_of(act), np.broadcast_to(want, (m, inter)), g, "act")
+
+
+@pytest.mark.parametrize("m,k,inter", [(3, 16, 4096), (300, 16, 6000), (600, 256, 5632)])
+def test_sigma_of_exact_gates_backward(fp8, m, k, inter):
+    """d(gate) = da u sigma (1 + g (1 - sigma)) and d(up) = da g sigma of gates that bf16
+    holds. Where 1 + g (1 - sigma) is no small difference (gates past -3 or -0.6) it is off by
+    1.5 (4 + 8 sigma) U + U, sigma by 15 U, and three products: 26 U at most."""
+    rng = np.random.default_rng(m + inter)
+    h = layer.values(workloads.bf16_bits(np.concatenate(
+        [rng.uniform(-88.5, -87.4, inter // 8), rng.uniform(-88, -3.1, inter // 2),
+         rng.uniform(-0.59, 88, inter - inter // 8 - inter // 2)]).astype(np.float32)))
+    up = layer.values(workloads.bf16_bits(rng.uniform(0.5, 2, inter).astype(np.float32)))
+    hd = torch.from_numpy(np.concatenate([h, up])).to(DEV).to(torch.bfloat16).repeat(m, 1)
+    s, c = layer.sigmoid(h), layer.sigmoid(-h)
+    dh = torch.empty((m, 2 * inter), dtype=torch.bfloat16, device=DEV)
+    one = torch.ones(1, device=DEV)
+    for what, factor, part in (("d(gate)", up * s * (1 + h * c), slice(0, inter)), ("d(up)", h * s, slice(inter, None))):
+        da, want = beside_middle(rng, factor, 48)
+        say("gated product's gradient, exact gates", m, k, inter, what)
+        fp8.fp8_gemm_swiglu_backward(unit_codes(m, k), 0, unit_codes(inter, k), 0, one, 0, dev_f32(da), 1, hd, dh)
+        torch.cuda.synchronize()
+        check_nearest(bf16_of(dh)[:, part], np.broadcast_to(want, (m, inter)), h, what)
