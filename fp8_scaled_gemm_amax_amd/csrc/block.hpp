@@ -45,6 +45,19 @@ struct GluBwd {
     int64_t ldact;
 };
 
+// Whether the kernel for a few rows takes a call of m rows (else tiles of 64 rows do). Up to
+// 16 rows it does; with 17 to 32 its loads of a's rows weigh as much as the weights, and tiles
+// of 64 x 64 outputs are faster where they occupy a good part of the CUs once. Few rows' kernel
+// and tiles (32 rows, us on the device): 2048 x 1408 6.1 and 9.4, 4096 x 4096 (64 tiles) 11.0
+// and 14.2, x 6144 (96) 15.8 and 14.2, x 11008 (172) 24 and 18.6, x 14336 (224) 31.8 and 29.7,
+// 8192 x 28672 (448, so a second round of tiles) 91 and 94; 17 rows 5.6 and 9.7, 11.0 and 14.2,
+// 13.8 and 14.4, 24.2 and 18.3, 30.0 and 29.7, 83 and 94; 33 rows of 4096 x 14336 42 and 30.
+constexpr int kFewRows = 32;
+inline bool glu_few_rows(int64_t m, int64_t inter, int64_t cus) {
+    const int64_t tiles = (inter + 63) / 64;
+    return m <= 16 || (m <= kFewRows && (tiles * 8 < cus * 3 || tiles > cus));
+}
+
 hipError_t launch_gemm_swiglu(const GluFwd& p, int fa, int fb, hipStream_t st);
 hipError_t launch_gemm_swiglu_backward(const GluBwd& p, int fa, int fb, hipStream_t st);
 

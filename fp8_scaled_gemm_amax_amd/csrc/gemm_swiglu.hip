@@ -65,7 +65,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // --------------------------------------------------------------- few rows --
-// Up to kFewRows rows of a (decoding): bound by the weights' bytes, each read once. A
+// Up to kFewRows rows of a (decoding; glu_few_rows): bound by the weights' bytes, each read once. A
 // workgroup has 16 columns of act: its 16 gate rows and 16 up rows of b against tiles
 // of 16 rows of a (16x16x128 products), its wavefronts taking K in turn in blocks of
 // 256 bytes, their sums added in LDS. Weights are loaded in the order of the rows (16
@@ -73,7 +73,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // through LDS of the wavefront's own; the next block is on its way while one is
 // multiplied. One row, 4096 x 14336: 24 us, 5 TB/s (8192 x 28672: 73 us, 6.4 TB/s; what
 // a short call loses is the ramp-up and the drain).
-constexpr int kFewRows = 32, kFewBlock = 256;
+constexpr int kFewBlock = 256;
 
 template <int FA, int FB, int NT, int W>
 __global__ __launch_bounds__(W * 64) void k_glu_few(GluFwd p) {
@@ -853,9 +853,7 @@ hipError_t glu_typed(const GluFwd& p, hipStream_t st) {
         else hipLaunchKernelGGL((k_glu_persist<FA, FB, false>), grid, dim3(256), 0, st, p);
         return hipGetLastError();
     }
-    // (32 rows, 2048 x 1408: 6.4 us, 9.0 in tiles of 64 rows; 4096 x 14336: 32.6 and 29.4;
-    // 33 rows 42 and 30)
-    if (p.m <= kFewRows) {
+    if (glu_few_rows(p.m, p.inter, current_device_props().cus)) {
         const dim3 grid((unsigned)((p.inter + 15) / 16));
         // Fewer workgroups than CUs: eight wavefronts each, else four. One row, 2048 x 1408
         // (88 workgroups) 4.4 and 4.9 us; 32 rows, 4096 x 4096 (256) 12.7 and 11.3.
