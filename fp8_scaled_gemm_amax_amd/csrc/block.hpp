@@ -58,6 +58,19 @@ inline bool glu_few_rows(int64_t m, int64_t inter, int64_t cus) {
     return m <= 16 || (m <= kFewRows && (tiles * 8 < cus * 3 || tiles > cus));
 }
 
+// Large tiles where those of a quarter of their size would take a CU more than one.
+// On 256 CUs: product of 512 x 4096 x 7168 (112 large tiles) 41 us, 45 in 128 x 128 tiles; of
+// 256 x 4096 x 8192 (64) 41 and 24; gradient of 2048 x 4096 x 4096 (128) 50 and 58, of
+// 1024 x 4096 x 4096 (64) 46 and 29.
+inline bool glu_large_tiles(int64_t large, int64_t cus) { return large * 4 > cus; }
+
+// Tiles of 64 rows where those of 128 would leave half of the CUs idle, or half of
+// each tile empty. On 256 CUs, with them and without: product of 300 x 2048 x 1408 10.2 and
+// 13.7 us, 64 x 4096 x 14336 30 and 32, gradient of 1001 x 2048 x 1408 13.5 and 19.2. Past the
+// limit: product of 777 x 2048 x 1408 (154 tiles of 128) 18.8 and 14.9, gradient of
+// 200 x 4096 x 14336 (224) 35 and 29.
+inline bool glu_tiles_of_64_rows(int64_t m, int64_t tiles128, int64_t cus) { return m <= 64 || tiles128 * 2 <= cus; }
+
 hipError_t launch_gemm_swiglu(const GluFwd& p, int fa, int fb, hipStream_t st);
 hipError_t launch_gemm_swiglu_backward(const GluBwd& p, int fa, int fb, hipStream_t st);
 

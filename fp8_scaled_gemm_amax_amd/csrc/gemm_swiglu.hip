@@ -206,7 +206,7 @@ __global__ __launch_bounds__(W * 64) void k_glu_few(GluFwd p) {
 // Rows past the operand's last one are loaded as that one and not stored; the step that
 // k ends in comes through registers, zeros behind k.
 //
-// MB: blocks of 32 rows a wavefront, 2 or, for tiles of 64 rows, 1 (mid_rows64).
+// MB: blocks of 32 rows a wavefront, 2 or, for tiles of 64 rows, 1 (glu_tiles_of_64_rows).
 template <int MB>
 struct Mid {
     static constexpr int kStages = 4, kA = MB * 64 * 128, kStage = kA + 128 * 128;
@@ -832,33 +832,21 @@ static int64_t persistent_grid(int64_t tiles) {
     const int64_t cus = current_device_props().cus, most = cus >= 8 ? cus / 8 * 8 : cus;
     return tiles < most ? tiles : most;
 }
-// Large tiles where those of a quarter of their size would take a CU more than one.
-// Product of 512 x 4096 x 7168 (112 large tiles) 41 us, 45 in 128 x 128 tiles; of
-// 256 x 4096 x 8192 (64) 41 and 24; gradient of 2048 x 4096 x 4096 (128) 50 and 58, of
-// 1024 x 4096 x 4096 (64) 46 and 29.
-constexpr int64_t kMidLarge = 64;
-// Tiles of 64 rows where those of 128 would leave half of the CUs idle, or half of
-// each tile empty. With them and without: product of 300 x 2048 x 1408 10.2 and 13.7 us,
-// 64 x 4096 x 14336 30 and 32, gradient of 1001 x 2048 x 1408 13.5 and 19.2. Past the limit:
-// product of 777 x 2048 x 1408 (154 tiles of 128) 18.8 and 14.9, gradient of
-// 200 x 4096 x 14336 (224) 35 and 29.
-static bool mid_rows64(int64_t m, int64_t tiles128) { return m <= 64 || tiles128 <= 128; }
-
 template <int FA, int FB>
 hipError_t glu_typed(const GluFwd& p, hipStream_t st) {
-    const int64_t large = (p.m + 255) / 256 * ((p.inter + 127) / 128);
-    if (p.k > 0 && p.k % 256 == 0 && p.m >= 256 && p.inter >= 128 && large > kMidLarge) {
+    const int64_t cus = current_device_props().cus, large = (p.m + 255) / 256 * ((p.inter + 127) / 128);
+    if (p.k > 0 && p.k % 256 == 0 && p.m >= 256 && p.inter >= 128 && glu_large_tiles(large, cus)) {
         const dim3 grid((unsigned)persistent_grid(large));
         if (p.h) hipLaunchKernelGGL((k_glu_persist<FA, FB, true>), grid, dim3(256), 0, st, p);
         else hipLaunchKernelGGL((k_glu_persist<FA, FB, false>), grid, dim3(256), 0, st, p);
         return hipGetLastError();
     }
-    if (glu_few_rows(p.m, p.inter, current_device_props().cus)) {
+    if (glu_few_rows(p.m, p.inter, cus)) {
         const dim3 grid((unsigned)((p.inter + 15) / 16));
         // Fewer workgroups than CUs: eight wavefronts each, else four. One row, 2048 x 1408
         // (88 workgroups) 4.4 and 4.9 us; 32 rows, 4096 x 4096 (256) 12.7 and 11.3.
 #define CALL(NT, W) hipLaunchKernelGGL((k_glu_few<FA, FB, NT, W>), grid, dim3(W * 64), 0, st, p)
-        if (grid.x < 256) {
+        if (grid.x < cus) {
             if (p.m <= 16) CALL(1, 8);
             else CALL(2, 8);
         } else {
@@ -869,7 +857,7 @@ hipError_t glu_typed(const GluFwd& p, hipStream_t st) {
         return hipGetLastError();
     }
     const int64_t tiles_n = (p.inter + 63) / 64, tiles = (p.m + 127) / 128 * tiles_n;
-    if (mid_rows64(p.m, tiles)) {
+    if (glu_tiles_of_64_rows(p.m, tiles, cus)) {
         const dim3 grid((unsigned)((p.m + 63) / 64 * tiles_n));
         hipLaunchKernelGGL((k_glu_mid<FA, FB, 1>), grid, dim3(256), 0, st, p);
     } else {
@@ -880,15 +868,15 @@ hipError_t glu_typed(const GluFwd& p, hipStream_t st) {
 
 template <int FA, int FB>
 hipError_t glu_grad_typed(const GluBwd& p, hipStream_t st) {
-    const int64_t large = (p.m + 255) / 256 * ((p.inter + 255) / 256);
-    if (p.k > 0 && p.k % 256 == 0 && p.m >= 256 && p.inter >= 256 && large > kMidLarge) {
+    const int64_t cus = current_device_props().cus, large = (p.m + 255) / 256 * ((p.inter + 255) / 256);
+    if (p.k > 0 && p.k % 256 == 0 && p.m >= 256 && p.inter >= 256 && glu_large_tiles(large, cus)) {
         const dim3 grid((unsigned)persistent_grid(large));
         if (p.act) hipLaunchKernelGGL((k_glu_grad_persist<FA, FB, true>), grid, dim3(256), 0, st, p);
         else hipLaunchKernelGGL((k_glu_grad_persist<FA, FB, false>), grid, dim3(256), 0, st, p);
         return hipGetLastError();
     }
     const int64_t tiles_n = (p.inter + 127) / 128, tiles = (p.m + 127) / 128 * tiles_n;
-    if (mid_rows64(p.m, tiles)) {
+    if (glu_tiles_of_64_rows(p.m, tiles, cus)) {
         const dim3 grid((unsigned)((p.m + 63) / 64 * tiles_n));
         hipLaunchKernelGGL((k_glu_grad_mid<FA, FB, 1>), grid, dim3(256), 0, st, p);
     } else {

@@ -27,7 +27,6 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 constexpr int kTile = 16;                       // tokens of a product
 constexpr int kStepK = 64;                      // columns of x of one step of a wavefront
 constexpr int kWaves = 4, kGroup = 64;          // wavefronts of a workgroup, tokens that it looks at
-constexpr int64_t kUpWorkgroups = 2560;         // of the second launch
 
 __device__ __forceinline__ v4f mfma(u32x4 a, u32x4 b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
@@ -480,15 +479,16 @@ hipError_t launch_lora_add(const Lora& call, hipStream_t st) {
 #undef CALL
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // Ten workgroups a CU in all where every unit has work for so many: those of a group of
-    // tokens are shared out among its units, whatever is loaded. (128 tokens of as many
-    // requests, rank 16, 4096 x 14336, 64 adapters: 16 a CU 18 us, 10 of them 15.) A unit has
-    // no more than the rest of the rule gives it with 12 units a group: beyond that the values of
-    // v are added up again too often (20000 tokens of 9 requests, rank 64: 148 us without the
-    // limit, 101 with it). One adapter of 5003 tokens, rank 64, 4096 x 14336, takes 97 us
-    // whether 8 or 64 are loaded (shared out among the adapters loaded: 95 and 122).
-    const int64_t blocks_n = (p.n + 255) / 256, shares = at_most((4096 + 12 * groups - 1) / (12 * groups), blocks_n);
-    const int64_t workgroups = at_most((kUpWorkgroups + groups - 1) / groups, slots * shares);
+    // About ten workgroups a CU, those of a group of tokens shared out among the units that it
+    // has, whatever is loaded. (128 tokens of as many requests, rank 16, 4096 x 14336, 64
+    // adapters: 16 a CU 18 us, 10 of them 15. 5003 tokens of one request, rank 64: 97 us with 8
+    // or with 64 adapters loaded; shared out among those, 95 and 122.) A unit has at most
+    // what it would have of 16 a CU in a group of 12 units: with more of them the values of v are
+    // added up too often (20000 tokens of 9 requests, rank 64, 4096 x 4096: 148 us without this
+    // limit, 101 with it).
+    const int64_t blocks_n = (p.n + 255) / 256, cus = current_device_props().cus;
+    const int64_t shares = at_most((16 * cus + 12 * groups - 1) / (12 * groups), blocks_n);
+    const int64_t workgroups = at_most((10 * cus + groups - 1) / groups, slots * shares);
     const dim3 grid((unsigned)groups, (unsigned)(workgroups + slots - 1));
 #define CALL(RS) hipLaunchKernelGGL((k_lora_up<RS>), grid, dim3(256), 0, st, p, blocks_n, (int)workgroups, (int)shares)
     FP8_LORA_BY_STEPS(CALL);

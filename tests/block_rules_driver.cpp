@@ -20,7 +20,22 @@ static void few(int64_t m, int64_t inter, bool want) {
     }
 }
 
+static void tiles(const char* rule, bool (*choose)(int64_t, int64_t), int64_t count, bool want) {
+    for (int64_t cus : {256, 64}) {
+        if (choose(count * cus / 256, cus) == want) continue;
+        ++bad;
+        std::fprintf(stderr, "%s, %lld tiles on %lld CUs: not %d\n", rule, (long long)(count * cus / 256), (long long)cus, want);
+    }
+}
+
 int main() {
+    const auto rows64 = [](int64_t t, int64_t cus) { return glu_tiles_of_64_rows(65, t, cus); };
+    for (int64_t t : {0, 4, 64}) tiles("large tiles", glu_large_tiles, t, false);
+    for (int64_t t : {68, 112, 128, 100000}) tiles("large tiles", glu_large_tiles, t, true);
+    for (int64_t t : {4, 66, 88, 128}) tiles("tiles of 64 rows", rows64, t, true);
+    for (int64_t t : {132, 154, 224, 100000}) tiles("tiles of 64 rows", rows64, t, false);
+    for (int64_t t : {1, 256, 100000})
+        if (!glu_tiles_of_64_rows(64, t, 256)) ++bad;
     for (int64_t inter : {4, 1408, 4096, 6144, 11008, 14336, 28672, 100000}) {
         for (int64_t m : {1, 2, 16}) few(m, inter, true);
         for (int64_t m : {33, 64, 1000}) few(m, inter, false);
