@@ -12,6 +12,7 @@
 // and SwiGLU needs no exchange.
 #include "block.hpp"
 #include "gemm_device.hpp"
+#include "layer_device.hpp"
 
 namespace fp8amax {
 namespace {
@@ -49,20 +50,8 @@ __device__ __forceinline__ SwigluGrad swiglu_grad(float da, float g, float u) {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-// Eight columns of a row, at any alignment: a base that is uniform over the wavefront
-// and the lane's offset in bytes. Nontemporal both ways: h, read once, would push the
-// operand panels out of L2 (gradient at 8192 x 4096 x 14336: 519 us with ordinary
-// loads, 484 with these).
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-__device__ __forceinline__ void store8(uint16_t* base, uint32_t bytes, u32x4 v) {
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(reinterpret_cast<char*>(base) + bytes));
-}
-__device__ __forceinline__ u32x4 load8(const uint16_t* base, uint32_t bytes) {
-    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(reinterpret_cast<const char*>(base) + bytes));
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2bf));
-}
+// h, act and dh pass the caches (load8, store8): h, read once, would push the operand
+// panels out of L2 (gradient at 8192 x 4096 x 14336: 519 us with ordinary loads, 484 so).
 
 // --------------------------------------------------------------- few rows --
 // Up to kFewRows rows of a (decoding; glu_few_rows): bound by the weights' bytes, each read once. A
@@ -548,10 +537,7 @@ __device__ __forceinline__ void first_steps(uint8_t* smem, v8i (&f0)[8], const u
 
 // Four rows of one column -> 8 bytes of bf16.
 __device__ __forceinline__ uint2 pack_rows(float a, float b, float c, float d) {
-    uint2 w;
-    w.x = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2bf));
-    w.y = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{c, d}), v2bf));
-    return w;
+    return make_uint2(pack2(a, b), pack2(c, d));
 }
 // Four 16-byte units of a staged block (4 rows x 8 columns) -> row r of the four.
 __device__ __forceinline__ u32x4 unit_row(const u32x4 (&un)[4], int r) {
@@ -761,10 +747,10 @@ __device__ __forceinline__ void glu_grad_epilogue(uint8_t* smem, v16f (&acc)[4][
             for (int e = 0; e < 4; ++e) {
                 const SwigluGrad lo = swiglu_grad(da[2 * e][j], bf16_lo(wg[e]), bf16_lo(wu[e]));
                 const SwigluGrad hi = swiglu_grad(da[2 * e + 1][j], bf16_hi(wg[e]), bf16_hi(wu[e]));
-                og[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo.dg, hi.dg}), v2bf));
-                ou[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo.du, hi.du}), v2bf));
+                og[e] = pack2(lo.dg, hi.dg);
+                ou[e] = pack2(lo.du, hi.du);
                 if constexpr (ACT)
-                    oa[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo.act, hi.act}), v2bf));
+                    oa[e] = pack2(lo.act, hi.act);
             }
             uint16_t* dst = p.dh + (wrow0 + 8 * n + j) * p.lddh + wcol0;
             store8(dst, od, og);

@@ -261,6 +261,15 @@ __device__ __forceinline__ void store_loose(void* base, uint32_t bytes, V v) {
     static_assert(alignof(Loose<V, A>) == A && sizeof(Loose<V, A>) == sizeof(V), "no more alignment than the layout has");
     at<Loose<V, A>>(base, bytes)->v = v;
 }
+// Eight values at any alignment, past the caches: what is met once leaves the place to
+// what is read again.
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+__device__ __forceinline__ u32x4 load8(const uint16_t* base, uint32_t bytes) {
+    return __builtin_nontemporal_load(at<u32x4_a2>(base, bytes));
+}
+__device__ __forceinline__ void store8(uint16_t* base, uint32_t bytes, u32x4 v) {
+    __builtin_nontemporal_store(v, at<u32x4_a2>(base, bytes));
+}
 template <bool LOOSE>
 __device__ __forceinline__ uint4 load_chunk(const uint16_t* row, uint32_t ch, uint32_t n) {
     if constexpr (!LOOSE) return load_stream(at<uint4>(row, ch * 16));

@@ -31,17 +31,6 @@ constexpr int kWaves = 4, kGroup = 64;          // wavefronts of a workgroup, to
 __device__ __forceinline__ v4f mfma(u32x4 a, u32x4 b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
-// Eight columns of base or out, at any alignment: a pointer that is uniform over the
-// wavefront and the lane's offset in bytes. Nontemporal: each is met once, and the
-// adapters' weights keep their place in the caches.
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-__device__ __forceinline__ u32x4 load8(const uint16_t* base, uint32_t bytes) {
-    return __builtin_nontemporal_load(at<u32x4_a2>(base, bytes));
-}
-__device__ __forceinline__ void store8(uint16_t* base, uint32_t bytes, u32x4 v) {
-    __builtin_nontemporal_store(v, at<u32x4_a2>(base, bytes));
-}
-
 // Up to 16 tokens of one adapter out of a group of 64: the slot-th such unit (by its
 // first token), an adapter of more tokens has several. Tokens without an adapter are
 // units too, those of e = p.adapters. Lane r holds the place in the group of the
