@@ -7,8 +7,8 @@
 //
 // A workgroup takes up to 16 tokens of one adapter out of 64, wherever they stand, so
 // that the adapter's weights are read once for them, in whatever order the requests'
-// tokens come: 5003 tokens of 9 requests, rank 16, 4096 x 14336, take 16 + 72 us, and
-// 23 + 144 if each is another request's of 16 adapters. (16 or 32 neighbours a workgroup, one
+// tokens come: 5003 tokens of 9 requests, rank 16, 4096 x 14336, take 16 + 70 us, and
+// 23 + 114 if each is another request's of 16 adapters. (16 or 32 neighbours a workgroup, one
 // adapter after the other: 20 + 86 and 145 + 532.) What bounds many tokens is base and
 // out, read and written once, and few ones the latency of two short launches (one
 // token 4 + 5 us). For few tokens the sums of v are split over parts of k.
@@ -468,16 +468,16 @@ hipError_t launch_lora_add(const Lora& call, hipStream_t st) {
 #undef CALL
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // About ten workgroups a CU, those of a group of tokens shared out among the units that it
-    // has, whatever is loaded. (128 tokens of as many requests, rank 16, 4096 x 14336, 64
-    // adapters: 16 a CU 18 us, 10 of them 15. 5003 tokens of one request, rank 64: 97 us with 8
-    // or with 64 adapters loaded; shared out among those, 95 and 122.) A unit has at most
-    // what it would have of 16 a CU in a group of 12 units: with more of them the values of v are
-    // added up too often (20000 tokens of 9 requests, rank 64, 4096 x 4096: 148 us without this
-    // limit, 101 with it).
+    // About eleven workgroups a CU, those of a group of tokens shared out among the units that
+    // it has, whatever is loaded. (128 tokens of as many requests, rank 16, 4096 x 14336, 64
+    // adapters: 16 a CU 18 us, 11 of them 16. 5003 of as many of 16 adapters, rank 128: 10 a CU
+    // 567, 11 of them 533. 5003 of one request, rank 64: 97 with 8 or with 64 adapters loaded;
+    // shared out among those, 95 and 122.) A unit has at most what it would have of 16 a CU
+    // in a group of 12 units: with more of them the values of v are added up too often (20000
+    // tokens of 9 requests, rank 64, 4096 x 4096: 148 us without this limit, 101 with it).
     const int64_t blocks_n = (p.n + 255) / 256, cus = current_device_props().cus;
     const int64_t shares = at_most((16 * cus + 12 * groups - 1) / (12 * groups), blocks_n);
-    const int64_t workgroups = at_most((10 * cus + groups - 1) / groups, slots * shares);
+    const int64_t workgroups = at_most((11 * cus + groups - 1) / groups, slots * shares);
     const dim3 grid((unsigned)groups, (unsigned)(workgroups + slots - 1));
 #define CALL(RS) hipLaunchKernelGGL((k_lora_up<RS>), grid, dim3(256), 0, st, p, blocks_n, (int)workgroups, (int)shares)
     FP8_LORA_BY_STEPS(CALL);
