@@ -264,3 +264,24 @@ def test_rank_wide_values_keep_24_bits(fp8, tokens, n, rank):
                      torch.zeros(tokens, dtype=torch.int32, device=DEV), None, out, fp8.lora_workspace(tokens, rank))
     torch.cuda.synchronize()
     assert (out.float() == 3 * 2.0 ** -18).all(), out.float().unique()
+
+
+@pytest.mark.parametrize("tokens", [1, 3, 63, 64, 65, 130, 520, 2000, 5003])
+@pytest.mark.parametrize("E", [1, 5, 64])
+def test_every_block_of_columns_is_reached(fp8, tokens, E):
+    """However a group's workgroups are shared out among its adapters: with x of 1 in one
+    column, A of 1 and B of 1 for the token's adapter number, every output is that number."""
+    k, rank = 8, 8
+    x = torch.ones((tokens, k), dtype=torch.bfloat16, device=DEV)
+    a = torch.zeros((E, rank, k), dtype=torch.bfloat16, device=DEV)
+    a[:, 2, 5] = 1
+    for how, ids in (("each", torch.arange(tokens, device=DEV) * 7 % (E + 1) - 1), ("runs", torch.arange(tokens, device=DEV) // 37 % E),
+                     ("one", torch.full((tokens,), E - 1, device=DEV))):
+        for n in (24, 256, 2000, 14336):
+            b = torch.zeros((E, n, rank), dtype=torch.bfloat16, device=DEV)
+            b[:, :, 2] = torch.arange(1, E + 1, device=DEV)[:, None]
+            out = torch.full((tokens, n), float("nan"), dtype=torch.bfloat16, device=DEV)
+            say("adapters, blocks of columns", tokens, E, how, n)
+            fp8.fp8_lora_add(x, a, b, torch.ones(E, device=DEV), ids.to(torch.int32), None, out, fp8.lora_workspace(tokens, rank))
+            torch.cuda.synchronize()
+            assert torch.equal(out, (ids + 1).to(torch.bfloat16)[:, None].expand(tokens, n)), (how, n)
