@@ -482,8 +482,8 @@ __global__ __launch_bounds__(256) void k_glu_grad_mid(GluBwd p) {
 // past the last row (column) are shifted back to end there (there are enough of both
 // for a tile); what the tile before computes too is stored twice, the same bits.
 // k % 256 == 0. 8192 x 4096 x 14336: product with h 735-760 us (2.6 PFLOP/s, matrix
-// cores busy 70% at the 1.66 GHz that power allows; without its stores 692), gradient
-// with act 472-484 us (without h, dh and act 356: their 1.2 GB are what bounds it).
+// cores busy 71% at the 1.67 GHz that power allows; without h 690), gradient
+// with act 480-494 us (without h, dh and act 356: their 1.2 GB are what bounds it).
 //
 // The steps of one tile: sums of the tile at (at, bt) over nk steps; its last two
 // load the first two of the tile at (nat, nbt).
