@@ -51,7 +51,8 @@ struct GluBwd {
 // and tiles (32 rows, us on the device): 2048 x 1408 6.1 and 9.4, 4096 x 4096 (64 tiles) 11.0
 // and 14.2, x 6144 (96) 15.8 and 14.2, x 11008 (172) 24 and 18.6, x 14336 (224) 31.8 and 29.7,
 // 8192 x 28672 (448, so a second round of tiles) 91 and 94; 17 rows 5.6 and 9.7, 11.0 and 14.2,
-// 13.8 and 14.4, 24.2 and 18.3, 30.0 and 29.7, 83 and 94; 33 rows of 4096 x 14336 42 and 30.
+// 13.8 and 14.4, 24.2 and 18.3, 30.0 and 29.7, 83 and 94; 16 rows 4.9 and 9.0, 10.3 and 14.0,
+// 12.6 and 14.0, 19.4 and 17.7, 29.3 and 29.1, 75 and 92; 33 rows of 4096 x 14336 42 and 30.
 constexpr int kFewRows = 32;
 inline bool glu_few_rows(int64_t m, int64_t inter, int64_t cus) {
     const int64_t tiles = (inter + 63) / 64;

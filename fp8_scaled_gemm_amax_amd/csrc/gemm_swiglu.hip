@@ -18,7 +18,8 @@ namespace fp8amax {
 namespace {
 
 // sigma(g) = 1 / (1 + t) and 1 - sigma(g) = t sigma(g), t = exp(-g), with a relative error
-// of 2^-20 at most for every g. t = 2^n exp(e): n = -g log2 e as rounded, and e = -g - n ln 2,
+// of 2^-20 at most for every g (1 - sigma as long as t 2^-24 is normal, g up to 70; what is
+// less adds nothing to the 1 that it is added to). t = 2^n exp(e): n = -g log2 e as rounded, and e = -g - n ln 2,
 // |e| < 2^-16, what that rounding lost (without it t's error grows with |g|, to 2^-17). The
 // sum is formed times 2^-24, so that its reciprocal is normal as long as t is finite: the
 // hardware's has no subnormal results, and sigma would vanish from t = 2^126. (A t of 2^128 and
