@@ -693,8 +693,9 @@ fp8_status_t fp8_mx_add_norm_backward(const uint16_t* dsum, int64_t lddsum, cons
  * the inter up rows (the b of an fp8_gemm_scaled with n = 2 inter); factors as
  * fp8_gemm_scaled (b_scale_inv [2 inter] with FP8_SCALE_VECTOR). act: bf16 [m x
  * inter] (ldact); h: bf16 [m x 2 inter] (ldh) = [g | u] for the backward pass, or
- * NULL. Sums and SwiGLU in fp32, each output rounded once (act is not formed from
- * the rounded h); an exp(-g) of 2^128 or more counts as infinite. A row's results
+ * NULL. Sums as fp8_gemm_scaled's (fp32 accumulators of the FP8 matrix instructions),
+ * SwiGLU in fp32, each output rounded once (act is not formed from the rounded h); an
+ * exp(-g) of 2^128 or more counts as infinite. A row's results
  * do not depend on the other rows' values; the same call gives the same bits.
  * k % 16 == 0 (k = 0: zeros); a, b 16-byte aligned with lda, ldb multiples of 16;
  * act, h 2-byte aligned, at full speed where they are 16-byte aligned and ldact,
